@@ -3,8 +3,9 @@
 Four operators, each through the package's entry points where ``own`` is true
 and as elementary torch operations where it is not:
 
-* ``quantize``: a matrix to 8-bit floating point with a power-of-two scale
-  for each block of 128 (``shampoo_quantize_f8``);
+* ``quantize``: a matrix (or its transpose, or both in one call) to 8-bit
+  floating point with a power-of-two scale for each block of 128
+  (``shampoo_quantize_f8``);
 * ``product``: C = A B^T of two such matrices (``shampoo_matmul_f8``);
 * ``linear``: a linear layer's forward and both gradients on those two;
 * ``xent``: softmax cross entropy of hidden @ weight^T against target rows,
@@ -257,19 +258,20 @@ def run(state):
         return plain_product(a, sa, b, sb, state["c"].dtype)
     if c["op"] == "linear":
         x, w, dy = state["x"], state["w"], state["dy"]
-        quantize = mir.shampoo_quantize_f8 if own else plain_quantize
-        xq, wq, dyq = quantize(x, "e4m3", 1, False), quantize(w, "e4m3", 128, False), quantize(dy, "e5m2", 1, False)
-        xt, wt, dyt = quantize(x, "e4m3", 1, True), quantize(w, "e4m3", 128, True), quantize(dy, "e5m2", 1, True)
         if own:
+            xq, xt = mir.shampoo_quantize_f8(x, fmt="e4m3", block_rows=1, transpose="both")
+            wq, wt = mir.shampoo_quantize_f8(w, fmt="e4m3", block_rows=128, transpose="both")
+            dyq, dyt = mir.shampoo_quantize_f8(dy, fmt="e5m2", block_rows=1, transpose="both")
             return (mir.shampoo_matmul_f8(*xq, *wq, state["y"]), mir.shampoo_matmul_f8(*dyq, *wt, state["dx"]),
                     mir.shampoo_matmul_f8(*dyt, *xt, state["dw"]))
+        quantize = plain_quantize
+        xq, wq, dyq = quantize(x, "e4m3", 1, False), quantize(w, "e4m3", 128, False), quantize(dy, "e5m2", 1, False)
+        xt, wt, dyt = quantize(x, "e4m3", 1, True), quantize(w, "e4m3", 128, True), quantize(dy, "e5m2", 1, True)
         return (plain_product(*xq, *wq, x.dtype), plain_product(*dyq, *wt, x.dtype), plain_product(*dyt, *xt, w.dtype))
     if own:
         loss = mir.shampoo_linear_xent(state["hidden"], state["weight"], state["targets"], reduction=c["reduction"],
                                        row_scale=state.get("row_scale"), dhidden=state.get("dhidden"),
                                        dweight=state.get("dweight"))
-        if c["reduction"] == "none" and c["grads"]:
-            return loss, state["dhidden"], state["dweight"]
         return (loss, state["dhidden"], state["dweight"]) if c["grads"] else loss
     got = plain_xent(state["hidden"], state["weight"], state["targets"], c["reduction"], state.get("row_scale"), c["grads"])
     return got if c["grads"] else got[0]
