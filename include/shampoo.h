@@ -53,7 +53,9 @@ typedef enum shampoo_dtype {
   SHAMPOO_F32 = 0,
   SHAMPOO_F16 = 1,
   SHAMPOO_BF16 = 2,
-  SHAMPOO_F64 = 3
+  SHAMPOO_F64 = 3,
+  SHAMPOO_E4M3 = 4, /* 8-bit floating point, 4 exponent and 3 mantissa bits, largest 448, no infinity */
+  SHAMPOO_E5M2 = 5  /* 8-bit floating point, 5 exponent and 2 mantissa bits, largest 57344 */
 } shampoo_dtype;
 
 /* Inverse-root solvers.  [NOTES] "Roots on idle CPUs, partial preconditioners
@@ -446,6 +448,97 @@ shampoo_status shampoo_timing_read(float* ms, int32_t capacity, int32_t* count);
  * Errors: E_UNSUPPORTED for another dtype, E_INVALID for null pointers,
  * E_HIP for launch/event failures. */
 shampoo_status shampoo_mfma_peak(shampoo_dtype dt, void* sink_dev, hipStream_t stream, double* tflops);
+
+/* ---------------------------------------------------------------------------
+ * 8-bit block-scaled products.
+ *
+ * A quantised matrix [n, rows, cols] is held as
+ *   q: uint8 [n, rows, Kp], Kp = cols rounded up to 128, zeros behind cols;
+ *   s: uint8 [n, ceil(rows / block_rows), Ks], Ks = Kp / 128 rounded up to 4:
+ *      byte e + 127 of the block's scale 2^e (127 behind Kp / 128).
+ * A block is 128 columns of one row (block_rows 1) or of 128 rows (128).
+ * q holds x 2^-e rounded to nearest even, 2^e the least power of two that
+ * keeps the block's largest finite magnitude within the format (e = 0 for an
+ * all-zero block, e >= -127).  NaN stays NaN; an infinity stays one in E5M2
+ * and becomes NaN in E4M3.  Both are exact apart from that one rounding.
+ * ------------------------------------------------------------------------- */
+
+/* Quantise x (F32, F16 or BF16; rows ld elements apart, matrices `stride`
+ * apart) and/or its transpose.  q, s: the matrix; qt, st: the transpose
+ * [n, cols, Rp] with blocks along the rows (block_rows then counts columns
+ * of x); either pair may be null.  fmt: SHAMPOO_E4M3 or SHAMPOO_E5M2.
+ * q, qt: 16-byte aligned; s, st: 4-byte aligned.  n at most 65535; rows and
+ * cols at most 2^23 - 128.  Empty matrices return at once. */
+shampoo_status shampoo_quantize_f8(const void* x, shampoo_dtype x_dt, int64_t n, int64_t rows, int64_t cols,
+                                   int64_t ld, int64_t stride, shampoo_dtype fmt, int32_t block_rows,
+                                   void* q, void* s, void* qt, void* st, hipStream_t stream);
+
+/* C = A B^T of quantised stacks: a [n, M, K], b [n, N, K], K a positive
+ * multiple of 128 (the padded width), scales as above with a_block_rows /
+ * b_block_rows 1 or 128; formats in any mix.  c: [n, M, N] contiguous in c_dt
+ * (F32, F16 or BF16).  The scales are applied exactly; sums run in float32 and
+ * are rounded once to c_dt.  ws: shampoo_matmul_f8_workspace bytes (0 for
+ * most shapes: float32 partial results where few outputs share a long K).
+ * Results do not depend on the stream, the workspace's contents or the run. */
+shampoo_status shampoo_matmul_f8_workspace(int64_t n, int64_t M, int64_t N, int64_t K, size_t* bytes);
+shampoo_status shampoo_matmul_f8(const void* a, shampoo_dtype a_dt, const void* a_scale, int32_t a_block_rows,
+                                 const void* b, shampoo_dtype b_dt, const void* b_scale, int32_t b_block_rows,
+                                 int64_t n, int64_t M, int64_t N, int64_t K, void* c, shampoo_dtype c_dt,
+                                 void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Softmax cross entropy of a projection, with its gradients.
+ *
+ * z = hidden weight^T (hidden [N, d], weight [V, d]), and for row i with
+ * target t_i:  loss_i = scale row_scale_i (log sum_v exp z_iv - z_it).  Rows
+ * with t_i == ignore_index have loss 0 and gradient 0.  MEAN divides by the
+ * number of kept rows (0 if there are none).  Gradients, of the reduced loss
+ * (of the sum for NONE):  P_iv = g_i (softmax(z_i)_v - [v = t_i]),
+ * dhidden = P weight,  dweight = P^T hidden.
+ * Any other target outside [0, V) makes its row's loss and gradients NaN.
+ * ------------------------------------------------------------------------- */
+typedef enum shampoo_reduction {
+  SHAMPOO_REDUCE_NONE = 0, /* loss: float32 [N] */
+  SHAMPOO_REDUCE_SUM = 1,  /* loss: float32 [1] */
+  SHAMPOO_REDUCE_MEAN = 2
+} shampoo_reduction;
+
+/* dt: F32 or BF16, the type of hidden, weight and dhidden; ld_*: elements
+ * between rows.  Products run on that type's matrix cores and sum in float32;
+ * for BF16 the softmax enters the gradients' products rounded to bfloat16.
+ * dhidden, dweight: null for no gradient.  dweight_dt: BF16 or F32
+ * (F32 only for dt F32); accumulate: dweight += instead of =.
+ * lse: float32 [N], the rows' log sum exp, or null.
+ * row_scale: float32 [N] or null (all ones).
+ * Logits are never kept: the vocabulary is walked in pieces of 128 columns
+ * that leave a maximum and a sum each.  For gradients the rows are taken
+ * panel_rows at a time (0: as many as keep the panel of exponentials within
+ * 2 GiB), with the panel in the workspace. */
+typedef struct shampoo_xent_args {
+  const void* hidden;
+  const void* weight;
+  const int64_t* targets;
+  const float* row_scale;
+  float* loss;
+  float* lse;
+  void* dhidden;
+  void* dweight;
+  int64_t ld_hidden, ld_weight, ld_dhidden, ld_dweight;
+  int64_t N, V, d;
+  int64_t ignore_index;
+  int64_t panel_rows;
+  shampoo_dtype dt;
+  shampoo_dtype dweight_dt;
+  int32_t reduction;
+  int32_t accumulate;
+  float scale;
+  void* ws;
+  size_t ws_bytes;
+} shampoo_xent_args;
+
+/* Workspace bytes for these arguments (ws fields ignored). */
+shampoo_status shampoo_linear_xent_workspace(const shampoo_xent_args* args, size_t* bytes);
+shampoo_status shampoo_linear_xent(const shampoo_xent_args* args, hipStream_t stream);
 
 #ifdef __cplusplus
 }

@@ -23,13 +23,15 @@ LIB_PATH = os.path.join(_PKG, "libshampoo.so")
 # ---------------------------------------------------------------------------
 OK, E_INVALID, E_UNSUPPORTED, E_WORKSPACE, E_HIP, E_NONFINITE = range(6)
 STATUS_NAMES = {0: "OK", 1: "E_INVALID", 2: "E_UNSUPPORTED", 3: "E_WORKSPACE", 4: "E_HIP", 5: "E_NONFINITE"}
-F32, F16, BF16, F64 = 0, 1, 2, 3
+F32, F16, BF16, F64, E4M3, E5M2 = 0, 1, 2, 3, 4, 5
 CN, NDB, CHEBYSHEV = 0, 1, 2
 SCALE_FROBENIUS, SCALE_POWER = 0, 1
 CHEB_CLENSHAW, CHEB_PS = 0, 1
 GRAFT_SGD, GRAFT_MOMENTUM, GRAFT_ADAM, GRAFT_NONE = 0, 1, 2, 3
 FLAG_NONFINITE, FLAG_ZERO_SCALE, FLAG_PI_FALLBACK, FLAG_RECOMPUTED_F64, FLAG_KEPT_PREVIOUS = 1, 2, 4, 8, 16
 FLAG_RESIDUAL = 32
+REDUCTIONS = {"none": 0, "sum": 1, "mean": 2}
+FORMATS_F8 = {"e4m3": E4M3, "e5m2": E5M2}
 FALLBACKS = {"none": 0, "keep": 1, "f64": 2}
 
 METHODS = {"cn": CN, "ndb": NDB, "chebyshev": CHEBYSHEV}
@@ -89,13 +91,27 @@ class StepArgsC(ctypes.Structure):
                 ("precond_dt", ctypes.c_int32)]
 
 
+class XentArgsC(ctypes.Structure):
+    _fields_ = [("hidden", ctypes.c_void_p), ("weight", ctypes.c_void_p), ("targets", ctypes.c_void_p),
+                ("row_scale", ctypes.c_void_p), ("loss", ctypes.c_void_p), ("lse", ctypes.c_void_p),
+                ("dhidden", ctypes.c_void_p), ("dweight", ctypes.c_void_p),
+                ("ld_hidden", ctypes.c_int64), ("ld_weight", ctypes.c_int64),
+                ("ld_dhidden", ctypes.c_int64), ("ld_dweight", ctypes.c_int64),
+                ("N", ctypes.c_int64), ("V", ctypes.c_int64), ("d", ctypes.c_int64),
+                ("ignore_index", ctypes.c_int64), ("panel_rows", ctypes.c_int64),
+                ("dt", ctypes.c_int32), ("dweight_dt", ctypes.c_int32), ("reduction", ctypes.c_int32),
+                ("accumulate", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("ws", ctypes.c_void_p), ("ws_bytes", ctypes.c_size_t)]
+
+
 EXPORTS = [
     "shampoo_version", "shampoo_last_error", "shampoo_plan_blocks", "shampoo_pack_blocks",
     "shampoo_unpack_blocks", "shampoo_update_stats", "shampoo_inverse_root_workspace",
     "shampoo_inverse_root", "shampoo_inverse_root_noalloc", "shampoo_precondition_workspace",
     "shampoo_precondition",
     "shampoo_step_workspace", "shampoo_step", "shampoo_check_flags", "shampoo_timing_enable",
-    "shampoo_timing_read", "shampoo_mfma_peak",
+    "shampoo_timing_read", "shampoo_mfma_peak", "shampoo_quantize_f8", "shampoo_matmul_f8_workspace",
+    "shampoo_matmul_f8", "shampoo_linear_xent_workspace", "shampoo_linear_xent",
 ]
 
 
@@ -131,6 +147,13 @@ def _load():
         "shampoo_timing_enable": ([i32], ctypes.c_int),
         "shampoo_timing_read": ([vp, i32, P(i32)], ctypes.c_int),
         "shampoo_mfma_peak": ([ctypes.c_int, vp, vp, P(ctypes.c_double)], ctypes.c_int),
+        "shampoo_quantize_f8": ([vp, ctypes.c_int, i64, i64, i64, i64, i64, ctypes.c_int, i32, vp, vp, vp, vp, vp],
+                                ctypes.c_int),
+        "shampoo_matmul_f8_workspace": ([i64, i64, i64, i64, P(sz)], ctypes.c_int),
+        "shampoo_matmul_f8": ([vp, ctypes.c_int, vp, i32, vp, ctypes.c_int, vp, i32, i64, i64, i64, i64, vp,
+                               ctypes.c_int, vp, sz, vp], ctypes.c_int),
+        "shampoo_linear_xent_workspace": ([P(XentArgsC), P(sz)], ctypes.c_int),
+        "shampoo_linear_xent": ([P(XentArgsC), vp], ctypes.c_int),
     }
     for name in EXPORTS:
         f = getattr(lib, name)
@@ -372,6 +395,226 @@ def shampoo_mfma_peak(dtype, stream=None):
     _check(lib.shampoo_mfma_peak(DTYPES[dtype], ctypes.c_void_p(sink.data_ptr()), _stream(stream),
                                  ctypes.byref(out)))
     return out.value
+
+
+# ---------------------------------------------------------------------------
+# 8-bit block-scaled products
+# ---------------------------------------------------------------------------
+def _on_device(*tensors):
+    """The common device of these tensors; ValueError unless they are device tensors of one device."""
+    dev = None
+    for t in tensors:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError("expected device tensors")
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise ValueError("tensors are on different devices")
+    return dev
+
+
+def _up(x, m):
+    return -(-x // m) * m
+
+
+def _f8_code(t):
+    torch = _torch()
+    if t.dtype == torch.float8_e4m3fn:
+        return E4M3
+    if t.dtype == torch.float8_e5m2:
+        return E5M2
+    raise TypeError("expected a float8_e4m3fn or float8_e5m2 tensor, got %s" % t.dtype)
+
+
+def shampoo_quantize_f8(x, fmt="e4m3", block_rows=1, transpose=False, out=None, stream=None):
+    """x [rows, cols] or [n, rows, cols] (float32, float16 or bfloat16, unit
+    column stride) as 8-bit floating point with a power-of-two scale for each
+    block of 128 columns of ``block_rows`` (1 or 128) rows.
+
+    Returns (q, scale): q float8 [.., rows, cols rounded up to 128], zeros
+    behind the columns; scale float8_e8m0fnu [.., ceil(rows / block_rows),
+    blocks rounded up to 4], ones behind the blocks.  transpose=True
+    quantises the transpose (blocks along x's rows) instead, "both" returns
+    ((q, scale), (q_t, scale_t)) from one reading of x.  ``out``: tensors to
+    write to, as returned."""
+    torch = _torch()
+    if fmt not in FORMATS_F8:
+        raise ValueError("fmt must be one of %s" % sorted(FORMATS_F8))
+    if block_rows not in (1, 128):
+        raise ValueError("block_rows must be 1 or 128")
+    if transpose not in (False, True, "both"):
+        raise ValueError("transpose must be False, True or 'both'")
+    if x.dim() not in (2, 3):
+        raise ValueError("x must have 2 or 3 dimensions")
+    if x.dtype not in (torch.float32, torch.float16, torch.bfloat16):
+        raise TypeError("unsupported dtype %s" % x.dtype)
+    dev = _on_device(x)
+    if x.numel() and x.shape[-1] > 1 and x.stride(-1) != 1:
+        raise ValueError("x must have unit column stride")
+    n = x.shape[0] if x.dim() == 3 else 1
+    rows, cols = x.shape[-2], x.shape[-1]
+    ld = x.stride(-2) if rows > 1 else cols
+    if x.numel() and (ld < cols or (n > 1 and x.dim() == 3 and x.stride(0) < 0)):
+        raise ValueError("x must not overlap itself (row stride %d, %d columns)" % (ld, cols))
+    kind = torch.float8_e4m3fn if fmt == "e4m3" else torch.float8_e5m2
+
+    def pair(r, k, given):
+        K = _up(k, 128)
+        shapes = ((n, r, K), (n, -(-r // block_rows), _up(K // 128, 4)))
+        if x.dim() == 2:
+            shapes = tuple(s[1:] for s in shapes)
+        kinds = (kind, torch.float8_e8m0fnu)
+        if given is None:
+            return tuple(torch.empty(s, dtype=d, device=dev) for s, d in zip(shapes, kinds))
+        for t, s, d in zip(given, shapes, kinds):
+            _dev(t, "out")
+            if tuple(t.shape) != s or t.dtype != d or t.device != dev:
+                raise ValueError("out must be a %s tensor of shape %s on %s" % (d, s, dev))
+        return tuple(given)
+
+    both = transpose == "both"
+    plain = pair(rows, cols, (out[0] if both else out) if out is not None else None) if transpose is not True else None
+    turned = pair(cols, rows, (out[1] if both else out) if out is not None else None) if transpose else None
+    q, s = plain if plain is not None else (None, None)
+    qt, st = turned if turned is not None else (None, None)
+    with torch.cuda.device(dev):
+        _check(lib.shampoo_quantize_f8(_ptr(x), _dtype_code(x), n, rows, cols, ld, x.stride(0) if x.dim() == 3 else 0,
+                                       FORMATS_F8[fmt], int(block_rows), _ptr(q), _ptr(s), _ptr(qt), _ptr(st),
+                                       _stream(stream)))
+    return (plain, turned) if both else turned if transpose else plain
+
+
+def shampoo_matmul_f8_workspace(n, M, N, K):
+    b = ctypes.c_size_t(0)
+    _check(lib.shampoo_matmul_f8_workspace(int(n), int(M), int(N), int(K), ctypes.byref(b)))
+    return b.value
+
+
+def shampoo_matmul_f8(a, a_scale, b, b_scale, c, ws=None, stream=None):
+    """c = a b^T of quantised matrices (as ``shampoo_quantize_f8`` returns
+    them): a [M, K] or [n, M, K], b [N, K] or [n, N, K] in any mix of the two
+    formats, c [M, N] or [n, M, N] float32, float16 or bfloat16.  A linear
+    layer y = x W^T and its gradients dx = dy W, dW = dy^T x are three of
+    these, on the operands quantised along each product's own inner side."""
+    torch = _torch()
+    dev = _on_device(a, a_scale, b, b_scale, c, ws)
+    for t, nm in ((a, "a"), (a_scale, "a_scale"), (b, "b"), (b_scale, "b_scale"), (c, "c")):
+        _dev(t, nm)
+    if not (a.dim() == b.dim() == c.dim() == a_scale.dim() == b_scale.dim()) or a.dim() not in (2, 3):
+        raise ValueError("a, b, c and the scales must all have 2, or all 3, dimensions")
+    if c.dtype not in (torch.float32, torch.float16, torch.bfloat16):
+        raise TypeError("unsupported result dtype %s" % c.dtype)
+    n = a.shape[0] if a.dim() == 3 else 1
+    M, K, N = a.shape[-2], a.shape[-1], b.shape[-2]
+    if b.shape[-1] != K or (a.dim() == 3 and b.shape[0] != n) or tuple(c.shape) != tuple(a.shape[:-2]) + (M, N):
+        raise ValueError("shapes do not match: a %s, b %s, c %s" % (tuple(a.shape), tuple(b.shape), tuple(c.shape)))
+
+    def block_rows(t, s, rows):
+        if s.dtype not in (torch.float8_e8m0fnu, torch.uint8):
+            raise TypeError("scales must be float8_e8m0fnu")
+        for rb in (1, 128):
+            if tuple(s.shape) == tuple(t.shape[:-2]) + (-(-rows // rb), _up(K // 128, 4)):
+                return rb
+        raise ValueError("scales of shape %s do not fit %s" % (tuple(s.shape), tuple(t.shape)))
+
+    arb, brb = block_rows(a, a_scale, M), block_rows(b, b_scale, N)
+    if ws is None:
+        nb = shampoo_matmul_f8_workspace(n, M, N, K)
+        ws = torch.empty(nb, dtype=torch.uint8, device=dev) if nb else None
+    with torch.cuda.device(dev):
+        _check(lib.shampoo_matmul_f8(_ptr(a), _f8_code(a), _ptr(a_scale), arb, _ptr(b), _f8_code(b), _ptr(b_scale), brb,
+                                     n, M, N, K, _ptr(c), _dtype_code(c), _ptr(ws),
+                                     0 if ws is None else ws.numel() * ws.element_size(), _stream(stream)))
+    return c
+
+
+# ---------------------------------------------------------------------------
+# softmax cross entropy of a projection
+# ---------------------------------------------------------------------------
+def _rows2d(t, name, shape, dtypes):
+    if t is None:
+        return 0
+    if tuple(t.shape) != shape or t.dtype not in dtypes:
+        raise ValueError("%s must be a %s tensor of shape %s, got %s %s" % (
+            name, " or ".join(str(d) for d in dtypes), shape, t.dtype, tuple(t.shape)))
+    if t.numel() and shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError("%s must have unit column stride" % name)
+    ld = t.stride(0) if shape[0] > 1 else shape[1]
+    if t.numel() and ld < shape[1]:
+        raise ValueError("%s must not overlap itself" % name)
+    return ld
+
+
+def _xent_args(hidden, weight, targets, loss, lse, dhidden, dweight, row_scale, ignore_index, reduction, scale, accumulate,
+               panel_rows):
+    torch = _torch()
+    if reduction not in REDUCTIONS:
+        raise ValueError("reduction must be one of %s" % sorted(REDUCTIONS))
+    if hidden.dim() != 2 or weight.dim() != 2:
+        raise ValueError("hidden and weight must have 2 dimensions")
+    N, d = hidden.shape
+    V = weight.shape[0]
+    if hidden.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError("unsupported dtype %s (float32, bfloat16)" % hidden.dtype)
+    ldh = _rows2d(hidden, "hidden", (N, d), (hidden.dtype,))
+    ldw = _rows2d(weight, "weight", (V, d), (hidden.dtype,))
+    lddh = _rows2d(dhidden, "dhidden", (N, d), (hidden.dtype,))
+    lddw = _rows2d(dweight, "dweight", (V, d), (hidden.dtype, torch.float32))
+    for t, name, dtype in ((targets, "targets", torch.int64), (row_scale, "row_scale", torch.float32),
+                           (lse, "lse", torch.float32)):
+        if t is not None and (t.dtype != dtype or tuple(t.shape) != (N,) or not t.is_contiguous()):
+            raise ValueError("%s must be a contiguous %s tensor of shape (%d,)" % (name, dtype, N))
+    shape = (N,) if reduction == "none" else ()
+    if loss is not None and (loss.dtype != torch.float32 or tuple(loss.shape) != shape or not loss.is_contiguous()):
+        raise ValueError("loss must be a contiguous float32 tensor of shape %s" % (shape,))
+
+    def at(t):
+        return None if t is None else t.data_ptr()
+
+    return XentArgsC(at(hidden), at(weight), at(targets), at(row_scale), at(loss), at(lse), at(dhidden), at(dweight),
+                     max(ldh, d), max(ldw, d), max(lddh, d), max(lddw, d), N, V, d, int(ignore_index), int(panel_rows),
+                     _dtype_code(hidden), _dtype_code(dweight) if dweight is not None else _dtype_code(hidden),
+                     REDUCTIONS[reduction], 1 if accumulate else 0, float(scale), None, 0)
+
+
+def shampoo_linear_xent_workspace(hidden, weight, targets, dhidden=None, dweight=None, panel_rows=0):
+    """Workspace bytes of ``shampoo_linear_xent`` with these tensors."""
+    b = ctypes.c_size_t(0)
+    args = _xent_args(hidden, weight, targets, None, None, dhidden, dweight, None, -100, "mean", 1.0, False, panel_rows)
+    _check(lib.shampoo_linear_xent_workspace(ctypes.byref(args), ctypes.byref(b)))
+    return b.value
+
+
+def shampoo_linear_xent(hidden, weight, targets, loss=None, lse=None, dhidden=None, dweight=None, row_scale=None,
+                        ignore_index=-100, reduction="mean", scale=1.0, accumulate=False, panel_rows=0, ws=None,
+                        stream=None):
+    """Softmax cross entropy of the projection hidden weight^T against
+    ``targets``, without keeping its logits; returns the loss.
+
+    hidden [N, d] and weight [V, d] (float32 or bfloat16, unit column
+    stride), targets int64 [N]; rows with target ``ignore_index`` count for
+    nothing.  reduction: "mean" over the other rows, "sum" or "none".
+    row_scale float32 [N] and scale multiply each row's loss.  dhidden, dweight:
+    tensors that receive the gradients of the (summed) loss; dweight may be
+    float32 beside bfloat16 inputs, and accumulate=True adds to it.  lse:
+    receives log sum exp of each row.  panel_rows bounds the rows whose
+    exponentials the workspace holds at a time (0: up to 2 GiB of them)."""
+    torch = _torch()
+    dev = _on_device(hidden, weight, targets, loss, lse, dhidden, dweight, row_scale, ws)
+    if loss is None:
+        loss = torch.empty((hidden.shape[0],) if reduction == "none" else (), dtype=torch.float32, device=dev)
+    args = _xent_args(hidden, weight, targets, loss, lse, dhidden, dweight, row_scale, ignore_index, reduction, scale,
+                      accumulate, panel_rows)
+    if ws is None:
+        b = ctypes.c_size_t(0)
+        _check(lib.shampoo_linear_xent_workspace(ctypes.byref(args), ctypes.byref(b)))
+        ws = torch.empty(max(b.value, 1), dtype=torch.uint8, device=dev)
+    args.ws, args.ws_bytes = ws.data_ptr(), ws.numel() * ws.element_size()
+    with torch.cuda.device(dev):
+        _check(lib.shampoo_linear_xent(ctypes.byref(args), _stream(stream)))
+    return loss
 
 
 from .optimizer import Shampoo, ShampooStack  # noqa: E402  (needs the binding above)

@@ -8,13 +8,16 @@ the package would load the library before it is rebuilt), or
 import os
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 LIB = os.path.join(PKG, "libshampoo.so")
-SOURCES = [os.path.join(PKG, "csrc", "shampoo.hip")]
+SOURCES = [os.path.join(PKG, "csrc", f) for f in ("shampoo.hip", "products.hip")]
 HEADERS = [os.path.join(PKG, "csrc", f) for f in ("gemm_common.hpp", "gemm.hpp", "gemm_hsym.hpp", "gemm_nn256.hpp",
-                                                  "kernels.hpp")] + [
+                                                  "kernels.hpp", "host_common.hpp", "product_core.hpp",
+                                                  "f8_kernels.hpp", "xent_kernels.hpp", "products.hpp")] + [
     os.path.join(ROOT, "include", "shampoo.h")]
 
 FLAGS = [
@@ -22,7 +25,6 @@ FLAGS = [
     "-O3",
     "-std=c++17",
     "-fPIC",
-    "-shared",
     # packed FP32 instructions are kept out of every kernel
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
     "-Wno-pass-failed",
@@ -39,16 +41,24 @@ def hipcc():
 def build(verbose=False):
     """Compile libshampoo.so (always recompiles)."""
     tmp = LIB + ".tmp"
-    cmd = [hipcc()] + FLAGS + ["-I", os.path.join(ROOT, "include"), "-o", tmp] + SOURCES
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    res = subprocess.run(cmd, capture_output=True, text=True)
     noise = "is not a recognized feature for this target"
-    err = "\n".join(l for l in res.stderr.splitlines() if noise not in l)
-    if res.returncode != 0:
-        raise RuntimeError("hipcc failed (%d):\n%s" % (res.returncode, err))
-    if verbose and err.strip():
-        print(err, file=sys.stderr)
+
+    def run(cmd):
+        if verbose:
+            print(" ".join(cmd), flush=True)
+        res = subprocess.run(cmd, capture_output=True, text=True)
+        err = "\n".join(l for l in res.stderr.splitlines() if noise not in l)
+        if res.returncode != 0:
+            raise RuntimeError("hipcc failed (%d):\n%s" % (res.returncode, err))
+        if verbose and err.strip():
+            print(err, file=sys.stderr)
+
+    with tempfile.TemporaryDirectory() as objdir:
+        objects = [os.path.join(objdir, os.path.basename(s) + ".o") for s in SOURCES]
+        base = [hipcc()] + FLAGS + ["-I", os.path.join(ROOT, "include")]
+        with ThreadPoolExecutor(len(SOURCES)) as pool:  # one compiler per source
+            list(pool.map(lambda so: run(base + ["-c", so[0], "-o", so[1]]), zip(SOURCES, objects)))
+        run([hipcc(), "--offload-arch=gfx950", "-fPIC", "-shared", "-o", tmp] + objects)
     os.replace(tmp, LIB)
     return LIB
 

@@ -1,0 +1,462 @@
+// 8-bit block-scaled products and the projection's softmax cross entropy
+// (see include/shampoo.h): argument checks, workspace carving, launches.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+#include <type_traits>
+
+#include "f8_kernels.hpp"
+#include "host_common.hpp"
+#include "product_core.hpp"
+#include "products.hpp"
+#include "shampoo.h"
+#include "xent_kernels.hpp"
+
+using namespace shampoo;
+
+namespace {
+
+inline int64_t up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
+inline bool aligned(const void* p, size_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
+inline size_t size_of(int dt) { return dt == SHAMPOO_F32 ? 4 : dt == SHAMPOO_E4M3 || dt == SHAMPOO_E5M2 ? 1 : 2; }
+
+// ---------------------------------------------------------------------------
+// products
+// ---------------------------------------------------------------------------
+// Tile of a product and its split of k.  LARGE: 256 x 256, one workgroup of
+// 8 waves per CU; SMALL: 128 x 128, two workgroups of 4 waves.
+struct Shape {
+  bool large;
+  int splits, split_stages, nst;
+};
+
+constexpr int CUS = 256;  // planning only; the grid follows the device
+
+Shape plan_shape(int64_t batch, int64_t M, int64_t N, int64_t K, int es, bool may_split) {
+  Shape s;
+  const int64_t stages = (K * es + 63) / 64;
+  s.nst = (int)up(stages, 2);
+  const int64_t tl = batch * ((M + 255) / 256) * ((N + 255) / 256);
+  const int64_t ts = batch * ((M + 127) / 128) * ((N + 127) / 128);
+  // rounds of the chip, a small round being half the work at 70% of the rate
+  const double large_cost = (double)((tl + CUS - 1) / CUS);
+  const double small_cost = (double)((ts + 2 * CUS - 1) / (2 * CUS)) * 0.5 / 0.7;
+  s.large = large_cost <= small_cost;
+  s.splits = 1;
+  s.split_stages = s.nst;
+  const int64_t items = s.large ? tl : ts, slots = s.large ? CUS : 2 * CUS;
+  if (may_split && items * 2 <= slots) {
+    // at least 16 stages a range
+    const int64_t want = std::min<int64_t>(slots / items, s.nst / 16);
+    if (want >= 2) {
+      s.split_stages = (int)up((s.nst + want - 1) / want, 8);
+      s.splits = (s.nst + s.split_stages - 1) / s.split_stages;
+    }
+  }
+  return s;
+}
+
+template <Elem E, int FM, int FN, int WM, int WN, int NS, int PER_CU, bool AS, bool BS, Epi EPI, int FA, int FB>
+hipError_t launch_tiles(ProductArgs g, int64_t batch, hipStream_t st) {
+  constexpr int TM = 32 * FM * WM, TN = 32 * FN * WN, LDS = NS * (TM + TN) * 64;
+  const auto kernel = product_kernel<E, FM, FN, WM, WN, NS, AS, BS, EPI, FA, FB>;
+  static bool ready[MAX_DEVICES] = {false};
+  int dev = 0, cus = 0;
+  HIP_TRY_ERR(hipGetDevice(&dev));
+  if (!(dev >= 0 && dev < MAX_DEVICES && ready[dev])) {
+    HIP_TRY_ERR(hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, LDS));
+    if (dev >= 0 && dev < MAX_DEVICES) ready[dev] = true;
+  }
+  HIP_TRY_ERR(cu_count(&cus));
+  g.mt = (g.M + TM - 1) / TM;
+  g.nt = (g.N + TN - 1) / TN;
+  g.items = batch * g.splits * (int64_t)g.mt * g.nt;
+  const int64_t grid = std::min<int64_t>(up(g.items, 8), std::max(8, cus * PER_CU / 8 * 8));
+  hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(64 * WM * WN), LDS, st, g);
+  return hipGetLastError();
+}
+
+template <Elem E, bool AS, bool BS, Epi EPI, int FA = 0, int FB = 0>
+hipError_t launch_product(const ProductArgs& g, bool large, int64_t batch, hipStream_t st) {
+  if (large) return launch_tiles<E, 2, 4, 4, 2, 4, 1, AS, BS, EPI, FA, FB>(g, batch, st);
+  return launch_tiles<E, 1, 4, 4, 1, 4, 2, AS, BS, EPI, FA, FB>(g, batch, st);
+}
+
+void set_shape(ProductArgs& g, const Shape& s) {
+  g.nst = s.nst;
+  g.splits = s.splits;
+  g.split_stages = s.split_stages;
+}
+
+size_t partial_bytes(const Shape& s, int64_t batch, int64_t M, int64_t N) {
+  return s.splits > 1 ? align_up((size_t)s.splits * batch * M * N * 4) : 0;
+}
+
+// Points a split product at its partial results; finish_split sums them.
+struct Out {
+  void* C;
+  int64_t ldc, strideC;
+  int c_dt, vec;
+  float beta;
+};
+void point_output(ProductArgs& g, const Shape& s, const Out& o, float* part, int64_t batch) {
+  if (s.splits > 1) {
+    g.C = part;
+    g.ldc = g.N;
+    g.strideC = (int64_t)g.M * g.N;
+    g.split_stride = batch * g.strideC;
+    g.c_dt = 0;
+    g.vec = g.N % 4 == 0;
+    g.beta = 0.f;
+  } else {
+    g.C = o.C;
+    g.ldc = o.ldc;
+    g.strideC = o.strideC;
+    g.c_dt = o.c_dt;
+    g.vec = o.vec;
+    g.beta = o.beta;
+  }
+}
+hipError_t sum_splits(const float* part, int splits, int64_t split_stride, const Out& o, int64_t batch, int M, int N, hipStream_t st) {
+  const int64_t total = (int64_t)M * N;
+  const int64_t gx = std::max<int64_t>(1, std::min<int64_t>((total + 255) / 256, 8192));
+  hipLaunchKernelGGL(sum_splits_kernel, dim3((unsigned)gx, (unsigned)batch), dim3(256), 0, st, part, splits, split_stride, o.C, o.ldc,
+                     o.strideC, M, N, o.c_dt, o.beta);
+  return hipGetLastError();
+}
+hipError_t finish_split(const ProductArgs& g, const Shape& s, const Out& o, const float* part, int64_t batch, hipStream_t st) {
+  if (s.splits == 1) return hipSuccess;
+  return sum_splits(part, s.splits, g.split_stride, o, batch, g.M, g.N, st);
+}
+
+int out_code(int dt) { return dt == SHAMPOO_F32 ? 0 : dt == SHAMPOO_F16 ? 1 : 2; }
+// rows that allow the epilogue's 16-byte stores
+int rows_vec(const void* C, int64_t ldc, int64_t strideC, int dt) {
+  const int64_t ve = 16 / (int64_t)size_of(dt);
+  return aligned(C, 16) && ldc % ve == 0 && strideC % ve == 0;
+}
+
+constexpr int64_t F8_MAX = (int64_t(1) << 23) - 128;
+
+shampoo_status check_f8_sizes(int64_t n, int64_t M, int64_t N, int64_t K) {
+  if (n < 0 || M < 0 || N < 0) return fail(SHAMPOO_E_INVALID, "negative size");
+  if (K < 128 || K % 128 != 0) return fail(SHAMPOO_E_INVALID, "K = %lld: must be a positive multiple of 128", (long long)K);
+  if (n > 65535 || M > F8_MAX || N > F8_MAX || K > F8_MAX)
+    return fail(SHAMPOO_E_UNSUPPORTED, "product too large (%lld of %lld x %lld x %lld)", (long long)n, (long long)M, (long long)N,
+                (long long)K);
+  if (((M + 127) / 128) * ((N + 127) / 128) > INT32_MAX / 2) return fail(SHAMPOO_E_UNSUPPORTED, "too many tiles");
+  return SHAMPOO_OK;
+}
+
+}  // namespace
+
+namespace shampoo {
+
+shampoo_status quantize_f8_impl(const void* x, int x_dt, int64_t n, int64_t rows, int64_t cols, int64_t ld, int64_t stride, int fmt,
+                                int32_t block_rows, void* q, void* s, void* qt, void* st_, hipStream_t st) {
+  if (n < 0 || rows < 0 || cols < 0) return fail(SHAMPOO_E_INVALID, "negative size");
+  if (x_dt != SHAMPOO_F32 && x_dt != SHAMPOO_F16 && x_dt != SHAMPOO_BF16)
+    return fail(SHAMPOO_E_UNSUPPORTED, "dtype %d to quantise (F32, F16, BF16)", x_dt);
+  if (fmt != SHAMPOO_E4M3 && fmt != SHAMPOO_E5M2) return fail(SHAMPOO_E_UNSUPPORTED, "8-bit format %d (E4M3, E5M2)", fmt);
+  if (block_rows != 1 && block_rows != 128) return fail(SHAMPOO_E_UNSUPPORTED, "block_rows = %d (1, 128)", block_rows);
+  if (n > 65535 || rows > F8_MAX || cols > F8_MAX) return fail(SHAMPOO_E_UNSUPPORTED, "matrix too large to quantise");
+  if (n == 0 || rows == 0 || cols == 0) return SHAMPOO_OK;
+  if ((q == nullptr) != (s == nullptr) || (qt == nullptr) != (st_ == nullptr))
+    return fail(SHAMPOO_E_INVALID, "values and scales are given together");
+  if (!q && !qt) return fail(SHAMPOO_E_INVALID, "no output");
+  if (!x) return fail(SHAMPOO_E_INVALID, "null pointer argument");
+  if (ld < cols || (n > 1 && stride < 0)) return fail(SHAMPOO_E_INVALID, "row stride %lld < %lld columns", (long long)ld, (long long)cols);
+  if (!aligned(q, 16) || !aligned(qt, 16) || !aligned(s, 4) || !aligned(st_, 4) || !aligned(x, size_of(x_dt)))
+    return fail(SHAMPOO_E_INVALID, "misaligned pointer");
+  if ((rows + 127) / 128 > 65535) return fail(SHAMPOO_E_UNSUPPORTED, "matrix too large to quantise");
+  QuantArgs g;
+  g.x = x; g.ld = ld; g.stride = n > 1 ? stride : 0;
+  g.q = (uint8_t*)q; g.s = (uint8_t*)s; g.qt = (uint8_t*)qt; g.st = (uint8_t*)st_;
+  g.rows = (int)rows; g.cols = (int)cols;
+  const dim3 grid((unsigned)((cols + 127) / 128), (unsigned)((rows + 127) / 128), (unsigned)n);
+#define SHAMPOO_QUANT(T, F, R) hipLaunchKernelGGL((quantize_tile_kernel<T, F, R>), grid, dim3(256), 0, st, g)
+#define SHAMPOO_QUANT_T(T)                                                     \
+  do {                                                                         \
+    if (fmt == SHAMPOO_E4M3) {                                                 \
+      if (block_rows == 1) SHAMPOO_QUANT(T, 0, 1); else SHAMPOO_QUANT(T, 0, 128); \
+    } else {                                                                   \
+      if (block_rows == 1) SHAMPOO_QUANT(T, 1, 1); else SHAMPOO_QUANT(T, 1, 128); \
+    }                                                                          \
+  } while (0)
+  if (x_dt == SHAMPOO_F32) SHAMPOO_QUANT_T(float);
+  else if (x_dt == SHAMPOO_F16) SHAMPOO_QUANT_T(_Float16);
+  else SHAMPOO_QUANT_T(uint16_t);
+#undef SHAMPOO_QUANT_T
+#undef SHAMPOO_QUANT
+  LAUNCH_CHECK("quantize_f8");
+  return SHAMPOO_OK;
+}
+
+size_t matmul_f8_bytes(int64_t n, int64_t M, int64_t N, int64_t K) {
+  if (n == 0 || M == 0 || N == 0) return 0;
+  return partial_bytes(plan_shape(n, M, N, K, 1, true), n, M, N);
+}
+
+shampoo_status matmul_f8_impl(const void* a, int a_dt, const void* sa, int32_t arb, const void* b, int b_dt, const void* sb, int32_t brb,
+                              int64_t n, int64_t M, int64_t N, int64_t K, void* c, int c_dt, void* ws, size_t ws_bytes, hipStream_t st) {
+  shampoo_status r = check_f8_sizes(n, M, N, K);
+  if (r != SHAMPOO_OK) return r;
+  for (int dt : {a_dt, b_dt})
+    if (dt != SHAMPOO_E4M3 && dt != SHAMPOO_E5M2) return fail(SHAMPOO_E_UNSUPPORTED, "operand dtype %d (E4M3, E5M2)", dt);
+  if (c_dt != SHAMPOO_F32 && c_dt != SHAMPOO_F16 && c_dt != SHAMPOO_BF16)
+    return fail(SHAMPOO_E_UNSUPPORTED, "result dtype %d (F32, F16, BF16)", c_dt);
+  for (int rb : {arb, brb})
+    if (rb != 1 && rb != 128) return fail(SHAMPOO_E_UNSUPPORTED, "block_rows = %d (1, 128)", rb);
+  if (n == 0 || M == 0 || N == 0) return SHAMPOO_OK;
+  if (!a || !b || !sa || !sb || !c) return fail(SHAMPOO_E_INVALID, "null pointer argument");
+  if (!aligned(a, 16) || !aligned(b, 16) || !aligned(sa, 4) || !aligned(sb, 4) || !aligned(c, size_of(c_dt)))
+    return fail(SHAMPOO_E_INVALID, "misaligned pointer");
+  const Shape s = plan_shape(n, M, N, K, 1, true);
+  const size_t need = partial_bytes(s, n, M, N);
+  if (need && (!ws || ws_bytes < need)) return fail(SHAMPOO_E_WORKSPACE, "workspace %zu bytes < %zu needed", ws ? ws_bytes : 0, need);
+  ProductArgs g{};
+  g.A = a; g.B = b; g.sa = (const uint8_t*)sa; g.sb = (const uint8_t*)sb;
+  g.M = (int)M; g.N = (int)N; g.K = (int)K;
+  g.lda = g.ldb = K;
+  g.strideA = M * K; g.strideB = N * K;
+  g.ldsa = g.ldsb = up(K / 128, 4);
+  g.sa_shift = arb == 128 ? 7 : 0;
+  g.sb_shift = brb == 128 ? 7 : 0;
+  g.strideSa = (arb == 128 ? (M + 127) / 128 : M) * g.ldsa;
+  g.strideSb = (brb == 128 ? (N + 127) / 128 : N) * g.ldsb;
+  set_shape(g, s);
+  const Out o{c, N, M * N, out_code(c_dt), rows_vec(c, N, n > 1 ? M * N : 0, c_dt), 0.f};
+  point_output(g, s, o, (float*)ws, n);
+  const bool a5 = a_dt == SHAMPOO_E5M2, b5 = b_dt == SHAMPOO_E5M2;
+  if (!a5 && !b5) HIP_TRY((launch_product<Elem::F8, false, false, Epi::STORE, 0, 0>(g, s.large, n, st)));
+  else if (a5 && !b5) HIP_TRY((launch_product<Elem::F8, false, false, Epi::STORE, 1, 0>(g, s.large, n, st)));
+  else if (!a5) HIP_TRY((launch_product<Elem::F8, false, false, Epi::STORE, 0, 1>(g, s.large, n, st)));
+  else HIP_TRY((launch_product<Elem::F8, false, false, Epi::STORE, 1, 1>(g, s.large, n, st)));
+  HIP_TRY(finish_split(g, s, o, (const float*)ws, n, st));
+  return SHAMPOO_OK;
+}
+
+}  // namespace shampoo
+
+namespace {
+
+// ---------------------------------------------------------------------------
+// softmax cross entropy
+// ---------------------------------------------------------------------------
+constexpr int64_t XENT_MAX_ROW = int64_t(1) << 21;  // elements: 256 rows stay within 32-bit offsets
+constexpr int64_t XENT_PANEL_BYTES = int64_t(1) << 31;
+constexpr int64_t XENT_STATS_BYTES = int64_t(1) << 28;
+
+struct XentLayout {
+  int64_t panel, pieces, ldE, dp;
+  bool grads, copy_hidden, copy_weight, dw_sum;  // dw_sum: float32 sum of the panels' bfloat16 gradients
+  size_t count, stats, logit, lse, rows, E, hidden, weight, part, dw, total;
+  Shape logits, dx, dwp;
+};
+
+int64_t row_elems(int dt) { return dt == SHAMPOO_F32 ? 4 : 8; }
+
+shampoo_status xent_layout(const shampoo_xent_args* a, XentLayout* L) {
+  if (!a) return fail(SHAMPOO_E_INVALID, "null arguments");
+  if (a->N < 0 || a->V < 1 || a->d < 1) return fail(SHAMPOO_E_INVALID, "N = %lld, V = %lld, d = %lld", (long long)a->N, (long long)a->V, (long long)a->d);
+  if (a->dt != SHAMPOO_F32 && a->dt != SHAMPOO_BF16) return fail(SHAMPOO_E_UNSUPPORTED, "dtype %d (F32, BF16)", (int)a->dt);
+  if (a->dweight && a->dweight_dt != SHAMPOO_F32 && !(a->dweight_dt == SHAMPOO_BF16 && a->dt == SHAMPOO_BF16))
+    return fail(SHAMPOO_E_UNSUPPORTED, "weight gradient dtype %d for dtype %d", (int)a->dweight_dt, (int)a->dt);
+  if (a->reduction < 0 || a->reduction > 2) return fail(SHAMPOO_E_INVALID, "reduction %d", a->reduction);
+  if (a->N > INT32_MAX / 4 || a->V > XENT_MAX_ROW || a->d > XENT_MAX_ROW / 4 || a->ld_hidden > XENT_MAX_ROW || a->ld_weight > XENT_MAX_ROW)
+    return fail(SHAMPOO_E_UNSUPPORTED, "N = %lld, V = %lld, d = %lld too large", (long long)a->N, (long long)a->V, (long long)a->d);
+  if (a->panel_rows < 0) return fail(SHAMPOO_E_INVALID, "panel_rows < 0");
+  const int64_t es = a->dt == SHAMPOO_F32 ? 4 : 2, ve = row_elems(a->dt);
+  L->grads = a->dhidden || a->dweight;
+  L->pieces = (a->V + 127) / 128;
+  L->ldE = L->pieces * 128;
+  int64_t rows = a->panel_rows;
+  if (rows == 0) {
+    rows = XENT_STATS_BYTES / (L->pieces * 8);
+    if (L->grads) rows = std::min(rows, XENT_PANEL_BYTES / (L->ldE * es));
+    rows = std::max<int64_t>(rows / 256 * 256, 256);
+  }
+  rows = std::min<int64_t>(rows, 131072);
+  L->panel = std::max<int64_t>(std::min(rows, a->N), 1);
+  // the products read 16-byte runs of rows: others are copied into rows that
+  // start on 16 bytes
+  L->dp = up(a->d, ve);
+  L->copy_hidden = a->d % ve || a->ld_hidden % ve || !aligned(a->hidden, 16);
+  L->copy_weight = a->d % ve || a->ld_weight % ve || !aligned(a->weight, 16);
+  L->dw_sum = a->dweight && a->dweight_dt == SHAMPOO_BF16 && L->panel < a->N;
+  L->logits = plan_shape(1, L->panel, a->V, a->d, (int)es, false);
+  L->dx = plan_shape(1, L->panel, a->d, a->V, (int)es, true);
+  L->dwp = plan_shape(1, a->V, a->d, L->panel, (int)es, true);
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t p = at;
+    at += align_up(bytes);
+    return p;
+  };
+  L->count = take(4);
+  L->stats = take((size_t)L->pieces * L->panel * 8);
+  L->logit = take((size_t)L->panel * 4);
+  L->lse = take((size_t)L->panel * 4);
+  L->rows = take((size_t)std::max<int64_t>(a->N, 1) * 4);
+  L->E = take(L->grads ? (size_t)L->panel * L->ldE * es : 0);
+  L->hidden = take(L->copy_hidden ? (size_t)a->N * L->dp * es : 0);
+  L->weight = take(L->copy_weight ? (size_t)a->V * L->dp * es : 0);
+  size_t part = 0;
+  if (a->dhidden) part = std::max(part, partial_bytes(L->dx, 1, L->panel, a->d));
+  if (a->dweight) part = std::max(part, partial_bytes(L->dwp, 1, a->V, a->d));
+  L->part = take(part);
+  L->dw = take(L->dw_sum ? (size_t)a->V * a->d * 4 : 0);
+  L->total = at;
+  return SHAMPOO_OK;
+}
+
+template <Elem E, bool AS, bool BS, Epi EPI>
+hipError_t product(ProductArgs& g, const Shape& s, hipStream_t st) {
+  set_shape(g, s);
+  return launch_product<E, AS, BS, EPI>(g, s.large, 1, st);
+}
+
+template <Elem E, typename T>
+shampoo_status run_xent(const shampoo_xent_args* a, const XentLayout& L, hipStream_t st) {
+  unsigned char* w = (unsigned char*)a->ws;
+  const int64_t N = a->N, V = a->V, d = a->d;
+  const int64_t es = sizeof(T);
+  float* inv_count = (float*)(w + L.count);
+  floatx2* stats = (floatx2*)(w + L.stats);
+  float* logit = (float*)(w + L.logit);
+  const bool mean = a->reduction == SHAMPOO_REDUCE_MEAN, each = a->reduction == SHAMPOO_REDUCE_NONE;
+  float* rows = each ? a->loss : (float*)(w + L.rows);
+  const unsigned char* hidden = (const unsigned char*)a->hidden;
+  const unsigned char* weight = (const unsigned char*)a->weight;
+  int64_t ldh = a->ld_hidden, ldw = a->ld_weight;
+  auto pad = [&](const unsigned char* from, int64_t ld, int64_t count, unsigned char* to) -> hipError_t {
+    const int64_t wgs = std::max<int64_t>(1, std::min<int64_t>((count * L.dp + 255) / 256, 16384));
+    hipLaunchKernelGGL((pad_rows_kernel<T>), dim3((unsigned)wgs), dim3(256), 0, st, (const T*)from, ld, count, (int)d, (T*)to, (int)L.dp);
+    return hipGetLastError();
+  };
+  if (N > 0 && L.copy_hidden) {
+    HIP_TRY(pad(hidden, ldh, N, w + L.hidden));
+    hidden = w + L.hidden;
+    ldh = L.dp;
+  }
+  if (N > 0 && L.copy_weight) {
+    HIP_TRY(pad(weight, ldw, V, w + L.weight));
+    weight = w + L.weight;
+    ldw = L.dp;
+  }
+  if (mean) {
+    hipLaunchKernelGGL(xent_count_kernel, dim3(1), dim3(1024), 0, st, a->targets, (int)N, a->ignore_index, inv_count);
+    LAUNCH_CHECK("xent_count");
+  }
+  const Out dw{a->dweight, a->ld_dweight, 0, out_code(a->dweight_dt),
+               a->dweight ? rows_vec(a->dweight, a->ld_dweight, 0, a->dweight_dt) : 0, a->accumulate ? 1.f : 0.f};
+  const Out dw32{w + L.dw, d, 0, 0, d % 4 == 0, 0.f};
+  for (int64_t r0 = 0; r0 < N; r0 += L.panel) {
+    const int64_t M = std::min(L.panel, N - r0);
+    // logits, consumed where they are made
+    ProductArgs g{};
+    g.A = hidden + r0 * ldh * es; g.B = weight;
+    g.lda = ldh; g.ldb = ldw;
+    g.M = (int)M; g.N = (int)V; g.K = (int)d;
+    g.C = L.grads ? w + L.E : nullptr;
+    g.ldc = L.ldE;
+    g.stats = stats; g.target_logit = logit; g.targets = a->targets + r0;
+    HIP_TRY((product<E, false, false, Epi::SOFTMAX>(g, plan_shape(1, M, V, d, (int)es, false), st)));
+    float* lse = a->lse ? a->lse + r0 : (float*)(w + L.lse);
+    RowArgs ra{(const floatx2_t*)stats, logit, a->targets + r0, a->row_scale ? a->row_scale + r0 : nullptr, lse, rows + r0,
+               a->ignore_index, (int)M, (int)V, (int)L.pieces, a->scale};
+    if (M <= 256) hipLaunchKernelGGL((xent_rows_kernel<1>), dim3((unsigned)M), dim3(1024), 0, st, ra);
+    else hipLaunchKernelGGL((xent_rows_kernel<32>), dim3((unsigned)((M + 31) / 32)), dim3(1024), 0, st, ra);
+    LAUNCH_CHECK("xent_rows");
+    if (!L.grads) continue;
+    GradArgs ga{w + L.E, L.ldE, (const floatx2_t*)stats, logit, lse, a->targets + r0, a->row_scale ? a->row_scale + r0 : nullptr,
+                mean ? inv_count : nullptr, a->ignore_index, (int)M, (int)V, (int)L.pieces, a->scale};
+    using TE = typename std::conditional<E == Elem::F32, float, uint16_t>::type;
+    hipLaunchKernelGGL((xent_grad_kernel<TE>), dim3((unsigned)((L.ldE + 2047) / 2048), (unsigned)((M + 3) / 4)), dim3(256), 0, st, ga);
+    LAUNCH_CHECK("xent_grad");
+    float* part = (float*)(w + L.part);
+    if (a->dhidden) {
+      unsigned char* C = (unsigned char*)a->dhidden + r0 * a->ld_dhidden * es;
+      const Out o{C, a->ld_dhidden, 0, out_code(a->dt), rows_vec(C, a->ld_dhidden, 0, a->dt), 0.f};
+      // a shorter last panel keeps the full panel's split, which the workspace holds
+      const Shape s = L.dx;
+      ProductArgs p{};
+      p.A = w + L.E; p.B = weight; p.lda = L.ldE; p.ldb = ldw;
+      p.M = (int)M; p.N = (int)d; p.K = (int)V;
+      point_output(p, s, o, part, 1);
+      HIP_TRY((product<E, false, true, Epi::STORE>(p, s, st)));
+      HIP_TRY(finish_split(p, s, o, part, 1, st));
+    }
+    if (a->dweight) {
+      Out o = L.dw_sum ? dw32 : dw;
+      if (r0 > 0) o.beta = 1.f;
+      Shape s = plan_shape(1, V, d, M, (int)es, true);
+      if (partial_bytes(s, 1, V, d) > partial_bytes(L.dwp, 1, V, d)) s = plan_shape(1, V, d, M, (int)es, false);
+      ProductArgs p{};
+      p.A = w + L.E; p.B = hidden + r0 * ldh * es; p.lda = L.ldE; p.ldb = ldh;
+      p.M = (int)V; p.N = (int)d; p.K = (int)M;
+      point_output(p, s, o, part, 1);
+      HIP_TRY((product<E, true, true, Epi::STORE>(p, s, st)));
+      HIP_TRY(finish_split(p, s, o, part, 1, st));
+    }
+  }
+  if (L.dw_sum) HIP_TRY(sum_splits((const float*)(w + L.dw), 1, 0, dw, 1, (int)V, (int)d, st));
+  if (N == 0 && a->dweight) HIP_TRY(sum_splits(nullptr, 0, 0, dw, 1, (int)V, (int)d, st));  // zeros (or unchanged)
+  if (!each) {
+    hipLaunchKernelGGL(xent_reduce_kernel, dim3(1), dim3(1024), 0, st, rows, (int)N, mean ? inv_count : nullptr, a->loss);
+    LAUNCH_CHECK("xent_reduce");
+  }
+  return SHAMPOO_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+shampoo_status shampoo_quantize_f8(const void* x, shampoo_dtype x_dt, int64_t n, int64_t rows, int64_t cols, int64_t ld, int64_t stride,
+                                   shampoo_dtype fmt, int32_t block_rows, void* q, void* s, void* qt, void* st, hipStream_t stream) {
+  return quantize_f8_impl(x, x_dt, n, rows, cols, ld, stride, fmt, block_rows, q, s, qt, st, stream);
+}
+
+shampoo_status shampoo_matmul_f8_workspace(int64_t n, int64_t M, int64_t N, int64_t K, size_t* bytes) {
+  if (!bytes) return fail(SHAMPOO_E_INVALID, "null pointer argument");
+  const shampoo_status r = check_f8_sizes(n, M, N, K);
+  if (r != SHAMPOO_OK) return r;
+  *bytes = matmul_f8_bytes(n, M, N, K);
+  return SHAMPOO_OK;
+}
+
+shampoo_status shampoo_matmul_f8(const void* a, shampoo_dtype a_dt, const void* a_scale, int32_t a_block_rows, const void* b,
+                                 shampoo_dtype b_dt, const void* b_scale, int32_t b_block_rows, int64_t n, int64_t M, int64_t N,
+                                 int64_t K, void* c, shampoo_dtype c_dt, void* ws, size_t ws_bytes, hipStream_t stream) {
+  return matmul_f8_impl(a, a_dt, a_scale, a_block_rows, b, b_dt, b_scale, b_block_rows, n, M, N, K, c, c_dt, ws, ws_bytes, stream);
+}
+
+shampoo_status shampoo_linear_xent_workspace(const shampoo_xent_args* args, size_t* bytes) {
+  if (!bytes) return fail(SHAMPOO_E_INVALID, "null pointer argument");
+  XentLayout L;
+  const shampoo_status r = xent_layout(args, &L);
+  if (r != SHAMPOO_OK) return r;
+  *bytes = L.total;
+  return SHAMPOO_OK;
+}
+
+shampoo_status shampoo_linear_xent(const shampoo_xent_args* a, hipStream_t stream) {
+  XentLayout L;
+  const shampoo_status r = xent_layout(a, &L);
+  if (r != SHAMPOO_OK) return r;
+  if (!a->weight || (a->N > 0 && (!a->hidden || !a->targets)) || (!a->loss && (a->N > 0 || a->reduction != SHAMPOO_REDUCE_NONE)))
+    return fail(SHAMPOO_E_INVALID, "null pointer argument");
+  const size_t es = size_of(a->dt);
+  if (a->ld_hidden < a->d || a->ld_weight < a->d || (a->dhidden && a->ld_dhidden < a->d) || (a->dweight && a->ld_dweight < a->d))
+    return fail(SHAMPOO_E_INVALID, "row stride below d = %lld", (long long)a->d);
+  if (!aligned(a->hidden, es) || !aligned(a->weight, es) || !aligned(a->dhidden, es) || !aligned(a->targets, 8) || !aligned(a->loss, 4) ||
+      (a->dweight && !aligned(a->dweight, size_of(a->dweight_dt))) || !aligned(a->row_scale, 4) || !aligned(a->lse, 4))
+    return fail(SHAMPOO_E_INVALID, "misaligned pointer");
+  if (!a->ws || a->ws_bytes < L.total || !aligned(a->ws, 256))
+    return fail(SHAMPOO_E_WORKSPACE, "workspace %zu bytes < %zu needed (256-byte aligned)", a->ws ? a->ws_bytes : 0, L.total);
+  return a->dt == SHAMPOO_F32 ? run_xent<Elem::F32, float>(a, L, stream) : run_xent<Elem::BF16, uint16_t>(a, L, stream);
+}
+
+}  // extern "C"

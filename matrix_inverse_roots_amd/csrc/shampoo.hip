@@ -18,14 +18,17 @@
 #include "gemm.hpp"
 #include "gemm_hsym.hpp"
 #include "gemm_nn256.hpp"
+#include "host_common.hpp"
 #include "kernels.hpp"
 #include "shampoo.h"
 
 using namespace shampoo;
 
 namespace {
-
 thread_local std::string g_err;
+}  // namespace
+
+namespace shampoo {
 
 shampoo_status fail(shampoo_status s, const char* fmt, ...) {
   char buf[512];
@@ -37,20 +40,24 @@ shampoo_status fail(shampoo_status s, const char* fmt, ...) {
   return s;
 }
 
-#define HIP_TRY(expr)                                                                  \
-  do {                                                                                 \
-    hipError_t e_ = (expr);                                                            \
-    if (e_ != hipSuccess) return fail(SHAMPOO_E_HIP, "%s: %s", #expr, hipGetErrorString(e_)); \
-  } while (0)
+hipError_t cu_count(int* cus) {
+  static int cache[MAX_DEVICES] = {0};
+  int dev = 0;
+  HIP_TRY_ERR(hipGetDevice(&dev));
+  if (dev >= 0 && dev < MAX_DEVICES && cache[dev] > 0) {
+    *cus = cache[dev];
+    return hipSuccess;
+  }
+  int v = 0;
+  HIP_TRY_ERR(hipDeviceGetAttribute(&v, hipDeviceAttributeMultiprocessorCount, dev));
+  if (dev >= 0 && dev < MAX_DEVICES) cache[dev] = v;
+  *cus = v;
+  return hipSuccess;
+}
 
-#define LAUNCH_CHECK(what)                                                             \
-  do {                                                                                 \
-    hipError_t e_ = hipGetLastError();                                                 \
-    if (e_ != hipSuccess) return fail(SHAMPOO_E_HIP, "%s launch: %s", what, hipGetErrorString(e_)); \
-  } while (0)
+}  // namespace shampoo
 
-constexpr size_t ALIGN = 256;
-inline size_t align_up(size_t x) { return (x + ALIGN - 1) / ALIGN * ALIGN; }
+namespace {
 
 size_t dtype_size(int dt) {
   switch (dt) {
@@ -89,30 +96,6 @@ struct GemmCall {
   const int32_t* cut = nullptr;
   int tile = 64;  // tile side of that list: 64 (tiled kernel) or 128 (persistent 128-tile kernel)
 };
-
-#define HIP_TRY_ERR(expr)         \
-  do {                            \
-    hipError_t e_ = (expr);       \
-    if (e_ != hipSuccess) return e_; \
-  } while (0)
-
-constexpr int MAX_DEVICES = 64;
-
-// Compute units of the current device, queried once per device.
-hipError_t cu_count(int* cus) {
-  static int cache[MAX_DEVICES] = {0};
-  int dev = 0;
-  HIP_TRY_ERR(hipGetDevice(&dev));
-  if (dev >= 0 && dev < MAX_DEVICES && cache[dev] > 0) {
-    *cus = cache[dev];
-    return hipSuccess;
-  }
-  int v = 0;
-  HIP_TRY_ERR(hipDeviceGetAttribute(&v, hipDeviceAttributeMultiprocessorCount, dev));
-  if (dev >= 0 && dev < MAX_DEVICES) cache[dev] = v;
-  *cus = v;
-  return hipSuccess;
-}
 
 // The large-tile products need 128 KB of dynamic LDS, above the default
 // limit; raise each kernel's limit once per device (K tells the kernels

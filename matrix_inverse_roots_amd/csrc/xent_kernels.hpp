@@ -1,0 +1,209 @@
+// Row passes of the projection's softmax cross entropy (gfx950); the products
+// are in product_core.hpp.
+//
+// With logits z = x W^T, the product's epilogue leaves for each row and each
+// piece of 128 columns the maximum m_j and s_j = sum exp(z - m_j), and, for
+// gradients, E = exp(z - m_j).  Then
+//     lse = M + log sum_j s_j exp(m_j - M),  M = max_j m_j,
+//     loss = lse - z_t,
+//     P = g (softmax - onehot) = E g exp(m_j - lse), and g (p_t - 1) at t.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "gemm_common.hpp"
+
+namespace shampoo {
+
+typedef float floatx2_t __attribute__((ext_vector_type(2)));
+
+// out[0] = number of rows whose target is kept, as 1 / max(count, 1)
+__global__ __launch_bounds__(1024) void xent_count_kernel(const int64_t* __restrict__ targets, int N, int64_t ignore,
+                                                          float* __restrict__ inv_count) {
+  __shared__ int red[16];
+  int c = 0;
+  for (int i = threadIdx.x; i < N; i += 1024) c += targets[i] != ignore;
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) c += __shfl_xor(c, d);
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = c;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    int t = 0;
+    for (int w = 0; w < 16; ++w) t += red[w];
+    *inv_count = 1.0f / (float)max(t, 1);
+  }
+}
+
+struct RowArgs {
+  const floatx2_t* stats;      // [pieces][M]
+  const float* target_logit;   // [M]
+  const int64_t* targets;      // [M]
+  const float* row_scale;      // [M] or null
+  float* lse;                  // [M]
+  float* loss;                 // [M] (scaled by row_scale and scale)
+  int64_t ignore;
+  int M, V, pieces;
+  float scale;
+};
+
+// R rows per workgroup of 1024 threads: thread t joins pieces t / R, + 1024 /
+// R, ... of row t % R
+template <int R>
+__global__ __launch_bounds__(1024) void xent_rows_kernel(RowArgs g) {
+  __shared__ floatx2_t red[1024];
+  const int tid = threadIdx.x, lr = tid % R, grp = tid / R;
+  constexpr int G = 1024 / R;
+  const int m = blockIdx.x * R + lr;
+  float mx = -INFINITY, s = 0.f;
+  if (m < g.M) {
+#pragma unroll 8
+    for (int p = grp; p < g.pieces; p += G) {
+      const floatx2_t v = g.stats[(int64_t)p * g.M + m];
+      const float nm = fmaxf(mx, v[0]);
+      const float ref = nm == -INFINITY ? 0.f : nm;
+      s = s * __expf(mx - ref) + v[1] * __expf(v[0] - ref);
+      mx = nm;
+    }
+  }
+  red[tid] = floatx2_t{mx, s};
+  __syncthreads();
+  for (int d = G / 2; d > 0; d /= 2) {
+    if (grp < d) {
+      const floatx2_t o = red[tid + d * R];
+      const float nm = fmaxf(mx, o[0]);
+      const float ref = nm == -INFINITY ? 0.f : nm;
+      s = s * __expf(mx - ref) + o[1] * __expf(o[0] - ref);
+      mx = nm;
+      red[tid] = floatx2_t{mx, s};
+    }
+    __syncthreads();
+  }
+  if (grp == 0 && m < g.M) {
+    const float lse = mx + logf(s);
+    g.lse[m] = lse;
+    const int64_t t = g.targets[m];
+    float l = 0.f;
+    if (t != g.ignore) {
+      l = t >= 0 && t < g.V ? lse - g.target_logit[m] : __builtin_nanf("");
+      l *= g.scale * (g.row_scale ? g.row_scale[m] : 1.f);
+    }
+    g.loss[m] = l;
+  }
+}
+
+// sum of the row losses (float64, fixed order), times 1 / count for the mean
+__global__ __launch_bounds__(1024) void xent_reduce_kernel(const float* __restrict__ rows, int N, const float* __restrict__ inv_count,
+                                                           float* __restrict__ out) {
+  __shared__ double red[16];
+  double a = 0.0;
+  for (int i = threadIdx.x; i < N; i += 1024) a += (double)rows[i];
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) a += __shfl_xor(a, d);
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = a;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    double t = 0.0;
+    for (int w = 0; w < 16; ++w) t += red[w];
+    *out = (float)(inv_count ? t * (double)*inv_count : t);
+  }
+}
+
+struct GradArgs {
+  void* E;                    // [M][ld], in place
+  int64_t ld;
+  const floatx2_t* stats;     // [pieces][M]
+  const float* target_logit;
+  const float* lse;
+  const int64_t* targets;
+  const float* row_scale;
+  const float* inv_count;     // or null
+  int64_t ignore;
+  int M, V, pieces;
+  float scale;
+};
+
+// P from E, in place: a workgroup of 4 waves takes 4 rows x 2048 columns,
+// 32 bytes a lane.  T: float, or uint16_t for bfloat16.
+template <typename T>
+__global__ __launch_bounds__(256) void xent_grad_kernel(GradArgs g) {
+  constexpr int VE = 16 / sizeof(T);
+  const int m = blockIdx.y * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
+  if (m >= g.M) return;
+  const int64_t t = g.targets[m];
+  const bool skip = t == g.ignore, bad = !skip && (t < 0 || t >= g.V);
+  float w = g.scale * (g.row_scale ? g.row_scale[m] : 1.f) * (g.inv_count ? *g.inv_count : 1.f);
+  if (bad) w = __builtin_nanf("");
+  const float lse = g.lse[m];
+  T* row = reinterpret_cast<T*>(g.E) + (int64_t)m * g.ld;
+#pragma unroll
+  for (int u = 0; u < 2048 / (64 * VE); ++u) {
+    const int c = blockIdx.x * 2048 + (u * 64 + lane) * VE;
+    if (c >= g.ld || c >= g.pieces * 128) continue;
+    u32x4 out = u32x4{0, 0, 0, 0};
+    if (!skip) {
+      const float f = w * __expf(g.stats[(int64_t)(c >> 7) * g.M + m][0] - lse);
+      const u32x4 in = *reinterpret_cast<const u32x4*>(row + c);
+      struct Pack { T v[VE]; };
+      Pack p = __builtin_bit_cast(Pack, in);
+#pragma unroll
+      for (int e = 0; e < VE; ++e) {
+        float y;
+        if constexpr (sizeof(T) == 4) y = p.v[e];
+        else y = __builtin_bit_cast(float, (uint32_t)p.v[e] << 16);
+        // a piece of nothing (maximum -inf) holds zeros
+        y = y == 0.f ? (f == f ? 0.f : f) : y * f;
+        if (c + e == t) {
+          // p_t - 1 from the float32 logit: the rounded exponential would
+          // lose it where p_t is near one
+          y = w * expm1f(g.target_logit[m] - lse);
+        }
+        if (c + e >= g.V) y = 0.f;
+        if constexpr (sizeof(T) == 4) p.v[e] = y;
+        else p.v[e] = __builtin_bit_cast(uint16_t, (__bf16)y);
+      }
+      out = __builtin_bit_cast(u32x4, p);
+    }
+    *reinterpret_cast<u32x4*>(row + c) = out;
+  }
+}
+
+// C = sum of `splits` float32 partial results (+ beta C), any output type
+// (0 float32, 1 half, 2 bfloat16); rows of N elements, ldc apart, batches
+// of M rows
+__global__ __launch_bounds__(256) void sum_splits_kernel(const float* __restrict__ part, int splits, int64_t split_stride,
+                                                         void* __restrict__ C, int64_t ldc, int64_t strideC, int M, int N,
+                                                         int c_dt, float beta) {
+  const int64_t total = (int64_t)M * N;
+  const int64_t b = blockIdx.y;
+  for (int64_t i = blockIdx.x * (int64_t)256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+    float a = 0.f;
+    const float* p = part + b * total + i;
+    for (int s = 0; s < splits; ++s) a += p[s * split_stride];
+    const int64_t m = i / N, at = b * strideC + m * ldc + (i - m * N);
+    if (c_dt == 0) {
+      float* o = reinterpret_cast<float*>(C) + at;
+      *o = a + (beta != 0.f ? beta * *o : 0.f);
+    } else if (c_dt == 1) {
+      _Float16* o = reinterpret_cast<_Float16*>(C) + at;
+      *o = (_Float16)(a + (beta != 0.f ? beta * (float)*o : 0.f));
+    } else {
+      __bf16* o = reinterpret_cast<__bf16*>(C) + at;
+      *o = (__bf16)(a + (beta != 0.f ? beta * (float)*o : 0.f));
+    }
+  }
+}
+
+// Rows of `cols` elements (es bytes each), ld apart, copied into rows of ldo
+// with zeros behind: an operand whose rows do not start on 16 bytes
+template <typename T>
+__global__ __launch_bounds__(256) void pad_rows_kernel(const T* __restrict__ x, int64_t ld, int64_t rows, int cols, T* __restrict__ o, int ldo) {
+  const int64_t total = rows * ldo;
+  for (int64_t i = blockIdx.x * (int64_t)256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+    const int64_t r = i / ldo;
+    const int c = (int)(i - r * ldo);
+    o[i] = c < cols ? x[r * ld + c] : T(0);
+  }
+}
+
+}  // namespace shampoo
