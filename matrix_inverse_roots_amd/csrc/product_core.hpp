@@ -52,9 +52,6 @@ typedef short shortx4_t __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef float floatx2 __attribute__((ext_vector_type(2)));
 
-// What a chunk outside an operand reads (16 bytes of zeros).
-__device__ __attribute__((aligned(16))) static const uint32_t product_zeros[4] = {0, 0, 0, 0};
-
 enum class Elem { BF16, F32, F8 };
 enum class Epi { STORE, SOFTMAX };
 
@@ -79,8 +76,6 @@ struct ProductArgs {
   int64_t items;                      // batch * splits * mt * nt
   // SOFTMAX
   floatx2* stats;                     // [pieces][M]: (max, sum of exp(z - max)) of 128 columns
-  float* target_logit;                // [M]
-  const int64_t* targets;             // [M]
 };
 
 template <Elem E> struct ElemTraits;
@@ -126,6 +121,15 @@ __device__ __forceinline__ uint32_t pack_f16(float x, float y) {
   return __builtin_bit_cast(uint32_t, h2{(_Float16)x, (_Float16)y});
 }
 
+// A buffer descriptor: loads at offsets past `bytes` return zeros.
+typedef __amdgpu_buffer_rsrc_t rsrc_t;
+constexpr uint32_t RSRC_FLAGS = 0x00027000;       // raw 32-bit buffer
+constexpr uint32_t RSRC_OUTSIDE = 0x80000000u;    // an offset outside every descriptor
+__device__ __forceinline__ rsrc_t rsrc_of(const unsigned char* p, int64_t bytes) {
+  const uint32_t n = bytes <= 0 ? 0u : bytes >= 0x7fffffff ? 0x7fffffffu : (uint32_t)bytes;
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<unsigned char*>(p), 0, n, RSRC_FLAGS);
+}
+
 template <Elem E, int FM, int FN, int WM, int WN, int NS, bool AS, bool BS, Epi EPI, int FA, int FB>
 __global__ __launch_bounds__(64 * WM * WN, 2) void product_kernel(ProductArgs g) {
   constexpr int ES = ElemTraits<E>::size;
@@ -133,10 +137,15 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_kernel(ProductArgs g)
   constexpr int OPA = TM * 64, STAGE = (TM + TN) * 64;
   constexpr int NIA = TM / 16 / W, NIB = TN / 16 / W, NI = NIA + NIB;
   constexpr int SK = 64 / ES;  // k of one stage
+  constexpr bool SCALED = E == Elem::F8;
+  constexpr int SCALES = NS * STAGE, SGROUP = 4 * (TM + TN);  // LDS: 4 groups of scales behind the ring
   static_assert(NIA * W * 16 == TM && NIB * W * 16 == TN, "loads divide among the waves");
-  static_assert(E != Elem::F8 || (!AS && !BS), "8-bit operands are k-contiguous");
+  static_assert(!SCALED || (!AS && !BS), "8-bit operands are k-contiguous");
+  static_assert(!SCALED || (TM + TN) % (64 * W) == 0, "each wave loads the scales of as many rows");
   static_assert(!(AS && TM < 64) && !(BS && TN < 64), "k-strided swizzles need 64 columns");
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
+  typedef __attribute__((address_space(3))) unsigned char lds_u8;
+  lds_u8* const lds = (lds_u8*)smem;
 
   // this workgroup's items: the XCD's contiguous share, dealt round-robin
   const int per = gridDim.x >> 3;
@@ -151,90 +160,116 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_kernel(ProductArgs g)
   const int wm = wave / WN, wn = wave % WN;
   const int l32 = lane & 31, half = lane >> 5;
 
-  struct Item { int64_t batch; int split, tm, tn, k0, stages; };
+  struct Item { int batch, split, tm, tn, k0, stages; };
   // tiles in bands of 8 rows of tiles, column by column: the tiles that run
   // at the same time on an XCD share the operands' panels in its L2
   auto item_of = [&](int it) {
     Item r;
-    int64_t w = first + (int64_t)it * per;
+    const int64_t w = first + (int64_t)it * per;
     const int tiles = g.mt * g.nt;
-    const int64_t bs = w / tiles;
-    int t = (int)(w - bs * tiles);
+    const int bs = (int)(w / tiles);
+    int t = (int)(w - (int64_t)bs * tiles);
     r.batch = bs / g.splits;
-    r.split = (int)(bs - r.batch * g.splits);
+    r.split = bs - r.batch * g.splits;
     const int band = t / (8 * g.nt), rows = min(8, g.mt - 8 * band);
     t -= band * 8 * g.nt;
-    r.tm = 8 * band + t % rows;
     r.tn = t / rows;
+    r.tm = 8 * band + t - r.tn * rows;
     r.k0 = r.split * g.split_stages;
     r.stages = min(g.split_stages, g.nst - r.k0);
     return r;
   };
 
   // ---- loads -------------------------------------------------------------
-  const unsigned char* LA;
-  const unsigned char* LB;
-  uint32_t offA[NIA], offB[NIB];
-  const int Kb = g.K * ES;  // k-contiguous: bytes of a row
-  int lit = 0, lk = 0, lend = 0, ls = 0;  // item, stage, its end, ring slot of the next load
+  // offA, offB: this lane's bytes within a stage's part of the tile; PA, PB:
+  // where that part starts; leftA, leftB: bytes from there to the operand's
+  // end, past which a descriptor reads zeros
+  uint32_t offA[NIA], offB[NIB], kA[NIA], kB[NIB];
   const int kchunk = 16 * ((lane & 3) ^ ((lane >> 4) & 3));  // k-contiguous: byte of the stage this lane loads
-  auto k_of = [&](int I, int T) { return (I * 1024 + lane * 16) / (T * ES); };  // k-strided: k-row in the stage
-  auto begin_loads = [&](const Item& t) {
-    LA = reinterpret_cast<const unsigned char*>(g.A) + t.batch * g.strideA * ES;
-    LB = reinterpret_cast<const unsigned char*>(g.B) + t.batch * g.strideB * ES;
-    auto contiguous = [&](const unsigned char*& P, uint32_t* off, int n, int rows, int row0, int64_t ld) {
-      P += (int64_t)row0 * ld * ES + (int64_t)t.k0 * 64;
-      for (int q = 0; q < n; ++q) {
-        const int r = min(16 * (wave * n + q) + (lane >> 2), rows - 1 - row0);
-        off[q] = (uint32_t)(r * ld * ES) + kchunk;
+  auto offsets = [&](uint32_t* off, uint32_t* kk, int n, bool strided, int T, int64_t ld) {
+#pragma unroll
+    for (int q = 0; q < n; ++q) {
+      const int at = (wave * n + q) * 1024 + lane * 16;
+      if (strided) {
+        const int k = at / (T * ES), pos = at % (T * ES) / 16;
+        off[q] = (uint32_t)(k * ld * ES) + 16 * (pos ^ (ES == 2 ? 4 * (k & 3) : 8 * ((k >> 2) & 1)));
+        kk[q] = k;
+      } else {
+        off[q] = (uint32_t)((at >> 6) * ld * ES) + kchunk;
+        kk[q] = 0;
       }
-    };
-    auto strided = [&](const unsigned char*& P, uint32_t* off, int n, int T, int rows, int row0, int64_t ld) {
-      P += (int64_t)t.k0 * SK * ld * ES + (int64_t)row0 * ES;
-      for (int q = 0; q < n; ++q) {
-        const int I = wave * n + q, k = k_of(I, T);
-        const int pos = (I * 1024 + lane * 16) % (T * ES) / 16;
-        int c = pos ^ (ES == 2 ? 4 * (k & 3) : 8 * ((k >> 2) & 1));
-        if (row0 + c * (16 / ES) >= rows) c = 0;
-        off[q] = (uint32_t)(k * ld * ES) + 16 * c;
-      }
-    };
-    if constexpr (AS) strided(LA, offA, NIA, TM, g.M, t.tm * TM, g.lda);
-    else contiguous(LA, offA, NIA, g.M, t.tm * TM, g.lda);
-    if constexpr (BS) strided(LB, offB, NIB, TN, g.N, t.tn * TN, g.ldb);
-    else contiguous(LB, offB, NIB, g.N, t.tn * TN, g.ldb);
-    lk = t.k0;
-    lend = t.k0 + t.stages;
+    }
+  };
+  offsets(offA, kA, NIA, AS, TM, g.lda);
+  offsets(offB, kB, NIB, BS, TN, g.ldb);
+  const int Kb = (g.K * ES + 15) & ~15;  // k-contiguous: bytes of a row, in whole chunks
+  const unsigned char *PA, *PB;
+  int64_t leftA, leftB;
+  int lit = 0, lk = 0, lend = 0, ls = 0, lg = 0;  // item, stage, its end, ring slot, scale group of the next load
+  Item li;
+  auto begin_loads = [&]() {
+    li = item_of(lit);
+    lk = li.k0;
+    lend = li.k0 + li.stages;
+    const int ra = li.tm * TM, rb = li.tn * TN;
+    const int64_t ka = AS ? (int64_t)lk * SK * g.lda * ES : (int64_t)lk * 64, kb = BS ? (int64_t)lk * SK * g.ldb * ES : (int64_t)lk * 64;
+    PA = reinterpret_cast<const unsigned char*>(g.A) + li.batch * g.strideA * ES + ka + (AS ? (int64_t)ra * ES : ra * g.lda * ES);
+    PB = reinterpret_cast<const unsigned char*>(g.B) + li.batch * g.strideB * ES + kb + (BS ? (int64_t)rb * ES : rb * g.ldb * ES);
+    // strided: the last k-row's columns, in whole chunks (rows start on 16 bytes)
+    leftA = AS ? (g.K - 1) * g.lda * ES + (((g.M - ra) * ES + 15) & ~15) - ka : (g.M - 1 - ra) * g.lda * ES + Kb - ka;
+    leftB = BS ? (g.K - 1) * g.ldb * ES + (((g.N - rb) * ES + 15) & ~15) - kb : (g.N - 1 - rb) * g.ldb * ES + Kb - kb;
   };
   // one stage into the ring; false once every item's stages are issued
   auto issue = [&]() -> bool {
     if (lit >= nitem) return false;
-    unsigned char* sa = smem + ls * STAGE;
-    unsigned char* sb = sa + OPA;
-    const unsigned char* zero = reinterpret_cast<const unsigned char*>(product_zeros);
-    const bool whole = (lk + 1) * 64 <= Kb;  // (a k-row is ES bytes here)
-    auto load = [&](const unsigned char* P, const uint32_t* off, int n, unsigned char* dst, bool strided, int T) {
+    const rsrc_t ra = rsrc_of(PA, leftA), rb = rsrc_of(PB, leftB);
+    lds_u8* const sa = lds + ls * STAGE + wave * (NIA * 1024);
+    lds_u8* const sb = lds + ls * STAGE + OPA + wave * (NIB * 1024);
+    const bool whole = (lk + 1) * SK <= g.K;
+    // the last stages of a row or column reach past K: zeros there
+    const uint32_t outside = lk * 64 + kchunk < Kb ? 0 : RSRC_OUTSIDE;
 #pragma unroll
-      for (int q = 0; q < n; ++q) {
-        const unsigned char* p = P + off[q];
-        if (!whole) {
-          const bool in = strided ? lk * SK + k_of(wave * n + q, T) < g.K : lk * 64 + kchunk < Kb;
-          p = in ? p : zero;
+    for (int q = 0; q < NIA; ++q) {
+      uint32_t o = offA[q];
+      if (!whole) o |= AS ? (lk * SK + (int)kA[q] < g.K ? 0 : RSRC_OUTSIDE) : outside;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, sa + q * 1024, 16, o, 0, 0, 0);
+    }
+#pragma unroll
+    for (int q = 0; q < NIB; ++q) {
+      uint32_t o = offB[q];
+      if (!whole) o |= BS ? (lk * SK + (int)kB[q] < g.K ? 0 : RSRC_OUTSIDE) : outside;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, sb + q * 1024, 16, o, 0, 0, 0);
+    }
+    if constexpr (SCALED) {
+      // with the first stage of 8: the 4 scales of each of the tile's rows
+      // for the 512 k that follow
+      if (((lk - li.k0) & 7) == 0) {
+        constexpr int NSG = (TM + TN) / (64 * W);
+#pragma unroll
+        for (int q = 0; q < NSG; ++q) {
+          const int first_row = (wave * NSG + q) * 64;  // wave-uniform: A's rows, then B's
+          const bool isA = first_row < TM;
+          const int row = isA ? min(li.tm * TM + first_row + lane, g.M - 1) >> g.sa_shift
+                              : min(li.tn * TN + first_row - TM + lane, g.N - 1) >> g.sb_shift;
+          const uint8_t* p = isA ? g.sa + li.batch * g.strideSa + (int64_t)row * g.ldsa
+                                 : g.sb + li.batch * g.strideSb + (int64_t)row * g.ldsb;
+          __builtin_amdgcn_global_load_lds((const void*)(p + 4 * (lk >> 3)), (void*)(smem + SCALES + lg * SGROUP + first_row * 4), 4, 0, 0);
         }
-        __builtin_amdgcn_global_load_lds((const void*)p, (void*)(dst + (wave * n + q) * 1024), 16, 0, 0);
+        lg = (lg + 1) & 3;
       }
-    };
-    load(LA, offA, NIA, sa, AS, TM);
-    load(LB, offB, NIB, sb, BS, TN);
-    LA += AS ? SK * g.lda * ES : 64;
-    LB += BS ? SK * g.ldb * ES : 64;
+    }
+    const int64_t da = AS ? SK * g.lda * ES : 64, db = BS ? SK * g.ldb * ES : 64;
+    PA += da; leftA -= da;
+    PB += db; leftB -= db;
     ls = ls + 1 == NS ? 0 : ls + 1;
-    if (++lk == lend && ++lit < nitem) begin_loads(item_of(lit));
+    if (++lk == lend && ++lit < nitem) begin_loads();
     return true;
   };
 
   // ---- fragments ---------------------------------------------------------
   const int kc0 = l32 * 64 + 16 * (half ^ ((l32 >> 2) & 3)), kc1 = kc0 ^ 32;
+  // k-strided bfloat16: k 16 st + 8 half + 4 q + i of column row + 16 grp + 4 u
+  const int ti = (lane & 15) >> 2, tu = lane & 3, tgrp = (lane >> 4) & 1;
   auto frag = [&](const unsigned char* base, int row, bool strided, int T) -> intx8 {
     if (!strided) {
       const u32x4 x = *reinterpret_cast<const u32x4*>(base + row * 64 + kc0);
@@ -242,10 +277,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_kernel(ProductArgs g)
       return intx8{(int)x[0], (int)x[1], (int)x[2], (int)x[3], (int)y[0], (int)y[1], (int)y[2], (int)y[3]};
     }
     if constexpr (E == Elem::BF16) {
-      // stage k 16 st + 8 half + 4 q + i of column row + 16 grp + 4 u
-      const int i = (lane & 15) >> 2, u = lane & 3, grp = (lane >> 4) & 1;
-      const int col = row + 16 * grp + 4 * u;
-      const unsigned char* p = base + (8 * half + i) * (T * 2) + 16 * ((col >> 3) ^ (4 * i)) + 2 * (col & 7);
+      const int col = row + 16 * tgrp + 4 * tu;
+      const unsigned char* p = base + (8 * half + ti) * (T * 2) + 16 * ((col >> 3) ^ (4 * ti)) + 2 * (col & 7);
       typedef __attribute__((address_space(3))) shortx4_t lds_s4;
       struct Four { shortx4_t v[4]; } f;
 #pragma unroll
@@ -271,58 +304,44 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_kernel(ProductArgs g)
 #pragma unroll
     for (int j = 0; j < FN; ++j) fb[set][j] = frag(sb, (wn * FN + j) * 32, BS, TN);
   };
-
-  // ---- scales (F8): one dword = 4 blocks of 128 k of a row ----------------
-  constexpr int NSC = E == Elem::F8 ? FM + FN : 1;
-  uint32_t sc[NSC], sn[NSC];
-  auto load_scales = [&](const Item& t, int kb4, uint32_t* to) {
-    if constexpr (E == Elem::F8) {
+  // the scale bytes of the block of 128 k that stage s (even) begins
+  int sca[FM], scb[FN];
+  auto read_scales = [&](int group, int s) {
+    if constexpr (SCALED) {
+      const unsigned char* p = smem + SCALES + group * SGROUP + l32 * 4 + ((s >> 1) & 3);
 #pragma unroll
-      for (int i = 0; i < FM; ++i) {
-        const int r = min(t.tm * TM + (wm * FM + i) * 32 + l32, g.M - 1) >> g.sa_shift;
-        to[i] = *reinterpret_cast<const uint32_t*>(g.sa + t.batch * g.strideSa + (int64_t)r * g.ldsa + 4 * kb4);
-      }
+      for (int i = 0; i < FM; ++i) sca[i] = p[(wm * FM + i) * 128];
 #pragma unroll
-      for (int j = 0; j < FN; ++j) {
-        const int r = min(t.tn * TN + (wn * FN + j) * 32 + l32, g.N - 1) >> g.sb_shift;
-        to[FM + j] = *reinterpret_cast<const uint32_t*>(g.sb + t.batch * g.strideSb + (int64_t)r * g.ldsb + 4 * kb4);
-      }
+      for (int j = 0; j < FN; ++j) scb[j] = p[(TM + (wn * FN + j) * 32) * 4];
     }
   };
 
   floatx16 acc[FM][FN];
-  Item cur = item_of(0);
-  begin_loads(cur);
-#pragma unroll
+  begin_loads();
+#pragma nounroll
   for (int s = 0; s < NS; ++s) issue();  // a dry ring leaves its slots unread
-  if constexpr (E == Elem::F8) load_scales(cur, cur.k0 >> 3, sc);
   wait_stage<0>();
   barrier_no_fence();
-  int rs = 0;  // ring slot of the stage being multiplied
+  int rs = 0, rg = 0;  // ring slot and scale group of the stage being multiplied
   read_frags(0, 0);
   wait_stage<0>();
   barrier_no_fence();
 
+#pragma nounroll
   for (int it = 0; it < nitem; ++it) {
+    const Item cur = item_of(it);
 #pragma unroll
     for (int i = 0; i < FM; ++i)
 #pragma unroll
       for (int j = 0; j < FN; ++j)
 #pragma unroll
         for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
-    const Item nxt = it + 1 < nitem ? item_of(it + 1) : cur;
+#pragma nounroll
     for (int s = 0; s < cur.stages; s += 2) {
-      if constexpr (E == Elem::F8) {
-        if ((s & 7) == 0) {
-          if (s) {
-#pragma unroll
-            for (int i = 0; i < NSC; ++i) sc[i] = sn[i];
-          }
-          const bool more = s + 8 < cur.stages;
-          load_scales(more ? cur : nxt, more ? (cur.k0 + s + 8) >> 3 : nxt.k0 >> 3, sn);
-        }
+      if constexpr (SCALED) {
+        if (s && (s & 7) == 0) rg = (rg + 1) & 3;
+        read_scales(rg, s);
       }
-      const int shift = 4 * (s & 6);  // byte of the block of 128
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         const bool dma = issue();  // into slot rs, read into registers before the last barrier
@@ -332,9 +351,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_kernel(ProductArgs g)
         for (int i = 0; i < FM; ++i)
 #pragma unroll
           for (int j = 0; j < FN; ++j)
-            acc[i][j] = stage_mma<E, FB, FA>(fb[u][j], fa[u][i], acc[i][j],
-                                             E == Elem::F8 ? (int)(sc[E == Elem::F8 ? FM + j : 0] >> shift) : 0,
-                                             E == Elem::F8 ? (int)(sc[E == Elem::F8 ? i : 0] >> shift) : 0);
+            acc[i][j] = stage_mma<E, FB, FA>(fb[u][j], fa[u][i], acc[i][j], SCALED ? scb[j] : 0, SCALED ? sca[i] : 0);
         // the stage after next has landed; NS - 2 younger ones may be in flight
         if (dma) wait_stage<(NS - 2) * NI>();
         else wait_stage<0>();
@@ -342,14 +359,17 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_kernel(ProductArgs g)
         rs = nx;
       }
     }
+    rg = (rg + 1) & 3;
 
     // ---- epilogue --------------------------------------------------------
+    int el32 = l32, ehalf = half;
+    asm volatile("" : "+v"(el32), "+v"(ehalf));  // addresses made here, not kept through the loop
     const int m0 = cur.tm * TM + wm * FM * 32, n0 = cur.tn * TN + wn * FN * 32;
     if constexpr (EPI == Epi::STORE) {
       const int64_t base = cur.batch * g.strideC + cur.split * g.split_stride;
 #pragma unroll
       for (int i = 0; i < FM; ++i) {
-        const int m = m0 + 32 * i + l32;
+        const int m = m0 + 32 * i + el32;
         const int64_t row = base + (int64_t)m * g.ldc;
 #pragma unroll
         for (int j = 0; j < FN; ++j) {
@@ -358,7 +378,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_kernel(ProductArgs g)
             float* C = reinterpret_cast<float*>(g.C) + row;
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-              const int n = nb + 8 * q + 4 * half;
+              const int n = nb + 8 * q + 4 * ehalf;
               floatx4 v = floatx4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
               if (m >= g.M || n >= g.N) continue;
               if (g.vec && n + 4 <= g.N) {
@@ -376,7 +396,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_kernel(ProductArgs g)
             // wave swap one run each
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
-              const int n = nb + 16 * q + 8 * half;
+              const int n = nb + 16 * q + 8 * ehalf;
               float x[8];
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
@@ -413,27 +433,27 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_kernel(ProductArgs g)
         }
       }
     } else {
-      // 128 columns of the wave's rows: maximum, sum of exponentials, the
-      // target's logit; the exponentials against that maximum, rounded to
-      // the gradients' type, where the caller wants gradients
+      // 128 columns of the wave's rows: maximum and sum of exponentials; the
+      // exponentials against that maximum, rounded to the gradients' type,
+      // where the caller wants gradients
       static_assert(FN == 4 || EPI != Epi::SOFTMAX, "a piece is 128 columns");
       constexpr float L2E = 1.4426950408889634f;
 #pragma unroll
       for (int i = 0; i < FM; ++i) {
-        const int m = m0 + 32 * i + l32;
-        const int64_t tg = m < g.M ? g.targets[m] : -1;
-        const int t = tg >= n0 && tg < g.N && tg < n0 + 128 ? (int)(tg - n0) : -1;
-        float mx = -INFINITY, tl = 0.f;
-        bool hit = false;
+        const int m = m0 + 32 * i + el32;
+        if (n0 + 128 > g.N) {
+          const int edge = g.N - n0 - 4 * ehalf;  // columns past the vocabulary count for nothing
+#pragma unroll
+          for (int j = 0; j < FN; ++j)
+#pragma unroll
+            for (int v = 0; v < 16; ++v)
+              if (32 * j + 8 * (v >> 2) + (v & 3) >= edge) acc[i][j][v] = -INFINITY;
+        }
+        float mx = -INFINITY;
 #pragma unroll
         for (int j = 0; j < FN; ++j)
 #pragma unroll
-          for (int v = 0; v < 16; ++v) {
-            const int c = 32 * j + 8 * (v >> 2) + 4 * half + (v & 3);
-            if (n0 + c >= g.N) acc[i][j][v] = -INFINITY;
-            mx = fmaxf(mx, acc[i][j][v]);
-            if (t == c) { tl = acc[i][j][v]; hit = true; }
-          }
+          for (int v = 0; v < 16; ++v) mx = fmaxf(mx, acc[i][j][v]);
         mx = fmaxf(mx, __shfl_xor(mx, 32));
         const float ref = mx == -INFINITY ? 0.f : mx;
         float sum = 0.f;
@@ -446,10 +466,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_kernel(ProductArgs g)
             sum += e;
           }
         sum += __shfl_xor(sum, 32);
-        if (m < g.M && n0 < g.N) {
-          if (half == 0) g.stats[(int64_t)(n0 >> 7) * g.M + m] = floatx2{mx, sum};
-          if (hit) g.target_logit[m] = tl;
-        }
+        if (m < g.M && n0 < g.N && ehalf == 0) g.stats[(int64_t)(n0 >> 7) * g.M + m] = floatx2{mx, sum};
         if (g.C) {
           // rows of ldc elements, a multiple of 128: no edge within a piece
 #pragma unroll
@@ -459,7 +476,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_kernel(ProductArgs g)
               for (int q = 0; q < 4; ++q) {
                 const floatx4 v = floatx4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
                 if (m < g.M && n0 < g.N)
-                  *reinterpret_cast<floatx4*>(reinterpret_cast<float*>(g.C) + (int64_t)m * g.ldc + n0 + 32 * j + 8 * q + 4 * half) = v;
+                  *reinterpret_cast<floatx4*>(reinterpret_cast<float*>(g.C) + (int64_t)m * g.ldc + n0 + 32 * j + 8 * q + 4 * ehalf) = v;
               }
             } else {
 #pragma unroll
@@ -469,7 +486,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_kernel(ProductArgs g)
                 const auto a = __builtin_amdgcn_permlane32_swap(p0, p2, false, false);
                 const auto b = __builtin_amdgcn_permlane32_swap(p1, p3, false, false);
                 if (m < g.M && n0 < g.N)
-                  *reinterpret_cast<u32x4*>(reinterpret_cast<uint16_t*>(g.C) + (int64_t)m * g.ldc + n0 + 32 * j + 16 * q + 8 * half) =
+                  *reinterpret_cast<u32x4*>(reinterpret_cast<uint16_t*>(g.C) + (int64_t)m * g.ldc + n0 + 32 * j + 16 * q + 8 * ehalf) =
                       u32x4{a[0], b[0], a[1], b[1]};
               }
             }
@@ -477,11 +494,6 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_kernel(ProductArgs g)
         }
       }
     }
-    if constexpr (E == Elem::F8) {
-#pragma unroll
-      for (int i = 0; i < NSC; ++i) sc[i] = sn[i];
-    }
-    cur = nxt;
   }
 }
 

@@ -59,7 +59,8 @@ Shape plan_shape(int64_t batch, int64_t M, int64_t N, int64_t K, int es, bool ma
 
 template <Elem E, int FM, int FN, int WM, int WN, int NS, int PER_CU, bool AS, bool BS, Epi EPI, int FA, int FB>
 hipError_t launch_tiles(ProductArgs g, int64_t batch, hipStream_t st) {
-  constexpr int TM = 32 * FM * WM, TN = 32 * FN * WN, LDS = NS * (TM + TN) * 64;
+  constexpr int TM = 32 * FM * WM, TN = 32 * FN * WN;
+  constexpr int LDS = NS * (TM + TN) * 64 + (E == Elem::F8 ? 16 * (TM + TN) : 0);  // ring, 4 groups of scales
   const auto kernel = product_kernel<E, FM, FN, WM, WN, NS, AS, BS, EPI, FA, FB>;
   static bool ready[MAX_DEVICES] = {false};
   int dev = 0, cus = 0;
@@ -244,7 +245,7 @@ namespace {
 // ---------------------------------------------------------------------------
 // softmax cross entropy
 // ---------------------------------------------------------------------------
-constexpr int64_t XENT_MAX_ROW = int64_t(1) << 21;  // elements: 256 rows stay within 32-bit offsets
+constexpr int64_t XENT_MAX_ROW = int64_t(1) << 20;  // elements: 256 rows stay within 32-bit offsets
 constexpr int64_t XENT_PANEL_BYTES = int64_t(1) << 31;
 constexpr int64_t XENT_STATS_BYTES = int64_t(1) << 28;
 
@@ -319,6 +320,7 @@ hipError_t product(ProductArgs& g, const Shape& s, hipStream_t st) {
 
 template <Elem E, typename T>
 shampoo_status run_xent(const shampoo_xent_args* a, const XentLayout& L, hipStream_t st) {
+  using TE = typename std::conditional<E == Elem::F32, float, uint16_t>::type;
   unsigned char* w = (unsigned char*)a->ws;
   const int64_t N = a->N, V = a->V, d = a->d;
   const int64_t es = sizeof(T);
@@ -361,18 +363,17 @@ shampoo_status run_xent(const shampoo_xent_args* a, const XentLayout& L, hipStre
     g.M = (int)M; g.N = (int)V; g.K = (int)d;
     g.C = L.grads ? w + L.E : nullptr;
     g.ldc = L.ldE;
-    g.stats = stats; g.target_logit = logit; g.targets = a->targets + r0;
+    g.stats = stats;
     HIP_TRY((product<E, false, false, Epi::SOFTMAX>(g, plan_shape(1, M, V, d, (int)es, false), st)));
     float* lse = a->lse ? a->lse + r0 : (float*)(w + L.lse);
-    RowArgs ra{(const floatx2_t*)stats, logit, a->targets + r0, a->row_scale ? a->row_scale + r0 : nullptr, lse, rows + r0,
+    RowArgs ra{(const floatx2_t*)stats, g.A, weight, ldh, ldw, (int)d, logit, a->targets + r0, a->row_scale ? a->row_scale + r0 : nullptr, lse, rows + r0,
                a->ignore_index, (int)M, (int)V, (int)L.pieces, a->scale};
-    if (M <= 256) hipLaunchKernelGGL((xent_rows_kernel<1>), dim3((unsigned)M), dim3(1024), 0, st, ra);
-    else hipLaunchKernelGGL((xent_rows_kernel<32>), dim3((unsigned)((M + 31) / 32)), dim3(1024), 0, st, ra);
+    if (M <= 256) hipLaunchKernelGGL((xent_rows_kernel<1, TE>), dim3((unsigned)M), dim3(1024), 0, st, ra);
+    else hipLaunchKernelGGL((xent_rows_kernel<32, TE>), dim3((unsigned)((M + 31) / 32)), dim3(1024), 0, st, ra);
     LAUNCH_CHECK("xent_rows");
     if (!L.grads) continue;
     GradArgs ga{w + L.E, L.ldE, (const floatx2_t*)stats, logit, lse, a->targets + r0, a->row_scale ? a->row_scale + r0 : nullptr,
                 mean ? inv_count : nullptr, a->ignore_index, (int)M, (int)V, (int)L.pieces, a->scale};
-    using TE = typename std::conditional<E == Elem::F32, float, uint16_t>::type;
     hipLaunchKernelGGL((xent_grad_kernel<TE>), dim3((unsigned)((L.ldE + 2047) / 2048), (unsigned)((M + 3) / 4)), dim3(256), 0, st, ga);
     LAUNCH_CHECK("xent_grad");
     float* part = (float*)(w + L.part);

@@ -37,7 +37,11 @@ __global__ __launch_bounds__(1024) void xent_count_kernel(const int64_t* __restr
 
 struct RowArgs {
   const floatx2_t* stats;      // [pieces][M]
-  const float* target_logit;   // [M]
+  const void* hidden;          // [M][ldh]
+  const void* weight;          // [V][ldw]
+  int64_t ldh, ldw;
+  int d;
+  float* target_logit;         // [M]
   const int64_t* targets;      // [M]
   const float* row_scale;      // [M] or null
   float* lse;                  // [M]
@@ -48,10 +52,13 @@ struct RowArgs {
 };
 
 // R rows per workgroup of 1024 threads: thread t joins pieces t / R, + 1024 /
-// R, ... of row t % R
-template <int R>
+// R, ... of row t % R.  The target's logit is a product of two rows of its
+// own, by 1024 / R threads: cheaper than to look for it among the logits in
+// the large product's epilogue.  T: float, or uint16_t for bfloat16.
+template <int R, typename T>
 __global__ __launch_bounds__(1024) void xent_rows_kernel(RowArgs g) {
   __shared__ floatx2_t red[1024];
+  __shared__ float dots[1024];
   const int tid = threadIdx.x, lr = tid % R, grp = tid / R;
   constexpr int G = 1024 / R;
   const int m = blockIdx.x * R + lr;
@@ -66,6 +73,22 @@ __global__ __launch_bounds__(1024) void xent_rows_kernel(RowArgs g) {
       mx = nm;
     }
   }
+  // z_t: threads of one row are R apart in `red`, so they are in the dot too
+  float dot = 0.f;
+  int64_t t = -1;
+  if (m < g.M) {
+    t = g.targets[m];
+    if (t != g.ignore && t >= 0 && t < g.V) {
+      const T* x = reinterpret_cast<const T*>(g.hidden) + m * g.ldh;
+      const T* w = reinterpret_cast<const T*>(g.weight) + t * g.ldw;
+#pragma unroll 4
+      for (int k = grp; k < g.d; k += G) {
+        if constexpr (sizeof(T) == 4) dot += x[k] * w[k];
+        else dot += __builtin_bit_cast(float, (uint32_t)x[k] << 16) * __builtin_bit_cast(float, (uint32_t)w[k] << 16);
+      }
+    }
+  }
+  dots[tid] = dot;
   red[tid] = floatx2_t{mx, s};
   __syncthreads();
   for (int d = G / 2; d > 0; d /= 2) {
@@ -76,16 +99,18 @@ __global__ __launch_bounds__(1024) void xent_rows_kernel(RowArgs g) {
       s = s * __expf(mx - ref) + o[1] * __expf(o[0] - ref);
       mx = nm;
       red[tid] = floatx2_t{mx, s};
+      dot += dots[tid + d * R];
+      dots[tid] = dot;
     }
     __syncthreads();
   }
   if (grp == 0 && m < g.M) {
     const float lse = mx + logf(s);
     g.lse[m] = lse;
-    const int64_t t = g.targets[m];
+    g.target_logit[m] = dot;
     float l = 0.f;
     if (t != g.ignore) {
-      l = t >= 0 && t < g.V ? lse - g.target_logit[m] : __builtin_nanf("");
+      l = t >= 0 && t < g.V ? lse - dot : __builtin_nanf("");
       l *= g.scale * (g.row_scale ? g.row_scale[m] : 1.f);
     }
     g.loss[m] = l;
