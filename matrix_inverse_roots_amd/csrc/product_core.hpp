@@ -16,19 +16,19 @@
 // Structure.  One workgroup of WM x WN waves computes a tile of
 // 32 FM WM x 32 FN WN outputs; workgroups are persistent and walk the tiles
 // of their XCD's share, so that the loads of the next tile run through the
-// end of the current one.  A stage is 64 bytes of k of every row of both
-// operands; stages go straight to LDS (global_load_lds, 16 bytes a lane)
-// into a ring of NS buffers.  Each wave reads the fragments of stage s + 1
-// into registers while the matrix cores work on stage s, so that stage s's
-// buffer is free by then and takes stage s + NS; one barrier per stage, which
-// a wave enters with its LDS reads done.
+// end of the current one.  A stage is 128 bytes of k of every row of both
+// operands; stages go straight to LDS (buffer_load ... lds, 16 bytes a lane)
+// into two buffers.  Each wave reads one half of a stage's k into registers
+// while the matrix cores work on the half before it, so a stage's buffer is
+// free when its second half is multiplied, and takes the stage after next:
+// loads have the time of a whole stage to land.  One barrier per stage.
 //
 // LDS layouts, conflict-free for the reads (16 lanes of a ds_read_b128 are
 // served together: lanes 0-3, 12-15, 20-23, 24-27 of each 32):
-//   k-contiguous: rows of 64 bytes, 16-byte chunk c of row r at
-//     c ^ ((r >> 2) & 3); lane l reads row l % 32, chunks h and 2 + h of the
-//     row, h = l / 32.  A fragment is 32 bytes a lane: the k a lane holds are
-//     the same for both operands, which is all a dot product needs.
+//   k-contiguous: rows of 128 bytes, 16-byte chunk c of row r at
+//     c ^ ((r >> 1) & 7); lane l reads row l % 32, chunks h and 2 + h of each
+//     half row, h = l / 32.  A fragment is 32 bytes a lane: the k a lane holds
+//     are the same for both operands, which is all a dot product needs.
 //   k-strided bfloat16: k-rows of the tile's width, chunk c of k-row k at
 //     c ^ 4 (k & 3); fragments come from ds_read_b64_tr_b16, which gives lane
 //     j of 16 column j of 4 k-rows.
@@ -68,8 +68,8 @@ struct ProductArgs {
   int M, N, K;
   int sa_shift, sb_shift;             // 0: a scale per row; 7: per 128 rows
   int mt, nt;                         // tiles along M and N
-  int nst;                            // k-stages (even; F8: a multiple of 8 or the last range's rest)
-  int splits, split_stages;           // ranges of k; stages of each but the last
+  int nst;                            // k-stages of 128 bytes
+  int splits, split_stages;           // ranges of k; stages of each but the last (F8: a multiple of 4)
   int c_dt;                           // 0 float32, 1 half, 2 bfloat16
   int vec;                            // rows of C allow 16-byte stores
   float beta;                         // C = acc + beta C (STORE)
@@ -106,7 +106,7 @@ __device__ __forceinline__ floatx16 stage_mma(intx8 b, intx8 a, floatx16 acc, in
 }
 
 // wait until at most K vector memory operations of this wave are in flight,
-// and none of its LDS reads
+// and no LDS reads
 template <int K> __device__ __forceinline__ void wait_stage() {
   static_assert(K >= 0 && K < 64, "vmcnt has 6 bits");
   __builtin_amdgcn_s_waitcnt((K & 15) | (0x7 << 4) | ((K >> 4) << 14));
@@ -130,16 +130,16 @@ __device__ __forceinline__ rsrc_t rsrc_of(const unsigned char* p, int64_t bytes)
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<unsigned char*>(p), 0, n, RSRC_FLAGS);
 }
 
-template <Elem E, int FM, int FN, int WM, int WN, int NS, bool AS, bool BS, Epi EPI, int FA, int FB>
+template <Elem E, int FM, int FN, int WM, int WN, bool AS, bool BS, Epi EPI, int FA, int FB>
 __global__ __launch_bounds__(64 * WM * WN, 2) void product_kernel(ProductArgs g) {
   constexpr int ES = ElemTraits<E>::size;
   constexpr int W = WM * WN, TM = 32 * FM * WM, TN = 32 * FN * WN;
-  constexpr int OPA = TM * 64, STAGE = (TM + TN) * 64;
-  constexpr int NIA = TM / 16 / W, NIB = TN / 16 / W, NI = NIA + NIB;
-  constexpr int SK = 64 / ES;  // k of one stage
+  constexpr int OPA = TM * 128, STAGE = (TM + TN) * 128;
+  constexpr int NIA = TM / 8 / W, NIB = TN / 8 / W;
+  constexpr int SK = 128 / ES;  // k of one stage
   constexpr bool SCALED = E == Elem::F8;
-  constexpr int SCALES = NS * STAGE, SGROUP = 4 * (TM + TN);  // LDS: 4 groups of scales behind the ring
-  static_assert(NIA * W * 16 == TM && NIB * W * 16 == TN, "loads divide among the waves");
+  constexpr int SCALES = 2 * STAGE, SGROUP = 4 * (TM + TN);  // LDS: 4 groups of scales behind the buffers
+  static_assert(NIA * W * 8 == TM && NIB * W * 8 == TN, "loads divide among the waves");
   static_assert(!SCALED || (!AS && !BS), "8-bit operands are k-contiguous");
   static_assert(!SCALED || (TM + TN) % (64 * W) == 0, "each wave loads the scales of as many rows");
   static_assert(!(AS && TM < 64) && !(BS && TN < 64), "k-strided swizzles need 64 columns");
@@ -184,8 +184,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_kernel(ProductArgs g)
   // offA, offB: this lane's bytes within a stage's part of the tile; PA, PB:
   // where that part starts; leftA, leftB: bytes from there to the operand's
   // end, past which a descriptor reads zeros
+  // (kA, kB: the k-row, or the byte of the row, within the stage)
   uint32_t offA[NIA], offB[NIB], kA[NIA], kB[NIB];
-  const int kchunk = 16 * ((lane & 3) ^ ((lane >> 4) & 3));  // k-contiguous: byte of the stage this lane loads
   auto offsets = [&](uint32_t* off, uint32_t* kk, int n, bool strided, int T, int64_t ld) {
 #pragma unroll
     for (int q = 0; q < n; ++q) {
@@ -195,8 +195,9 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_kernel(ProductArgs g)
         off[q] = (uint32_t)(k * ld * ES) + 16 * (pos ^ (ES == 2 ? 4 * (k & 3) : 8 * ((k >> 2) & 1)));
         kk[q] = k;
       } else {
-        off[q] = (uint32_t)((at >> 6) * ld * ES) + kchunk;
-        kk[q] = 0;
+        const int row = at >> 7;
+        kk[q] = 16 * ((lane & 7) ^ ((row >> 1) & 7));
+        off[q] = (uint32_t)(row * ld * ES) + kk[q];
       }
     }
   };
@@ -205,45 +206,44 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_kernel(ProductArgs g)
   const int Kb = (g.K * ES + 15) & ~15;  // k-contiguous: bytes of a row, in whole chunks
   const unsigned char *PA, *PB;
   int64_t leftA, leftB;
-  int lit = 0, lk = 0, lend = 0, ls = 0, lg = 0;  // item, stage, its end, ring slot, scale group of the next load
+  int lit = 0, lk = 0, lend = 0, ls = 0, lg = 0;  // item, stage, its end, buffer, scale group of the next load
   Item li;
   auto begin_loads = [&]() {
     li = item_of(lit);
     lk = li.k0;
     lend = li.k0 + li.stages;
     const int ra = li.tm * TM, rb = li.tn * TN;
-    const int64_t ka = AS ? (int64_t)lk * SK * g.lda * ES : (int64_t)lk * 64, kb = BS ? (int64_t)lk * SK * g.ldb * ES : (int64_t)lk * 64;
+    const int64_t ka = AS ? (int64_t)lk * SK * g.lda * ES : (int64_t)lk * 128, kb = BS ? (int64_t)lk * SK * g.ldb * ES : (int64_t)lk * 128;
     PA = reinterpret_cast<const unsigned char*>(g.A) + li.batch * g.strideA * ES + ka + (AS ? (int64_t)ra * ES : ra * g.lda * ES);
     PB = reinterpret_cast<const unsigned char*>(g.B) + li.batch * g.strideB * ES + kb + (BS ? (int64_t)rb * ES : rb * g.ldb * ES);
     // strided: the last k-row's columns, in whole chunks (rows start on 16 bytes)
     leftA = AS ? (g.K - 1) * g.lda * ES + (((g.M - ra) * ES + 15) & ~15) - ka : (g.M - 1 - ra) * g.lda * ES + Kb - ka;
     leftB = BS ? (g.K - 1) * g.ldb * ES + (((g.N - rb) * ES + 15) & ~15) - kb : (g.N - 1 - rb) * g.ldb * ES + Kb - kb;
   };
-  // one stage into the ring; false once every item's stages are issued
-  auto issue = [&]() -> bool {
-    if (lit >= nitem) return false;
+  // one stage into its buffer, until every item's stages are issued
+  auto issue = [&]() {
+    if (lit >= nitem) return;
     const rsrc_t ra = rsrc_of(PA, leftA), rb = rsrc_of(PB, leftB);
     lds_u8* const sa = lds + ls * STAGE + wave * (NIA * 1024);
     lds_u8* const sb = lds + ls * STAGE + OPA + wave * (NIB * 1024);
     const bool whole = (lk + 1) * SK <= g.K;
-    // the last stages of a row or column reach past K: zeros there
-    const uint32_t outside = lk * 64 + kchunk < Kb ? 0 : RSRC_OUTSIDE;
+    // the last stage of a row or column may reach past K: zeros there
 #pragma unroll
     for (int q = 0; q < NIA; ++q) {
       uint32_t o = offA[q];
-      if (!whole) o |= AS ? (lk * SK + (int)kA[q] < g.K ? 0 : RSRC_OUTSIDE) : outside;
+      if (!whole) o |= (AS ? lk * SK + (int)kA[q] < g.K : lk * 128 + (int)kA[q] < Kb) ? 0 : RSRC_OUTSIDE;
       __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, sa + q * 1024, 16, o, 0, 0, 0);
     }
 #pragma unroll
     for (int q = 0; q < NIB; ++q) {
       uint32_t o = offB[q];
-      if (!whole) o |= BS ? (lk * SK + (int)kB[q] < g.K ? 0 : RSRC_OUTSIDE) : outside;
+      if (!whole) o |= (BS ? lk * SK + (int)kB[q] < g.K : lk * 128 + (int)kB[q] < Kb) ? 0 : RSRC_OUTSIDE;
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, sb + q * 1024, 16, o, 0, 0, 0);
     }
     if constexpr (SCALED) {
-      // with the first stage of 8: the 4 scales of each of the tile's rows
+      // with the first stage of 4: the 4 scales of each of the tile's rows
       // for the 512 k that follow
-      if (((lk - li.k0) & 7) == 0) {
+      if (((lk - li.k0) & 3) == 0) {
         constexpr int NSG = (TM + TN) / (64 * W);
 #pragma unroll
         for (int q = 0; q < NSG; ++q) {
@@ -253,32 +253,31 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_kernel(ProductArgs g)
                               : min(li.tn * TN + first_row - TM + lane, g.N - 1) >> g.sb_shift;
           const uint8_t* p = isA ? g.sa + li.batch * g.strideSa + (int64_t)row * g.ldsa
                                  : g.sb + li.batch * g.strideSb + (int64_t)row * g.ldsb;
-          __builtin_amdgcn_global_load_lds((const void*)(p + 4 * (lk >> 3)), (void*)(smem + SCALES + lg * SGROUP + first_row * 4), 4, 0, 0);
+          __builtin_amdgcn_global_load_lds((const void*)(p + lk), (void*)(smem + SCALES + lg * SGROUP + first_row * 4), 4, 0, 0);
         }
         lg = (lg + 1) & 3;
       }
     }
-    const int64_t da = AS ? SK * g.lda * ES : 64, db = BS ? SK * g.ldb * ES : 64;
+    const int64_t da = AS ? SK * g.lda * ES : 128, db = BS ? SK * g.ldb * ES : 128;
     PA += da; leftA -= da;
     PB += db; leftB -= db;
-    ls = ls + 1 == NS ? 0 : ls + 1;
+    ls ^= 1;
     if (++lk == lend && ++lit < nitem) begin_loads();
-    return true;
   };
 
   // ---- fragments ---------------------------------------------------------
-  const int kc0 = l32 * 64 + 16 * (half ^ ((l32 >> 2) & 3)), kc1 = kc0 ^ 32;
+  const int kc = l32 * 128 + 16 * (half ^ ((l32 >> 1) & 7));
   // k-strided bfloat16: k 16 st + 8 half + 4 q + i of column row + 16 grp + 4 u
   const int ti = (lane & 15) >> 2, tu = lane & 3, tgrp = (lane >> 4) & 1;
-  auto frag = [&](const unsigned char* base, int row, bool strided, int T) -> intx8 {
+  auto frag = [&](const unsigned char* base, int row, int hh, bool strided, int T) -> intx8 {
     if (!strided) {
-      const u32x4 x = *reinterpret_cast<const u32x4*>(base + row * 64 + kc0);
-      const u32x4 y = *reinterpret_cast<const u32x4*>(base + row * 64 + kc1);
+      const u32x4 x = *reinterpret_cast<const u32x4*>(base + row * 128 + (kc ^ (64 * hh)));
+      const u32x4 y = *reinterpret_cast<const u32x4*>(base + row * 128 + (kc ^ (64 * hh + 32)));
       return intx8{(int)x[0], (int)x[1], (int)x[2], (int)x[3], (int)y[0], (int)y[1], (int)y[2], (int)y[3]};
     }
     if constexpr (E == Elem::BF16) {
       const int col = row + 16 * tgrp + 4 * tu;
-      const unsigned char* p = base + (8 * half + ti) * (T * 2) + 16 * ((col >> 3) ^ (4 * ti)) + 2 * (col & 7);
+      const unsigned char* p = base + (32 * hh + 8 * half + ti) * (T * 2) + 16 * ((col >> 3) ^ (4 * ti)) + 2 * (col & 7);
       typedef __attribute__((address_space(3))) shortx4_t lds_s4;
       struct Four { shortx4_t v[4]; } f;
 #pragma unroll
@@ -288,7 +287,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_kernel(ProductArgs g)
           f.v[2 * st + q] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)(p + (16 * st + 4 * q) * (T * 2)));
       return __builtin_bit_cast(intx8, f);
     } else {
-      const unsigned char* p = base + (4 * half) * (T * 4) + 4 * ((row + l32) ^ (32 * half));
+      const unsigned char* p = base + (16 * hh + 4 * half) * (T * 4) + 4 * ((row + l32) ^ (32 * half));
       intx8 f;
 #pragma unroll
       for (int j = 0; j < 8; ++j) f[j] = *reinterpret_cast<const int*>(p + ((j < 4 ? j : 4 + j)) * (T * 4));
@@ -296,36 +295,42 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_kernel(ProductArgs g)
     }
   };
   intx8 fa[2][FM], fb[2][FN];
-  auto read_frags = [&](int slot_, int set) {
-    const unsigned char* sa = smem + slot_ * STAGE;
+  auto read_frags = [&](int buffer, int hh) {
+    const unsigned char* sa = smem + buffer * STAGE;
     const unsigned char* sb = sa + OPA;
 #pragma unroll
-    for (int i = 0; i < FM; ++i) fa[set][i] = frag(sa, (wm * FM + i) * 32, AS, TM);
+    for (int i = 0; i < FM; ++i) fa[hh][i] = frag(sa, (wm * FM + i) * 32, hh, AS, TM);
 #pragma unroll
-    for (int j = 0; j < FN; ++j) fb[set][j] = frag(sb, (wn * FN + j) * 32, BS, TN);
+    for (int j = 0; j < FN; ++j) fb[hh][j] = frag(sb, (wn * FN + j) * 32, hh, BS, TN);
   };
-  // the scale bytes of the block of 128 k that stage s (even) begins
-  int sca[FM], scb[FN];
-  auto read_scales = [&](int group, int s) {
+  // the scale bytes of a stage, which is a block of 128 k
+  int sc[2][FM + FN];
+  auto read_scales = [&](int group, int stage, int* to) {
     if constexpr (SCALED) {
-      const unsigned char* p = smem + SCALES + group * SGROUP + l32 * 4 + ((s >> 1) & 3);
+      const unsigned char* p = smem + SCALES + group * SGROUP + l32 * 4 + (stage & 3);
 #pragma unroll
-      for (int i = 0; i < FM; ++i) sca[i] = p[(wm * FM + i) * 128];
+      for (int i = 0; i < FM; ++i) to[i] = p[(wm * FM + i) * 128];
 #pragma unroll
-      for (int j = 0; j < FN; ++j) scb[j] = p[(TM + (wn * FN + j) * 32) * 4];
+      for (int j = 0; j < FN; ++j) to[FM + j] = p[(TM + (wn * FN + j) * 32) * 4];
     }
   };
 
   floatx16 acc[FM][FN];
+  auto multiply = [&](int hh) {
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+      for (int j = 0; j < FN; ++j)
+        acc[i][j] = stage_mma<E, FB, FA>(fb[hh][j], fa[hh][i], acc[i][j], SCALED ? sc[0][FM + j] : 0, SCALED ? sc[0][i] : 0);
+  };
   begin_loads();
-#pragma nounroll
-  for (int s = 0; s < NS; ++s) issue();  // a dry ring leaves its slots unread
+  issue();
+  issue();
   wait_stage<0>();
   barrier_no_fence();
-  int rs = 0, rg = 0;  // ring slot and scale group of the stage being multiplied
+  int rb = 0, rg = 0;  // buffer and scale group of the stage being multiplied
   read_frags(0, 0);
-  wait_stage<0>();
-  barrier_no_fence();
+  read_scales(0, 0, sc[0]);
 
 #pragma nounroll
   for (int it = 0; it < nitem; ++it) {
@@ -337,29 +342,24 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_kernel(ProductArgs g)
 #pragma unroll
         for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
 #pragma nounroll
-    for (int s = 0; s < cur.stages; s += 2) {
-      if constexpr (SCALED) {
-        if (s && (s & 7) == 0) rg = (rg + 1) & 3;
-        read_scales(rg, s);
-      }
+    for (int s = 0; s < cur.stages; ++s) {
+      // first half of the stage's k; its second half into registers
+      read_frags(rb, 1);
+      multiply(0);
+      wait_stage<0>();  // this wave is done with the buffer, and its part of the next stage has landed
+      barrier_no_fence();
+      // second half; the buffer takes the stage after next (at the very end
+      // the other buffer is stale, and what is read from it unused)
+      issue();
+      const bool last = s + 1 == cur.stages;
+      if (last || (s & 3) == 3) rg = (rg + 1) & 3;
+      read_frags(rb ^ 1, 0);
+      read_scales(rg, last ? 0 : s + 1, sc[1]);
+      multiply(1);
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const bool dma = issue();  // into slot rs, read into registers before the last barrier
-        const int nx = rs + 1 == NS ? 0 : rs + 1;
-        read_frags(nx, 1 - u);  // (after the last stage: a stale slot, unused)
-#pragma unroll
-        for (int i = 0; i < FM; ++i)
-#pragma unroll
-          for (int j = 0; j < FN; ++j)
-            acc[i][j] = stage_mma<E, FB, FA>(fb[u][j], fa[u][i], acc[i][j], SCALED ? scb[j] : 0, SCALED ? sca[i] : 0);
-        // the stage after next has landed; NS - 2 younger ones may be in flight
-        if (dma) wait_stage<(NS - 2) * NI>();
-        else wait_stage<0>();
-        barrier_no_fence();
-        rs = nx;
-      }
+      for (int i = 0; i < FM + FN; ++i) sc[0][i] = sc[1][i];
+      rb ^= 1;
     }
-    rg = (rg + 1) & 3;
 
     // ---- epilogue --------------------------------------------------------
     int el32 = l32, ehalf = half;

@@ -35,8 +35,7 @@ constexpr int CUS = 256;  // planning only; the grid follows the device
 
 Shape plan_shape(int64_t batch, int64_t M, int64_t N, int64_t K, int es, bool may_split) {
   Shape s;
-  const int64_t stages = (K * es + 63) / 64;
-  s.nst = (int)up(stages, 2);
+  s.nst = (int)((K * es + 127) / 128);
   const int64_t tl = batch * ((M + 255) / 256) * ((N + 255) / 256);
   const int64_t ts = batch * ((M + 127) / 128) * ((N + 127) / 128);
   // rounds of the chip, a small round being half the work at 70% of the rate
@@ -47,21 +46,21 @@ Shape plan_shape(int64_t batch, int64_t M, int64_t N, int64_t K, int es, bool ma
   s.split_stages = s.nst;
   const int64_t items = s.large ? tl : ts, slots = s.large ? CUS : 2 * CUS;
   if (may_split && items * 2 <= slots) {
-    // at least 16 stages a range
-    const int64_t want = std::min<int64_t>(slots / items, s.nst / 16);
+    // at least 8 stages a range
+    const int64_t want = std::min<int64_t>(slots / items, s.nst / 8);
     if (want >= 2) {
-      s.split_stages = (int)up((s.nst + want - 1) / want, 8);
+      s.split_stages = (int)up((s.nst + want - 1) / want, 4);
       s.splits = (s.nst + s.split_stages - 1) / s.split_stages;
     }
   }
   return s;
 }
 
-template <Elem E, int FM, int FN, int WM, int WN, int NS, int PER_CU, bool AS, bool BS, Epi EPI, int FA, int FB>
+template <Elem E, int FM, int FN, int WM, int WN, int PER_CU, bool AS, bool BS, Epi EPI, int FA, int FB>
 hipError_t launch_tiles(ProductArgs g, int64_t batch, hipStream_t st) {
   constexpr int TM = 32 * FM * WM, TN = 32 * FN * WN;
-  constexpr int LDS = NS * (TM + TN) * 64 + (E == Elem::F8 ? 16 * (TM + TN) : 0);  // ring, 4 groups of scales
-  const auto kernel = product_kernel<E, FM, FN, WM, WN, NS, AS, BS, EPI, FA, FB>;
+  constexpr int LDS = 2 * (TM + TN) * 128 + (E == Elem::F8 ? 16 * (TM + TN) : 0);  // two stages, 4 groups of scales
+  const auto kernel = product_kernel<E, FM, FN, WM, WN, AS, BS, EPI, FA, FB>;
   static bool ready[MAX_DEVICES] = {false};
   int dev = 0, cus = 0;
   HIP_TRY_ERR(hipGetDevice(&dev));
@@ -80,8 +79,8 @@ hipError_t launch_tiles(ProductArgs g, int64_t batch, hipStream_t st) {
 
 template <Elem E, bool AS, bool BS, Epi EPI, int FA = 0, int FB = 0>
 hipError_t launch_product(const ProductArgs& g, bool large, int64_t batch, hipStream_t st) {
-  if (large) return launch_tiles<E, 2, 4, 4, 2, 4, 1, AS, BS, EPI, FA, FB>(g, batch, st);
-  return launch_tiles<E, 1, 4, 4, 1, 4, 2, AS, BS, EPI, FA, FB>(g, batch, st);
+  if (large) return launch_tiles<E, 2, 4, 4, 2, 1, AS, BS, EPI, FA, FB>(g, batch, st);
+  return launch_tiles<E, 1, 4, 4, 1, 2, AS, BS, EPI, FA, FB>(g, batch, st);
 }
 
 void set_shape(ProductArgs& g, const Shape& s) {
