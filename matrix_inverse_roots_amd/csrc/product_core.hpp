@@ -87,21 +87,20 @@ template <> struct ElemTraits<Elem::F8> { static constexpr int size = 1; };
 __device__ __forceinline__ float bits_float(uint32_t b) { return __builtin_bit_cast(float, b); }
 __device__ __forceinline__ uint32_t float_bits(float f) { return __builtin_bit_cast(uint32_t, f); }
 
-// acc += B fragment x A fragment over one stage (64 bytes of k)
+// matrix-core instructions that a fragment pair (32 bytes a lane) takes
+template <Elem E> constexpr int MMA_STEPS = E == Elem::F8 ? 1 : E == Elem::BF16 ? 2 : 8;
+
+// acc += step `st` of B fragment x A fragment
 template <Elem E, int FB, int FA>
-__device__ __forceinline__ floatx16 stage_mma(intx8 b, intx8 a, floatx16 acc, int scb, int sca) {
+__device__ __forceinline__ floatx16 mma_step(int st, intx8 b, intx8 a, floatx16 acc, int scb, int sca) {
   if constexpr (E == Elem::F8) {
     return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(b, a, acc, FB, FA, 0, scb, 0, sca);
   } else if constexpr (E == Elem::BF16) {
     struct Two { bf16x8 v[2]; };
     const Two bb = __builtin_bit_cast(Two, b), aa = __builtin_bit_cast(Two, a);
-    acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(bb.v[0], aa.v[0], acc, 0, 0, 0);
-    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(bb.v[1], aa.v[1], acc, 0, 0, 0);
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(bb.v[st], aa.v[st], acc, 0, 0, 0);
   } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      acc = __builtin_amdgcn_mfma_f32_32x32x2f32(bits_float(b[j]), bits_float(a[j]), acc, 0, 0, 0);
-    return acc;
+    return __builtin_amdgcn_mfma_f32_32x32x2f32(bits_float(b[st]), bits_float(a[st]), acc, 0, 0, 0);
   }
 }
 
@@ -220,9 +219,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_kernel(ProductArgs g)
     leftA = AS ? (g.K - 1) * g.lda * ES + (((g.M - ra) * ES + 15) & ~15) - ka : (g.M - 1 - ra) * g.lda * ES + Kb - ka;
     leftB = BS ? (g.K - 1) * g.ldb * ES + (((g.N - rb) * ES + 15) & ~15) - kb : (g.N - 1 - rb) * g.ldb * ES + Kb - kb;
   };
-  // one stage into its buffer, until every item's stages are issued
+  // one stage into its buffer (zeros once every item's stages are issued)
   auto issue = [&]() {
-    if (lit >= nitem) return;
     const rsrc_t ra = rsrc_of(PA, leftA), rb = rsrc_of(PB, leftB);
     lds_u8* const sa = lds + ls * STAGE + wave * (NIA * 1024);
     lds_u8* const sb = lds + ls * STAGE + OPA + wave * (NIB * 1024);
@@ -231,19 +229,21 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_kernel(ProductArgs g)
 #pragma unroll
     for (int q = 0; q < NIA; ++q) {
       uint32_t o = offA[q];
-      if (!whole) o |= (AS ? lk * SK + (int)kA[q] < g.K : lk * 128 + (int)kA[q] < Kb) ? 0 : RSRC_OUTSIDE;
+      if (!SCALED && !whole) o |= (AS ? lk * SK + (int)kA[q] < g.K : lk * 128 + (int)kA[q] < Kb) ? 0 : RSRC_OUTSIDE;
       __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, sa + q * 1024, 16, o, 0, 0, 0);
     }
 #pragma unroll
     for (int q = 0; q < NIB; ++q) {
       uint32_t o = offB[q];
-      if (!whole) o |= (BS ? lk * SK + (int)kB[q] < g.K : lk * 128 + (int)kB[q] < Kb) ? 0 : RSRC_OUTSIDE;
+      if (!SCALED && !whole) o |= (BS ? lk * SK + (int)kB[q] < g.K : lk * 128 + (int)kB[q] < Kb) ? 0 : RSRC_OUTSIDE;
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, sb + q * 1024, 16, o, 0, 0, 0);
     }
+  };
+  auto issue_scales = [&]() {
     if constexpr (SCALED) {
       // with the first stage of 4: the 4 scales of each of the tile's rows
       // for the 512 k that follow
-      if (((lk - li.k0) & 3) == 0) {
+      if (((lk - li.k0) & 3) == 0 && lend >= 0) {
         constexpr int NSG = (TM + TN) / (64 * W);
 #pragma unroll
         for (int q = 0; q < NSG; ++q) {
@@ -258,11 +258,16 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_kernel(ProductArgs g)
         lg = (lg + 1) & 3;
       }
     }
+  };
+  auto advance = [&]() {
     const int64_t da = AS ? SK * g.lda * ES : 128, db = BS ? SK * g.ldb * ES : 128;
     PA += da; leftA -= da;
     PB += db; leftB -= db;
     ls ^= 1;
-    if (++lk == lend && ++lit < nitem) begin_loads();
+    if (++lk == lend) {
+      if (++lit < nitem) begin_loads();
+      else leftA = leftB = 0, lend = -1;
+    }
   };
 
   // ---- fragments ---------------------------------------------------------
@@ -318,14 +323,34 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_kernel(ProductArgs g)
   floatx16 acc[FM][FN];
   auto multiply = [&](int hh) {
 #pragma unroll
-    for (int i = 0; i < FM; ++i)
+    for (int st = 0; st < MMA_STEPS<E>; ++st)  // outermost: consecutive instructions write different blocks
 #pragma unroll
-      for (int j = 0; j < FN; ++j)
-        acc[i][j] = stage_mma<E, FB, FA>(fb[hh][j], fa[hh][i], acc[i][j], SCALED ? sc[0][FM + j] : 0, SCALED ? sc[0][i] : 0);
+      for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+          acc[i][j] = mma_step<E, FB, FA>(st, fb[hh][j], fa[hh][i], acc[i][j], SCALED ? sc[0][FM + j] : 0, SCALED ? sc[0][i] : 0);
+  };
+  // The reads (and loads) of a half go between its first matrix-core
+  // instructions: left to itself the compiler puts them behind the last and
+  // waits for them there.
+  constexpr int NMMA = FM * FN * MMA_STEPS<E>;
+  constexpr int NREAD = FM * (AS ? 4 : 2) + FN * (BS ? 4 : 2) + (SCALED ? FM + FN : 0);
+  constexpr int STEPS = NMMA * 3 / 4 < 16 ? NMMA * 3 / 4 : 16, RPS = (NREAD + STEPS - 1) / STEPS;
+  auto interleave = [&](bool loads) {
+#pragma unroll
+    for (int k = 0; k < STEPS; ++k) {
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x100, RPS, 0);
+      if (loads && k < NIA + NIB) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+    }
   };
   begin_loads();
   issue();
+  issue_scales();
+  advance();
   issue();
+  issue_scales();
+  advance();
   wait_stage<0>();
   barrier_no_fence();
   int rb = 0, rg = 0;  // buffer and scale group of the stage being multiplied
@@ -346,19 +371,23 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_kernel(ProductArgs g)
       // first half of the stage's k; its second half into registers
       read_frags(rb, 1);
       multiply(0);
+      interleave(false);
       wait_stage<0>();  // this wave is done with the buffer, and its part of the next stage has landed
       barrier_no_fence();
       // second half; the buffer takes the stage after next (at the very end
       // the other buffer is stale, and what is read from it unused)
-      issue();
+      issue_scales();
       const bool last = s + 1 == cur.stages;
       if (last || (s & 3) == 3) rg = (rg + 1) & 3;
+      issue();
       read_frags(rb ^ 1, 0);
       read_scales(rg, last ? 0 : s + 1, sc[1]);
       multiply(1);
+      interleave(true);
 #pragma unroll
       for (int i = 0; i < FM + FN; ++i) sc[0][i] = sc[1][i];
       rb ^= 1;
+      advance();
     }
 
     // ---- epilogue --------------------------------------------------------
