@@ -120,6 +120,15 @@ __device__ __forceinline__ uint32_t pack_f16(float x, float y) {
   return __builtin_bit_cast(uint32_t, h2{(_Float16)x, (_Float16)y});
 }
 
+// ds_read_b64_tr_b16.  The restrict-qualified parameter tells the compiler
+// that nothing writes what the read sees while it runs: without it, it would
+// wait for every load into LDS in flight before each such read (the waits
+// and barriers that order them are the kernel's own).
+typedef __attribute__((address_space(3))) shortx4_t lds_s4;
+__device__ __forceinline__ shortx4_t read_transposed(const lds_s4* __restrict__ p) {
+  return __builtin_amdgcn_ds_read_tr16_b64_v4i16(const_cast<lds_s4*>(p));
+}
+
 // A buffer descriptor: loads at offsets past `bytes` return zeros.
 typedef __amdgpu_buffer_rsrc_t rsrc_t;
 constexpr uint32_t RSRC_FLAGS = 0x00027000;       // raw 32-bit buffer
@@ -283,13 +292,12 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_kernel(ProductArgs g)
     if constexpr (E == Elem::BF16) {
       const int col = row + 16 * tgrp + 4 * tu;
       const unsigned char* p = base + (32 * hh + 8 * half + ti) * (T * 2) + 16 * ((col >> 3) ^ (4 * ti)) + 2 * (col & 7);
-      typedef __attribute__((address_space(3))) shortx4_t lds_s4;
       struct Four { shortx4_t v[4]; } f;
 #pragma unroll
       for (int st = 0; st < 2; ++st)
 #pragma unroll
         for (int q = 0; q < 2; ++q)
-          f.v[2 * st + q] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)(p + (16 * st + 4 * q) * (T * 2)));
+          f.v[2 * st + q] = read_transposed((const lds_s4*)(p + (16 * st + 4 * q) * (T * 2)));
       return __builtin_bit_cast(intx8, f);
     } else {
       const unsigned char* p = base + (16 * hh + 4 * half) * (T * 4) + 4 * ((row + l32) ^ (32 * half));
