@@ -7,7 +7,13 @@
 // (v_mfma_f32_32x32x2_f32) and 8-bit floating point with a power-of-two
 // scale for each block of 128 k (v_mfma_scale_f32_32x32x64_f8f6f4, which
 // applies the scales to the operands' exponents inside the matrix core: no
-// instruction is spent on them).  Accumulation is float32 throughout.
+// instruction is spent on them).  Accumulation is float32 throughout.  The
+// 8-bit matrix instructions align the products of one instruction to the
+// largest of them and drop what lies some 13 bits below (measured: 1.5e-5
+// relative on random operands, at every K), which a 16-bit result does not
+// show and a float32 result does.  F8W, for float32 results, widens the
+// operands with their scales to bfloat16 in registers (exactly) and
+// multiplies those (5e-9 relative), at half the matrix-core rate.
 //
 // Operand layouts.  "k-contiguous": row r at r * ld, k along the row.
 // "k-strided" (template flags AS, BS; bfloat16 and float32): element (r, k)
@@ -52,7 +58,7 @@ typedef short shortx4_t __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef float floatx2 __attribute__((ext_vector_type(2)));
 
-enum class Elem { BF16, F32, F8 };
+enum class Elem { BF16, F32, F8, F8W };
 enum class Epi { STORE, SOFTMAX };
 
 struct ProductArgs {
@@ -72,7 +78,8 @@ struct ProductArgs {
   int splits, split_stages;           // ranges of k; stages of each but the last (F8: a multiple of 4)
   int c_dt;                           // 0 float32, 1 half, 2 bfloat16
   int vec;                            // rows of C allow 16-byte stores
-  float beta;                         // C = acc + beta C (STORE)
+  float alpha, beta;                  // STORE: C = alpha acc + beta C
+  const float* alpha_dev;             // times this, or null
   int64_t items;                      // batch * splits * mt * nt
   // SOFTMAX
   floatx2* stats;                     // [pieces][M]: (max, sum of exp(z - max)) of 128 columns
@@ -82,13 +89,33 @@ template <Elem E> struct ElemTraits;
 template <> struct ElemTraits<Elem::BF16> { static constexpr int size = 2; };
 template <> struct ElemTraits<Elem::F32> { static constexpr int size = 4; };
 template <> struct ElemTraits<Elem::F8> { static constexpr int size = 1; };
+template <> struct ElemTraits<Elem::F8W> { static constexpr int size = 1; };
 
 // By value: __builtin_bit_cast of a vector's element reads element 0.
 __device__ __forceinline__ float bits_float(uint32_t b) { return __builtin_bit_cast(float, b); }
 __device__ __forceinline__ uint32_t float_bits(float f) { return __builtin_bit_cast(uint32_t, f); }
 
 // matrix-core instructions that a fragment pair (32 bytes a lane) takes
-template <Elem E> constexpr int MMA_STEPS = E == Elem::F8 ? 1 : E == Elem::BF16 ? 2 : 8;
+template <Elem E> constexpr int MMA_STEPS = E == Elem::F8 ? 1 : E == Elem::BF16 ? 2 : E == Elem::F8W ? 4 : 8;
+
+// 8 bytes of a fragment times 2^(byte - 127), as bfloat16
+template <int F> __device__ __forceinline__ bf16x8 widen_f8(int lo, int hi, int byte) {
+  const float scale = bits_float((uint32_t)byte << 23);
+  struct Four { __bf16 v __attribute__((ext_vector_type(2))); };
+  struct { decltype(Four::v) v[4]; } r;
+  if constexpr (F == 0) {
+    r.v[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, false);
+    r.v[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, true);
+    r.v[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, false);
+    r.v[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, true);
+  } else {
+    r.v[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(lo, scale, false);
+    r.v[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(lo, scale, true);
+    r.v[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(hi, scale, false);
+    r.v[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(hi, scale, true);
+  }
+  return __builtin_bit_cast(bf16x8, r);
+}
 
 // acc += step `st` of B fragment x A fragment
 template <Elem E, int FB, int FA>
@@ -145,7 +172,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_kernel(ProductArgs g)
   constexpr int OPA = TM * 128, STAGE = (TM + TN) * 128;
   constexpr int NIA = TM / 8 / W, NIB = TN / 8 / W;
   constexpr int SK = 128 / ES;  // k of one stage
-  constexpr bool SCALED = E == Elem::F8;
+  constexpr bool SCALED = E == Elem::F8 || E == Elem::F8W;
   constexpr int SCALES = 2 * STAGE, SGROUP = 4 * (TM + TN);  // LDS: 4 groups of scales behind the buffers
   static_assert(NIA * W * 8 == TM && NIB * W * 8 == TN, "loads divide among the waves");
   static_assert(!SCALED || (!AS && !BS), "8-bit operands are k-contiguous");
@@ -330,13 +357,29 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_kernel(ProductArgs g)
 
   floatx16 acc[FM][FN];
   auto multiply = [&](int hh) {
+    if constexpr (E == Elem::F8W) {
 #pragma unroll
-    for (int st = 0; st < MMA_STEPS<E>; ++st)  // outermost: consecutive instructions write different blocks
+      for (int st = 0; st < 4; ++st) {
+        bf16x8 a[FM], b[FN];
 #pragma unroll
-      for (int i = 0; i < FM; ++i)
+        for (int i = 0; i < FM; ++i) a[i] = widen_f8<FA>(fa[hh][i][2 * st], fa[hh][i][2 * st + 1], sc[0][i]);
 #pragma unroll
-        for (int j = 0; j < FN; ++j)
-          acc[i][j] = mma_step<E, FB, FA>(st, fb[hh][j], fa[hh][i], acc[i][j], SCALED ? sc[0][FM + j] : 0, SCALED ? sc[0][i] : 0);
+        for (int j = 0; j < FN; ++j) b[j] = widen_f8<FB>(fb[hh][j][2 * st], fb[hh][j][2 * st + 1], sc[0][FM + j]);
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+          for (int j = 0; j < FN; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(b[j], a[i], acc[i][j], 0, 0, 0);
+      }
+      return;
+    } else {
+#pragma unroll
+      for (int st = 0; st < MMA_STEPS<E>; ++st)  // outermost: consecutive instructions write different blocks
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+          for (int j = 0; j < FN; ++j)
+            acc[i][j] = mma_step<E, FB, FA>(st, fb[hh][j], fa[hh][i], acc[i][j], SCALED ? sc[0][FM + j] : 0, SCALED ? sc[0][i] : 0);
+    }
   };
   // The reads (and loads) of a half go between its first matrix-core
   // instructions: left to itself the compiler puts them behind the last and
@@ -404,6 +447,13 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_kernel(ProductArgs g)
     const int m0 = cur.tm * TM + wm * FM * 32, n0 = cur.tn * TN + wn * FN * 32;
     if constexpr (EPI == Epi::STORE) {
       const int64_t base = cur.batch * g.strideC + cur.split * g.split_stride;
+      const float alpha = g.alpha * (g.alpha_dev ? *g.alpha_dev : 1.f);
+      if (alpha != 1.f) {
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+          for (int j = 0; j < FN; ++j) acc[i][j] *= alpha;
+      }
 #pragma unroll
       for (int i = 0; i < FM; ++i) {
         const int m = m0 + 32 * i + el32;

@@ -59,7 +59,7 @@ Shape plan_shape(int64_t batch, int64_t M, int64_t N, int64_t K, int es, bool ma
 template <Elem E, int FM, int FN, int WM, int WN, int PER_CU, bool AS, bool BS, Epi EPI, int FA, int FB>
 hipError_t launch_tiles(ProductArgs g, int64_t batch, hipStream_t st) {
   constexpr int TM = 32 * FM * WM, TN = 32 * FN * WN;
-  constexpr int LDS = 2 * (TM + TN) * 128 + (E == Elem::F8 ? 16 * (TM + TN) : 0);  // two stages, 4 groups of scales
+  constexpr int LDS = 2 * (TM + TN) * 128 + (E == Elem::F8 || E == Elem::F8W ? 16 * (TM + TN) : 0);  // two stages, 4 groups of scales
   const auto kernel = product_kernel<E, FM, FN, WM, WN, AS, BS, EPI, FA, FB>;
   static bool ready[MAX_DEVICES] = {false};
   int dev = 0, cus = 0;
@@ -99,6 +99,8 @@ struct Out {
   int64_t ldc, strideC;
   int c_dt, vec;
   float beta;
+  float alpha = 1.f;
+  const float* alpha_dev = nullptr;
 };
 void point_output(ProductArgs& g, const Shape& s, const Out& o, float* part, int64_t batch) {
   if (s.splits > 1) {
@@ -108,6 +110,7 @@ void point_output(ProductArgs& g, const Shape& s, const Out& o, float* part, int
     g.split_stride = batch * g.strideC;
     g.c_dt = 0;
     g.vec = g.N % 4 == 0;
+    g.alpha = 1.f;
     g.beta = 0.f;
   } else {
     g.C = o.C;
@@ -115,6 +118,8 @@ void point_output(ProductArgs& g, const Shape& s, const Out& o, float* part, int
     g.strideC = o.strideC;
     g.c_dt = o.c_dt;
     g.vec = o.vec;
+    g.alpha = o.alpha;
+    g.alpha_dev = o.alpha_dev;
     g.beta = o.beta;
   }
 }
@@ -122,7 +127,7 @@ hipError_t sum_splits(const float* part, int splits, int64_t split_stride, const
   const int64_t total = (int64_t)M * N;
   const int64_t gx = std::max<int64_t>(1, std::min<int64_t>((total + 255) / 256, 8192));
   hipLaunchKernelGGL(sum_splits_kernel, dim3((unsigned)gx, (unsigned)batch), dim3(256), 0, st, part, splits, split_stride, o.C, o.ldc,
-                     o.strideC, M, N, o.c_dt, o.beta);
+                     o.strideC, M, N, o.c_dt, o.alpha, o.alpha_dev, o.beta);
   return hipGetLastError();
 }
 hipError_t finish_split(const ProductArgs& g, const Shape& s, const Out& o, const float* part, int64_t batch, hipStream_t st) {
@@ -193,13 +198,22 @@ shampoo_status quantize_f8_impl(const void* x, int x_dt, int64_t n, int64_t rows
   return SHAMPOO_OK;
 }
 
+template <Elem E>
+static hipError_t launch_f8(const ProductArgs& g, int a_dt, int b_dt, bool large, int64_t n, hipStream_t st) {
+  const bool a5 = a_dt == SHAMPOO_E5M2, b5 = b_dt == SHAMPOO_E5M2;
+  if (!a5 && !b5) return launch_product<E, false, false, Epi::STORE, 0, 0>(g, large, n, st);
+  if (!b5) return launch_product<E, false, false, Epi::STORE, 1, 0>(g, large, n, st);
+  if (!a5) return launch_product<E, false, false, Epi::STORE, 0, 1>(g, large, n, st);
+  return launch_product<E, false, false, Epi::STORE, 1, 1>(g, large, n, st);
+}
+
 size_t matmul_f8_bytes(int64_t n, int64_t M, int64_t N, int64_t K) {
   if (n == 0 || M == 0 || N == 0) return 0;
   return partial_bytes(plan_shape(n, M, N, K, 1, true), n, M, N);
 }
 
 shampoo_status matmul_f8_impl(const void* a, int a_dt, const void* sa, int32_t arb, const void* b, int b_dt, const void* sb, int32_t brb,
-                              int64_t n, int64_t M, int64_t N, int64_t K, void* c, int c_dt, void* ws, size_t ws_bytes, hipStream_t st) {
+                              int64_t n, int64_t M, int64_t N, int64_t K, void* c, int c_dt, bool exact, void* ws, size_t ws_bytes, hipStream_t st) {
   shampoo_status r = check_f8_sizes(n, M, N, K);
   if (r != SHAMPOO_OK) return r;
   for (int dt : {a_dt, b_dt})
@@ -228,11 +242,10 @@ shampoo_status matmul_f8_impl(const void* a, int a_dt, const void* sa, int32_t a
   set_shape(g, s);
   const Out o{c, N, M * N, out_code(c_dt), rows_vec(c, N, n > 1 ? M * N : 0, c_dt), 0.f};
   point_output(g, s, o, (float*)ws, n);
-  const bool a5 = a_dt == SHAMPOO_E5M2, b5 = b_dt == SHAMPOO_E5M2;
-  if (!a5 && !b5) HIP_TRY((launch_product<Elem::F8, false, false, Epi::STORE, 0, 0>(g, s.large, n, st)));
-  else if (a5 && !b5) HIP_TRY((launch_product<Elem::F8, false, false, Epi::STORE, 1, 0>(g, s.large, n, st)));
-  else if (!a5) HIP_TRY((launch_product<Elem::F8, false, false, Epi::STORE, 0, 1>(g, s.large, n, st)));
-  else HIP_TRY((launch_product<Elem::F8, false, false, Epi::STORE, 1, 1>(g, s.large, n, st)));
+  // float32 results take the exact form, unless the caller's own rounding is
+  // coarser anyway
+  HIP_TRY(exact && c_dt == SHAMPOO_F32 ? launch_f8<Elem::F8W>(g, a_dt, b_dt, s.large, n, st)
+                                       : launch_f8<Elem::F8>(g, a_dt, b_dt, s.large, n, st));
   HIP_TRY(finish_split(g, s, o, (const float*)ws, n, st));
   return SHAMPOO_OK;
 }
@@ -351,7 +364,8 @@ shampoo_status run_xent(const shampoo_xent_args* a, const XentLayout& L, hipStre
     LAUNCH_CHECK("xent_count");
   }
   const Out dw{a->dweight, a->ld_dweight, 0, out_code(a->dweight_dt),
-               a->dweight ? rows_vec(a->dweight, a->ld_dweight, 0, a->dweight_dt) : 0, a->accumulate ? 1.f : 0.f};
+               a->dweight ? rows_vec(a->dweight, a->ld_dweight, 0, a->dweight_dt) : 0, a->accumulate ? 1.f : 0.f,
+               a->scale, mean ? inv_count : nullptr};
   const Out dw32{w + L.dw, d, 0, 0, d % 4 == 0, 0.f};
   for (int64_t r0 = 0; r0 < N; r0 += L.panel) {
     const int64_t M = std::min(L.panel, N - r0);
@@ -372,13 +386,13 @@ shampoo_status run_xent(const shampoo_xent_args* a, const XentLayout& L, hipStre
     LAUNCH_CHECK("xent_rows");
     if (!L.grads) continue;
     GradArgs ga{w + L.E, L.ldE, (const floatx2_t*)stats, logit, lse, a->targets + r0, a->row_scale ? a->row_scale + r0 : nullptr,
-                mean ? inv_count : nullptr, a->ignore_index, (int)M, (int)V, (int)L.pieces, a->scale};
+                a->ignore_index, (int)M, (int)V, (int)L.pieces};
     hipLaunchKernelGGL((xent_grad_kernel<TE>), dim3((unsigned)((L.ldE + 2047) / 2048), (unsigned)((M + 3) / 4)), dim3(256), 0, st, ga);
     LAUNCH_CHECK("xent_grad");
     float* part = (float*)(w + L.part);
     if (a->dhidden) {
       unsigned char* C = (unsigned char*)a->dhidden + r0 * a->ld_dhidden * es;
-      const Out o{C, a->ld_dhidden, 0, out_code(a->dt), rows_vec(C, a->ld_dhidden, 0, a->dt), 0.f};
+      const Out o{C, a->ld_dhidden, 0, out_code(a->dt), rows_vec(C, a->ld_dhidden, 0, a->dt), 0.f, a->scale, mean ? inv_count : nullptr};
       // a shorter last panel keeps the full panel's split, which the workspace holds
       const Shape s = L.dx;
       ProductArgs p{};
@@ -430,7 +444,7 @@ shampoo_status shampoo_matmul_f8_workspace(int64_t n, int64_t M, int64_t N, int6
 shampoo_status shampoo_matmul_f8(const void* a, shampoo_dtype a_dt, const void* a_scale, int32_t a_block_rows, const void* b,
                                  shampoo_dtype b_dt, const void* b_scale, int32_t b_block_rows, int64_t n, int64_t M, int64_t N,
                                  int64_t K, void* c, shampoo_dtype c_dt, void* ws, size_t ws_bytes, hipStream_t stream) {
-  return matmul_f8_impl(a, a_dt, a_scale, a_block_rows, b, b_dt, b_scale, b_block_rows, n, M, N, K, c, c_dt, ws, ws_bytes, stream);
+  return matmul_f8_impl(a, a_dt, a_scale, a_block_rows, b, b_dt, b_scale, b_block_rows, n, M, N, K, c, c_dt, true, ws, ws_bytes, stream);
 }
 
 shampoo_status shampoo_linear_xent_workspace(const shampoo_xent_args* args, size_t* bytes) {

@@ -142,10 +142,8 @@ struct GradArgs {
   const float* lse;
   const int64_t* targets;
   const float* row_scale;
-  const float* inv_count;     // or null
   int64_t ignore;
   int M, V, pieces;
-  float scale;
 };
 
 // P from E, in place: a workgroup of 4 waves takes 4 rows x 2048 columns,
@@ -157,7 +155,9 @@ __global__ __launch_bounds__(256) void xent_grad_kernel(GradArgs g) {
   if (m >= g.M) return;
   const int64_t t = g.targets[m];
   const bool skip = t == g.ignore, bad = !skip && (t < 0 || t >= g.V);
-  float w = g.scale * (g.row_scale ? g.row_scale[m] : 1.f) * (g.inv_count ? *g.inv_count : 1.f);
+  // 1 / count and the caller's scale wait for the products' float32 results:
+  // here they would round every -1 of an unlikely target the same way
+  float w = g.row_scale ? g.row_scale[m] : 1.f;
   if (bad) w = __builtin_nanf("");
   const float lse = g.lse[m];
   T* row = reinterpret_cast<T*>(g.E) + (int64_t)m * g.ld;
@@ -179,9 +179,10 @@ __global__ __launch_bounds__(256) void xent_grad_kernel(GradArgs g) {
         // a piece of nothing (maximum -inf) holds zeros
         y = y == 0.f ? (f == f ? 0.f : f) : y * f;
         if (c + e == t) {
-          // p_t - 1 from the float32 logit: the rounded exponential would
-          // lose it where p_t is near one
-          y = w * expm1f(g.target_logit[m] - lse);
+          // p_t - 1; from the float32 logit where the exponential is rounded,
+          // which would lose it where p_t is near one
+          if constexpr (sizeof(T) == 4) y -= w;
+          else y = w * expm1f(g.target_logit[m] - lse);
         }
         if (c + e >= g.V) y = 0.f;
         if constexpr (sizeof(T) == 4) p.v[e] = y;
@@ -193,18 +194,20 @@ __global__ __launch_bounds__(256) void xent_grad_kernel(GradArgs g) {
   }
 }
 
-// C = sum of `splits` float32 partial results (+ beta C), any output type
+// C = alpha x the sum of `splits` float32 partial results (+ beta C), any output type
 // (0 float32, 1 half, 2 bfloat16); rows of N elements, ldc apart, batches
 // of M rows
 __global__ __launch_bounds__(256) void sum_splits_kernel(const float* __restrict__ part, int splits, int64_t split_stride,
                                                          void* __restrict__ C, int64_t ldc, int64_t strideC, int M, int N,
-                                                         int c_dt, float beta) {
+                                                         int c_dt, float alpha, const float* __restrict__ alpha_dev, float beta) {
+  if (alpha_dev) alpha *= *alpha_dev;
   const int64_t total = (int64_t)M * N;
   const int64_t b = blockIdx.y;
   for (int64_t i = blockIdx.x * (int64_t)256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
     float a = 0.f;
     const float* p = part + b * total + i;
     for (int s = 0; s < splits; ++s) a += p[s * split_stride];
+    a *= alpha;
     const int64_t m = i / N, at = b * strideC + m * ldc + (i - m * N);
     if (c_dt == 0) {
       float* o = reinterpret_cast<float*>(C) + at;
