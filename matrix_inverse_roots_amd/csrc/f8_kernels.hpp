@@ -44,8 +44,9 @@ __device__ __forceinline__ uint32_t finite_bits(float v) {
 // 2^-e from the scale byte (e <= 120, so the exponent field is at least 7)
 __device__ __forceinline__ float inverse_scale(int byte) { return __builtin_bit_cast(float, (uint32_t)(254 - byte) << 23); }
 
-// four finite values, already scaled, as four bytes: the conversion
-// instructions round to nearest even
+// four values, already scaled, as four bytes: the conversion instructions
+// round to nearest even, keep NaN, and turn an infinity into e5m2's infinity
+// or e4m3's NaN
 template <int FMT> __device__ __forceinline__ uint32_t to_f8x4(float a, float b, float c, float d) {
   uint32_t r = 0;
   if constexpr (FMT == 0) {
@@ -57,14 +58,6 @@ template <int FMT> __device__ __forceinline__ uint32_t to_f8x4(float a, float b,
   }
   return r;
 }
-// the byte of a value that is not finite, put in by hand
-template <int FMT> __device__ __forceinline__ uint32_t fix_f8(uint32_t word, int byte, float v) {
-  const uint32_t bits = __builtin_bit_cast(uint32_t, v), mag = bits & 0x7fffffffu;
-  if (mag < 0x7f800000u) return word;
-  const uint32_t code = ((bits >> 24) & 0x80u) | (FMT == 1 && mag == 0x7f800000u ? 0x7cu : 0x7fu);
-  return (word & ~(0xffu << (8 * byte))) | (code << (8 * byte));
-}
-
 template <typename T> __device__ __forceinline__ float wide(T v) { return (float)v; }
 template <> __device__ __forceinline__ float wide<uint16_t>(uint16_t v) { return __builtin_bit_cast(float, (uint32_t)v << 16); }
 
@@ -118,17 +111,21 @@ __global__ __launch_bounds__(256) void quantize_tile_kernel(QuantArgs g) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) raw = max(raw, __builtin_bit_cast(uint32_t, v[r][i]) & 0x7fffffffu);
   const bool odd = __any(raw >= 0x7f800000u);
+  auto maxima = [&](auto bits) {
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    uint32_t a = 0, b = 0;
+    for (int k = 0; k < 8; ++k) {
+      uint32_t a = 0, b = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      a = max(a, odd ? finite_bits(v[k][i]) : __builtin_bit_cast(uint32_t, v[k][i]) & 0x7fffffffu);
-      b = max(b, odd ? finite_bits(v[i][k]) : __builtin_bit_cast(uint32_t, v[i][k]) & 0x7fffffffu);
+      for (int i = 0; i < 8; ++i) {
+        a = max(a, bits(v[k][i]));
+        b = max(b, bits(v[i][k]));
+      }
+      row_max[k] = a;
+      col_max[k] = b;
     }
-    row_max[k] = a;
-    col_max[k] = b;
-  }
+  };
+  if (odd) maxima([](float f) { return finite_bits(f); });
+  else maxima([](float f) { return __builtin_bit_cast(uint32_t, f) & 0x7fffffffu; });
   auto over = [](uint32_t a, int d) { return max(a, (uint32_t)__shfl_xor((int)a, d)); };
   uint32_t tile_max = 0;
   if constexpr (RB == 128) {
@@ -156,10 +153,6 @@ __global__ __launch_bounds__(256) void quantize_tile_kernel(QuantArgs g) {
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         uint32_t w = to_f8x4<FMT>(v[r][4 * k] * inv, v[r][4 * k + 1] * inv, v[r][4 * k + 2] * inv, v[r][4 * k + 3] * inv);
-        if (odd) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) w = fix_f8<FMT>(w, e, v[r][4 * k + e]);
-        }
         o[k] = w;
       }
       if (row1 + r < g.rows) {
@@ -196,10 +189,6 @@ __global__ __launch_bounds__(256) void quantize_tile_kernel(QuantArgs g) {
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         uint32_t w = to_f8x4<FMT>(v[4 * k][c] * inv, v[4 * k + 1][c] * inv, v[4 * k + 2][c] * inv, v[4 * k + 3][c] * inv);
-        if (odd) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) w = fix_f8<FMT>(w, e, v[4 * k + e][c]);
-        }
         o[k] = w;
       }
       // rows of 128 bytes, run rg of transposed row 8 cg + c at rg ^ 2 (cg % 8)
