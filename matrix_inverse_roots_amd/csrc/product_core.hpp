@@ -387,12 +387,15 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_kernel(ProductArgs g)
   constexpr int NMMA = FM * FN * MMA_STEPS<E>;
   constexpr int NREAD = FM * (AS ? 4 : 2) + FN * (BS ? 4 : 2) + (SCALED ? FM + FN : 0);
   constexpr int STEPS = NMMA * 3 / 4 < 16 ? NMMA * 3 / 4 : 16, RPS = (NREAD + STEPS - 1) / STEPS;
+  // loads over the whole half: a compute unit takes 16 cycles for each, and a
+  // wave that meets a full queue stalls with its matrix-core instructions
+  constexpr int LGAP = NMMA >= 2 * (NIA + NIB) ? NMMA / (NIA + NIB) : 1;
   auto interleave = [&](bool loads) {
 #pragma unroll
-    for (int k = 0; k < STEPS; ++k) {
+    for (int k = 0; k < (NMMA < 64 ? NMMA : 64); ++k) {
       __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-      __builtin_amdgcn_sched_group_barrier(0x100, RPS, 0);
-      if (loads && k < NIA + NIB) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+      if (k < STEPS) __builtin_amdgcn_sched_group_barrier(0x100, RPS, 0);
+      if (loads && k % LGAP == 0 && k / LGAP < NIA + NIB) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
     }
   };
   begin_loads();
