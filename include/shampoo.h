@@ -503,9 +503,14 @@ typedef enum shampoo_reduction {
   SHAMPOO_REDUCE_MEAN = 2
 } shampoo_reduction;
 
-/* dt: F32 or BF16, the type of hidden, weight and dhidden; ld_*: elements
- * between rows.  Products run on that type's matrix cores and sum in float32;
+/* dt: F32 or BF16, the type of hidden and dhidden; weight_dt: dt, or F32
+ * beside BF16 (the weight is then rounded to bfloat16 in the workspace: an
+ * optimizer's float32 parameter); ld_*: elements between rows.  Products run on that type's matrix cores and sum in float32;
  * for BF16 the softmax enters the gradients' products rounded to bfloat16.
+ * logits_dt: dt, or E4M3 beside BF16: hidden and weight are quantised as
+ * shampoo_quantize_f8 does (a scale for each 128 entries of a row) and the
+ * logits are their 8-bit product; the softmax and its gradient are those of
+ * these logits, the gradients' products run on the bfloat16 operands.
  * dhidden, dweight: null for no gradient.  dweight_dt: BF16 or F32
  * (F32 only for dt F32); accumulate: dweight += instead of =.
  * lse: float32 [N], the rows' log sum exp, or null.
@@ -528,7 +533,9 @@ typedef struct shampoo_xent_args {
   int64_t ignore_index;
   int64_t panel_rows;
   shampoo_dtype dt;
+  shampoo_dtype weight_dt;
   shampoo_dtype dweight_dt;
+  shampoo_dtype logits_dt;
   int32_t reduction;
   int32_t accumulate;
   float scale;

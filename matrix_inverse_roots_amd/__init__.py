@@ -99,7 +99,8 @@ class XentArgsC(ctypes.Structure):
                 ("ld_dhidden", ctypes.c_int64), ("ld_dweight", ctypes.c_int64),
                 ("N", ctypes.c_int64), ("V", ctypes.c_int64), ("d", ctypes.c_int64),
                 ("ignore_index", ctypes.c_int64), ("panel_rows", ctypes.c_int64),
-                ("dt", ctypes.c_int32), ("dweight_dt", ctypes.c_int32), ("reduction", ctypes.c_int32),
+                ("dt", ctypes.c_int32), ("weight_dt", ctypes.c_int32), ("dweight_dt", ctypes.c_int32),
+                ("logits_dt", ctypes.c_int32), ("reduction", ctypes.c_int32),
                 ("accumulate", ctypes.c_int32), ("scale", ctypes.c_float),
                 ("ws", ctypes.c_void_p), ("ws_bytes", ctypes.c_size_t)]
 
@@ -548,7 +549,7 @@ def _rows2d(t, name, shape, dtypes):
 
 
 def _xent_args(hidden, weight, targets, loss, lse, dhidden, dweight, row_scale, ignore_index, reduction, scale, accumulate,
-               panel_rows):
+               panel_rows, logits_dtype=None):
     torch = _torch()
     if reduction not in REDUCTIONS:
         raise ValueError("reduction must be one of %s" % sorted(REDUCTIONS))
@@ -559,7 +560,7 @@ def _xent_args(hidden, weight, targets, loss, lse, dhidden, dweight, row_scale, 
     if hidden.dtype not in (torch.float32, torch.bfloat16):
         raise TypeError("unsupported dtype %s (float32, bfloat16)" % hidden.dtype)
     ldh = _rows2d(hidden, "hidden", (N, d), (hidden.dtype,))
-    ldw = _rows2d(weight, "weight", (V, d), (hidden.dtype,))
+    ldw = _rows2d(weight, "weight", (V, d), (hidden.dtype, torch.float32))
     lddh = _rows2d(dhidden, "dhidden", (N, d), (hidden.dtype,))
     lddw = _rows2d(dweight, "dweight", (V, d), (hidden.dtype, torch.float32))
     for t, name, dtype in ((targets, "targets", torch.int64), (row_scale, "row_scale", torch.float32),
@@ -570,43 +571,54 @@ def _xent_args(hidden, weight, targets, loss, lse, dhidden, dweight, row_scale, 
     if loss is not None and (loss.dtype != torch.float32 or tuple(loss.shape) != shape or not loss.is_contiguous()):
         raise ValueError("loss must be a contiguous float32 tensor of shape %s" % (shape,))
 
+    if logits_dtype not in (None, hidden.dtype, torch.float8_e4m3fn):
+        raise ValueError("logits_dtype must be None, hidden's dtype or torch.float8_e4m3fn")
+    if logits_dtype == torch.float8_e4m3fn and hidden.dtype != torch.bfloat16:
+        raise ValueError("8-bit logits need bfloat16 hidden")
+
     def at(t):
         return None if t is None else t.data_ptr()
 
     return XentArgsC(at(hidden), at(weight), at(targets), at(row_scale), at(loss), at(lse), at(dhidden), at(dweight),
                      max(ldh, d), max(ldw, d), max(lddh, d), max(lddw, d), N, V, d, int(ignore_index), int(panel_rows),
-                     _dtype_code(hidden), _dtype_code(dweight) if dweight is not None else _dtype_code(hidden),
+                     _dtype_code(hidden), _dtype_code(weight), _dtype_code(dweight) if dweight is not None else _dtype_code(hidden),
+                     E4M3 if logits_dtype == torch.float8_e4m3fn else _dtype_code(hidden),
                      REDUCTIONS[reduction], 1 if accumulate else 0, float(scale), None, 0)
 
 
-def shampoo_linear_xent_workspace(hidden, weight, targets, dhidden=None, dweight=None, panel_rows=0):
+def shampoo_linear_xent_workspace(hidden, weight, targets, dhidden=None, dweight=None, panel_rows=0, logits_dtype=None):
     """Workspace bytes of ``shampoo_linear_xent`` with these tensors."""
     b = ctypes.c_size_t(0)
-    args = _xent_args(hidden, weight, targets, None, None, dhidden, dweight, None, -100, "mean", 1.0, False, panel_rows)
+    args = _xent_args(hidden, weight, targets, None, None, dhidden, dweight, None, -100, "mean", 1.0, False, panel_rows,
+                      logits_dtype)
     _check(lib.shampoo_linear_xent_workspace(ctypes.byref(args), ctypes.byref(b)))
     return b.value
 
 
 def shampoo_linear_xent(hidden, weight, targets, loss=None, lse=None, dhidden=None, dweight=None, row_scale=None,
-                        ignore_index=-100, reduction="mean", scale=1.0, accumulate=False, panel_rows=0, ws=None,
-                        stream=None):
+                        ignore_index=-100, reduction="mean", scale=1.0, accumulate=False, panel_rows=0, logits_dtype=None,
+                        ws=None, stream=None):
     """Softmax cross entropy of the projection hidden weight^T against
     ``targets``, without keeping its logits; returns the loss.
 
     hidden [N, d] and weight [V, d] (float32 or bfloat16, unit column
-    stride), targets int64 [N]; rows with target ``ignore_index`` count for
+    stride; a float32 weight beside bfloat16 hidden is rounded to bfloat16),
+    targets int64 [N]; rows with target ``ignore_index`` count for
     nothing.  reduction: "mean" over the other rows, "sum" or "none".
     row_scale float32 [N] and scale multiply each row's loss.  dhidden, dweight:
     tensors that receive the gradients of the (summed) loss; dweight may be
     float32 beside bfloat16 inputs, and accumulate=True adds to it.  lse:
     receives log sum exp of each row.  panel_rows bounds the rows whose
-    exponentials the workspace holds at a time (0: up to 2 GiB of them)."""
+    exponentials the workspace holds at a time (0: up to 2 GiB of them).
+    logits_dtype=torch.float8_e4m3fn (bfloat16 hidden only) quantises hidden
+    and weight as ``shampoo_quantize_f8`` does and takes the logits from their
+    8-bit product; the gradients' products stay in bfloat16."""
     torch = _torch()
     dev = _on_device(hidden, weight, targets, loss, lse, dhidden, dweight, row_scale, ws)
     if loss is None:
         loss = torch.empty((hidden.shape[0],) if reduction == "none" else (), dtype=torch.float32, device=dev)
     args = _xent_args(hidden, weight, targets, loss, lse, dhidden, dweight, row_scale, ignore_index, reduction, scale,
-                      accumulate, panel_rows)
+                      accumulate, panel_rows, logits_dtype)
     if ws is None:
         b = ctypes.c_size_t(0)
         _check(lib.shampoo_linear_xent_workspace(ctypes.byref(args), ctypes.byref(b)))

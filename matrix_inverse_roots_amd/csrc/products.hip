@@ -9,7 +9,6 @@
 #include "f8_kernels.hpp"
 #include "host_common.hpp"
 #include "product_core.hpp"
-#include "products.hpp"
 #include "shampoo.h"
 #include "xent_kernels.hpp"
 
@@ -154,10 +153,6 @@ shampoo_status check_f8_sizes(int64_t n, int64_t M, int64_t N, int64_t K) {
   return SHAMPOO_OK;
 }
 
-}  // namespace
-
-namespace shampoo {
-
 shampoo_status quantize_f8_impl(const void* x, int x_dt, int64_t n, int64_t rows, int64_t cols, int64_t ld, int64_t stride, int fmt,
                                 int32_t block_rows, void* q, void* s, void* qt, void* st_, hipStream_t st) {
   if (n < 0 || rows < 0 || cols < 0) return fail(SHAMPOO_E_INVALID, "negative size");
@@ -199,7 +194,7 @@ shampoo_status quantize_f8_impl(const void* x, int x_dt, int64_t n, int64_t rows
 }
 
 template <Elem E>
-static hipError_t launch_f8(const ProductArgs& g, int a_dt, int b_dt, bool large, int64_t n, hipStream_t st) {
+hipError_t launch_f8(const ProductArgs& g, int a_dt, int b_dt, bool large, int64_t n, hipStream_t st) {
   const bool a5 = a_dt == SHAMPOO_E5M2, b5 = b_dt == SHAMPOO_E5M2;
   if (!a5 && !b5) return launch_product<E, false, false, Epi::STORE, 0, 0>(g, large, n, st);
   if (!b5) return launch_product<E, false, false, Epi::STORE, 1, 0>(g, large, n, st);
@@ -213,7 +208,7 @@ size_t matmul_f8_bytes(int64_t n, int64_t M, int64_t N, int64_t K) {
 }
 
 shampoo_status matmul_f8_impl(const void* a, int a_dt, const void* sa, int32_t arb, const void* b, int b_dt, const void* sb, int32_t brb,
-                              int64_t n, int64_t M, int64_t N, int64_t K, void* c, int c_dt, bool exact, void* ws, size_t ws_bytes, hipStream_t st) {
+                              int64_t n, int64_t M, int64_t N, int64_t K, void* c, int c_dt, void* ws, size_t ws_bytes, hipStream_t st) {
   shampoo_status r = check_f8_sizes(n, M, N, K);
   if (r != SHAMPOO_OK) return r;
   for (int dt : {a_dt, b_dt})
@@ -242,17 +237,11 @@ shampoo_status matmul_f8_impl(const void* a, int a_dt, const void* sa, int32_t a
   set_shape(g, s);
   const Out o{c, N, M * N, out_code(c_dt), rows_vec(c, N, n > 1 ? M * N : 0, c_dt), 0.f};
   point_output(g, s, o, (float*)ws, n);
-  // float32 results take the exact form, unless the caller's own rounding is
-  // coarser anyway
-  HIP_TRY(exact && c_dt == SHAMPOO_F32 ? launch_f8<Elem::F8W>(g, a_dt, b_dt, s.large, n, st)
-                                       : launch_f8<Elem::F8>(g, a_dt, b_dt, s.large, n, st));
+  HIP_TRY(c_dt == SHAMPOO_F32 ? launch_f8<Elem::F8W>(g, a_dt, b_dt, s.large, n, st)
+                              : launch_f8<Elem::F8>(g, a_dt, b_dt, s.large, n, st));
   HIP_TRY(finish_split(g, s, o, (const float*)ws, n, st));
   return SHAMPOO_OK;
 }
-
-}  // namespace shampoo
-
-namespace {
 
 // ---------------------------------------------------------------------------
 // softmax cross entropy
@@ -263,9 +252,10 @@ constexpr int64_t XENT_STATS_BYTES = int64_t(1) << 28;
 
 struct XentLayout {
   int64_t panel, pieces, ldE, dp;
-  bool grads, copy_hidden, copy_weight, dw_sum;  // dw_sum: float32 sum of the panels' bfloat16 gradients
-  size_t count, stats, logit, lse, rows, E, hidden, weight, part, dw, total;
-  Shape logits, dx, dwp;
+  int64_t Kp, Ks;  // 8-bit logits: padded width, scales of a row
+  bool f8, grads, copy_hidden, copy_weight, dw_sum;  // dw_sum: float32 sum of the panels' bfloat16 gradients
+  size_t count, stats, logit, lse, rows, E, hidden, weight, hq, hs, wq, wsc, part, dw, total;
+  Shape dx, dwp;
 };
 
 int64_t row_elems(int dt) { return dt == SHAMPOO_F32 ? 4 : 8; }
@@ -274,10 +264,14 @@ shampoo_status xent_layout(const shampoo_xent_args* a, XentLayout* L) {
   if (!a) return fail(SHAMPOO_E_INVALID, "null arguments");
   if (a->N < 0 || a->V < 1 || a->d < 1) return fail(SHAMPOO_E_INVALID, "N = %lld, V = %lld, d = %lld", (long long)a->N, (long long)a->V, (long long)a->d);
   if (a->dt != SHAMPOO_F32 && a->dt != SHAMPOO_BF16) return fail(SHAMPOO_E_UNSUPPORTED, "dtype %d (F32, BF16)", (int)a->dt);
+  if (a->weight_dt != a->dt && a->weight_dt != SHAMPOO_F32)
+    return fail(SHAMPOO_E_UNSUPPORTED, "weight dtype %d for dtype %d", (int)a->weight_dt, (int)a->dt);
+  if (a->logits_dt != a->dt && !(a->logits_dt == SHAMPOO_E4M3 && a->dt == SHAMPOO_BF16))
+    return fail(SHAMPOO_E_UNSUPPORTED, "logits dtype %d for dtype %d", (int)a->logits_dt, (int)a->dt);
   if (a->dweight && a->dweight_dt != SHAMPOO_F32 && !(a->dweight_dt == SHAMPOO_BF16 && a->dt == SHAMPOO_BF16))
     return fail(SHAMPOO_E_UNSUPPORTED, "weight gradient dtype %d for dtype %d", (int)a->dweight_dt, (int)a->dt);
   if (a->reduction < 0 || a->reduction > 2) return fail(SHAMPOO_E_INVALID, "reduction %d", a->reduction);
-  if (a->N > INT32_MAX / 4 || a->V > XENT_MAX_ROW || a->d > XENT_MAX_ROW / 4 || a->ld_hidden > XENT_MAX_ROW || a->ld_weight > XENT_MAX_ROW)
+  if (a->N > (a->logits_dt == SHAMPOO_E4M3 ? F8_MAX : INT32_MAX / 4) || a->V > XENT_MAX_ROW || a->d > XENT_MAX_ROW / 4 || a->ld_hidden > XENT_MAX_ROW || a->ld_weight > XENT_MAX_ROW)
     return fail(SHAMPOO_E_UNSUPPORTED, "N = %lld, V = %lld, d = %lld too large", (long long)a->N, (long long)a->V, (long long)a->d);
   if (a->panel_rows < 0) return fail(SHAMPOO_E_INVALID, "panel_rows < 0");
   const int64_t es = a->dt == SHAMPOO_F32 ? 4 : 2, ve = row_elems(a->dt);
@@ -294,11 +288,14 @@ shampoo_status xent_layout(const shampoo_xent_args* a, XentLayout* L) {
   L->panel = std::max<int64_t>(std::min(rows, a->N), 1);
   // the products read 16-byte runs of rows: others are copied into rows that
   // start on 16 bytes
-  L->dp = up(a->d, ve);
-  L->copy_hidden = a->d % ve || a->ld_hidden % ve || !aligned(a->hidden, 16);
-  L->copy_weight = a->d % ve || a->ld_weight % ve || !aligned(a->weight, 16);
+  L->dp = up(a->d, 8);
+  L->f8 = a->logits_dt == SHAMPOO_E4M3;
+  L->Kp = up(a->d, 128);
+  L->Ks = up(L->Kp / 128, 4);
+  const bool needed = L->grads || !L->f8;
+  L->copy_hidden = needed && (a->d % ve || a->ld_hidden % ve || !aligned(a->hidden, 16));
+  L->copy_weight = needed && (a->weight_dt != a->dt || a->d % ve || a->ld_weight % ve || !aligned(a->weight, 16));
   L->dw_sum = a->dweight && a->dweight_dt == SHAMPOO_BF16 && L->panel < a->N;
-  L->logits = plan_shape(1, L->panel, a->V, a->d, (int)es, false);
   L->dx = plan_shape(1, L->panel, a->d, a->V, (int)es, true);
   L->dwp = plan_shape(1, a->V, a->d, L->panel, (int)es, true);
   size_t at = 0;
@@ -315,6 +312,10 @@ shampoo_status xent_layout(const shampoo_xent_args* a, XentLayout* L) {
   L->E = take(L->grads ? (size_t)L->panel * L->ldE * es : 0);
   L->hidden = take(L->copy_hidden ? (size_t)a->N * L->dp * es : 0);
   L->weight = take(L->copy_weight ? (size_t)a->V * L->dp * es : 0);
+  L->hq = take(L->f8 ? a->N * L->Kp : 0);
+  L->hs = take(L->f8 ? a->N * L->Ks : 0);
+  L->wq = take(L->f8 ? a->V * L->Kp : 0);
+  L->wsc = take(L->f8 ? a->V * L->Ks : 0);
   size_t part = 0;
   if (a->dhidden) part = std::max(part, partial_bytes(L->dx, 1, L->panel, a->d));
   if (a->dweight) part = std::max(part, partial_bytes(L->dwp, 1, a->V, a->d));
@@ -344,20 +345,30 @@ shampoo_status run_xent(const shampoo_xent_args* a, const XentLayout& L, hipStre
   const unsigned char* hidden = (const unsigned char*)a->hidden;
   const unsigned char* weight = (const unsigned char*)a->weight;
   int64_t ldh = a->ld_hidden, ldw = a->ld_weight;
-  auto pad = [&](const unsigned char* from, int64_t ld, int64_t count, unsigned char* to) -> hipError_t {
-    const int64_t wgs = std::max<int64_t>(1, std::min<int64_t>((count * L.dp + 255) / 256, 16384));
-    hipLaunchKernelGGL((pad_rows_kernel<T>), dim3((unsigned)wgs), dim3(256), 0, st, (const T*)from, ld, count, (int)d, (T*)to, (int)L.dp);
+  auto pad = [&](const void* from, int dt, int64_t ld, int64_t count, unsigned char* to) -> hipError_t {
+    const int wgs = (int)std::max<int64_t>(1, std::min<int64_t>((count + 3) / 4, 8192));
+    const int vec = ld % 4 == 0 && aligned(from, 4 * size_of(dt));
+    if (sizeof(T) == 2 && dt == SHAMPOO_F32)
+      hipLaunchKernelGGL((pad_rows_kernel<float, T>), dim3(wgs), dim3(256), 0, st, (const float*)from, ld, count, (int)d, (T*)to, (int)L.dp, vec);
+    else
+      hipLaunchKernelGGL((pad_rows_kernel<T, T>), dim3(wgs), dim3(256), 0, st, (const T*)from, ld, count, (int)d, (T*)to, (int)L.dp, vec);
     return hipGetLastError();
   };
   if (N > 0 && L.copy_hidden) {
-    HIP_TRY(pad(hidden, ldh, N, w + L.hidden));
+    HIP_TRY(pad(a->hidden, a->dt, ldh, N, w + L.hidden));
     hidden = w + L.hidden;
     ldh = L.dp;
   }
   if (N > 0 && L.copy_weight) {
-    HIP_TRY(pad(weight, ldw, V, w + L.weight));
+    HIP_TRY(pad(a->weight, a->weight_dt, ldw, V, w + L.weight));
     weight = w + L.weight;
     ldw = L.dp;
+  }
+  if (N > 0 && L.f8) {
+    shampoo_status r = quantize_f8_impl(a->hidden, a->dt, 1, N, d, a->ld_hidden, 0, SHAMPOO_E4M3, 1, w + L.hq, w + L.hs, nullptr, nullptr, st);
+    if (r == SHAMPOO_OK)
+      r = quantize_f8_impl(a->weight, a->weight_dt, 1, V, d, a->ld_weight, 0, SHAMPOO_E4M3, 1, w + L.wq, w + L.wsc, nullptr, nullptr, st);
+    if (r != SHAMPOO_OK) return r;
   }
   if (mean) {
     hipLaunchKernelGGL(xent_count_kernel, dim3(1), dim3(1024), 0, st, a->targets, (int)N, a->ignore_index, inv_count);
@@ -377,12 +388,22 @@ shampoo_status run_xent(const shampoo_xent_args* a, const XentLayout& L, hipStre
     g.C = L.grads ? w + L.E : nullptr;
     g.ldc = L.ldE;
     g.stats = stats;
-    HIP_TRY((product<E, false, false, Epi::SOFTMAX>(g, plan_shape(1, M, V, d, (int)es, false), st)));
+    if (L.f8) {
+      g.A = w + L.hq + r0 * L.Kp; g.sa = w + L.hs + r0 * L.Ks;
+      g.B = w + L.wq; g.sb = w + L.wsc;
+      g.lda = g.ldb = L.Kp;
+      g.ldsa = g.ldsb = L.Ks;
+      g.K = (int)L.Kp;
+      HIP_TRY((product<Elem::F8, false, false, Epi::SOFTMAX>(g, plan_shape(1, M, V, L.Kp, 1, false), st)));
+    } else {
+      HIP_TRY((product<E, false, false, Epi::SOFTMAX>(g, plan_shape(1, M, V, d, (int)es, false), st)));
+    }
     float* lse = a->lse ? a->lse + r0 : (float*)(w + L.lse);
-    RowArgs ra{(const floatx2_t*)stats, g.A, weight, ldh, ldw, (int)d, logit, a->targets + r0, a->row_scale ? a->row_scale + r0 : nullptr, lse, rows + r0,
+    RowArgs ra{(const floatx2_t*)stats, g.A, g.B, g.lda, g.ldb, g.sa, g.sb, L.Ks, g.K, logit, a->targets + r0, a->row_scale ? a->row_scale + r0 : nullptr, lse, rows + r0,
                a->ignore_index, (int)M, (int)V, (int)L.pieces, a->scale};
-    if (M <= 256) hipLaunchKernelGGL((xent_rows_kernel<1, TE>), dim3((unsigned)M), dim3(1024), 0, st, ra);
-    else hipLaunchKernelGGL((xent_rows_kernel<32, TE>), dim3((unsigned)((M + 31) / 32)), dim3(1024), 0, st, ra);
+    const auto rows_kernel = L.f8 ? (M <= 256 ? xent_rows_kernel<1, uint8_t> : xent_rows_kernel<32, uint8_t>)
+                                  : (M <= 256 ? xent_rows_kernel<1, TE> : xent_rows_kernel<32, TE>);
+    hipLaunchKernelGGL(rows_kernel, dim3((unsigned)(M <= 256 ? M : (M + 31) / 32)), dim3(1024), 0, st, ra);
     LAUNCH_CHECK("xent_rows");
     if (!L.grads) continue;
     GradArgs ga{w + L.E, L.ldE, (const floatx2_t*)stats, logit, lse, a->targets + r0, a->row_scale ? a->row_scale + r0 : nullptr,
@@ -444,7 +465,7 @@ shampoo_status shampoo_matmul_f8_workspace(int64_t n, int64_t M, int64_t N, int6
 shampoo_status shampoo_matmul_f8(const void* a, shampoo_dtype a_dt, const void* a_scale, int32_t a_block_rows, const void* b,
                                  shampoo_dtype b_dt, const void* b_scale, int32_t b_block_rows, int64_t n, int64_t M, int64_t N,
                                  int64_t K, void* c, shampoo_dtype c_dt, void* ws, size_t ws_bytes, hipStream_t stream) {
-  return matmul_f8_impl(a, a_dt, a_scale, a_block_rows, b, b_dt, b_scale, b_block_rows, n, M, N, K, c, c_dt, true, ws, ws_bytes, stream);
+  return matmul_f8_impl(a, a_dt, a_scale, a_block_rows, b, b_dt, b_scale, b_block_rows, n, M, N, K, c, c_dt, ws, ws_bytes, stream);
 }
 
 shampoo_status shampoo_linear_xent_workspace(const shampoo_xent_args* args, size_t* bytes) {
@@ -465,7 +486,7 @@ shampoo_status shampoo_linear_xent(const shampoo_xent_args* a, hipStream_t strea
   const size_t es = size_of(a->dt);
   if (a->ld_hidden < a->d || a->ld_weight < a->d || (a->dhidden && a->ld_dhidden < a->d) || (a->dweight && a->ld_dweight < a->d))
     return fail(SHAMPOO_E_INVALID, "row stride below d = %lld", (long long)a->d);
-  if (!aligned(a->hidden, es) || !aligned(a->weight, es) || !aligned(a->dhidden, es) || !aligned(a->targets, 8) || !aligned(a->loss, 4) ||
+  if (!aligned(a->hidden, es) || !aligned(a->weight, size_of(a->weight_dt)) || !aligned(a->dhidden, es) || !aligned(a->targets, 8) || !aligned(a->loss, 4) ||
       (a->dweight && !aligned(a->dweight, size_of(a->dweight_dt))) || !aligned(a->row_scale, 4) || !aligned(a->lse, 4))
     return fail(SHAMPOO_E_INVALID, "misaligned pointer");
   if (!a->ws || a->ws_bytes < L.total || !aligned(a->ws, 256))

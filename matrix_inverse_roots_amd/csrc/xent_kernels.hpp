@@ -40,6 +40,9 @@ struct RowArgs {
   const void* hidden;          // [M][ldh]
   const void* weight;          // [V][ldw]
   int64_t ldh, ldw;
+  const uint8_t* hs;           // 8-bit operands: their scales, lds bytes a row
+  const uint8_t* ws;
+  int64_t lds;
   int d;
   float* target_logit;         // [M]
   const int64_t* targets;      // [M]
@@ -54,7 +57,8 @@ struct RowArgs {
 // R rows per workgroup of 1024 threads: thread t joins pieces t / R, + 1024 /
 // R, ... of row t % R.  The target's logit is a product of two rows of its
 // own, by 1024 / R threads: cheaper than to look for it among the logits in
-// the large product's epilogue.  T: float, or uint16_t for bfloat16.
+// the large product's epilogue.  T: float, uint16_t for bfloat16, or uint8_t
+// for 8-bit operands (d their padded width).
 template <int R, typename T>
 __global__ __launch_bounds__(1024) void xent_rows_kernel(RowArgs g) {
   __shared__ floatx2_t red[1024];
@@ -81,10 +85,24 @@ __global__ __launch_bounds__(1024) void xent_rows_kernel(RowArgs g) {
     if (t != g.ignore && t >= 0 && t < g.V) {
       const T* x = reinterpret_cast<const T*>(g.hidden) + m * g.ldh;
       const T* w = reinterpret_cast<const T*>(g.weight) + t * g.ldw;
+      if constexpr (sizeof(T) == 1) {
+        const uint8_t* sx = g.hs + m * g.lds;
+        const uint8_t* sw = g.ws + t * g.lds;
+#pragma unroll 2
+        for (int k = grp; k < g.d / 4; k += G) {
+          const uint32_t a = reinterpret_cast<const uint32_t*>(x)[k], b = reinterpret_cast<const uint32_t*>(w)[k];
+          float q = __builtin_amdgcn_cvt_f32_fp8(a, 0) * __builtin_amdgcn_cvt_f32_fp8(b, 0);
+          q += __builtin_amdgcn_cvt_f32_fp8(a, 1) * __builtin_amdgcn_cvt_f32_fp8(b, 1);
+          q += __builtin_amdgcn_cvt_f32_fp8(a, 2) * __builtin_amdgcn_cvt_f32_fp8(b, 2);
+          q += __builtin_amdgcn_cvt_f32_fp8(a, 3) * __builtin_amdgcn_cvt_f32_fp8(b, 3);
+          dot += ldexpf(q, (int)sx[k >> 5] + (int)sw[k >> 5] - 254);
+        }
+      } else {
 #pragma unroll 4
       for (int k = grp; k < g.d; k += G) {
         if constexpr (sizeof(T) == 4) dot += x[k] * w[k];
         else dot += __builtin_bit_cast(float, (uint32_t)x[k] << 16) * __builtin_bit_cast(float, (uint32_t)w[k] << 16);
+      }
       }
     }
   }
@@ -222,15 +240,35 @@ __global__ __launch_bounds__(256) void sum_splits_kernel(const float* __restrict
   }
 }
 
-// Rows of `cols` elements (es bytes each), ld apart, copied into rows of ldo
-// with zeros behind: an operand whose rows do not start on 16 bytes
-template <typename T>
-__global__ __launch_bounds__(256) void pad_rows_kernel(const T* __restrict__ x, int64_t ld, int64_t rows, int cols, T* __restrict__ o, int ldo) {
-  const int64_t total = rows * ldo;
-  for (int64_t i = blockIdx.x * (int64_t)256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-    const int64_t r = i / ldo;
-    const int c = (int)(i - r * ldo);
-    o[i] = c < cols ? x[r * ld + c] : T(0);
+// Rows of `cols` elements, ld apart, as rows of ldo elements (a multiple of
+// 8) with zeros behind: an operand whose rows do not start on 16 bytes, or a
+// float32 weight rounded to bfloat16.  TI, TO: float, or uint16_t for
+// bfloat16.  A wave takes a row at a time, 4 elements a lane.
+template <typename TI, typename TO>
+__global__ __launch_bounds__(256) void pad_rows_kernel(const TI* __restrict__ x, int64_t ld, int64_t rows, int cols, TO* __restrict__ o,
+                                                       int ldo, int vec) {
+  struct Four { TI v[4]; };
+  struct Out { TO v[4]; };
+  auto turn = [](TI v) -> TO {
+    if constexpr (sizeof(TI) == sizeof(TO)) return v;
+    else return __builtin_bit_cast(uint16_t, (__bf16)v);
+  };
+  const int lane = threadIdx.x & 63;
+  for (int64_t r = blockIdx.x * (int64_t)4 + (threadIdx.x >> 6); r < rows; r += (int64_t)gridDim.x * 4) {
+    const TI* from = x + r * ld;
+    TO* to = o + r * ldo;
+    for (int c = 4 * lane; c < ldo; c += 256) {
+      Out w;
+      if (vec && c + 4 <= cols) {
+        const Four f = *reinterpret_cast<const Four*>(from + c);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w.v[e] = turn(f.v[e]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w.v[e] = c + e < cols ? turn(from[c + e]) : TO(0);
+      }
+      *reinterpret_cast<Out*>(to + c) = w;
+    }
   }
 }
 

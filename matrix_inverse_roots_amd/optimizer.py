@@ -14,8 +14,8 @@ import math
 
 import numpy as np
 
-from . import (RootOpts, StepArgsC, GRAFTS, FALLBACKS, F32, F64, BF16, shampoo_plan_blocks, shampoo_step,
-               shampoo_step_workspace, table_to_device, _ptr)
+from . import (RootOpts, StepArgsC, GRAFTS, FALLBACKS, F32, F64, BF16, shampoo_linear_xent,
+               shampoo_plan_blocks, shampoo_step, shampoo_step_workspace, table_to_device, _ptr)
 
 
 def reshape_2d(shape):
@@ -177,6 +177,10 @@ class Shampoo:
     precondition_dtype: None (the products of D = L^{-1/4} G R^{-1/4} in the
     roots' precision) or torch.bfloat16 (bfloat16 operands, float32
     accumulation and D; bfloat16 gradients and float32 statistics only).
+
+    ``projection_loss`` computes the softmax cross entropy of a parameter
+    used as the output projection and keeps that parameter's gradient for the
+    next ``step``.
     """
 
     def __init__(self, params, block_size=1024, beta2=1.0, eps=1e-12, p=4, root=None, graft="sgd",
@@ -222,6 +226,8 @@ class Shampoo:
                               params[0].device)
             self.stacks.append(st)
             self.members.append(idx)
+        self._kept = {}         # parameter index -> gradient buffer that projection_loss writes
+        self._pending = set()   # those written since the last step
         self.frequency = int(precondition_frequency)
         self.t = 0
         self.device = params[0].device
@@ -231,14 +237,64 @@ class Shampoo:
         # so that the longest chain starts while the host enqueues the rest
         self._order = sorted(range(len(self.stacks)), key=lambda k: -self.stacks[k].nblk * self.stacks[k].B ** 3)
 
+    def projection_loss(self, index, hidden, targets, dhidden=None, row_scale=None, ignore_index=-100,
+                        reduction="mean", scale=1.0, panel_rows=0, logits_dtype=None, stream=None):
+        """Softmax cross entropy of hidden params[index]^T against ``targets``
+        (``shampoo_linear_xent``: the logits are never kept); returns the loss.
+
+        params[index] is the output projection [vocabulary, width]; hidden
+        [tokens, width] is float32, or bfloat16 (the parameter is then
+        rounded to bfloat16 for the products).  The parameter's gradient goes
+        to a buffer of the optimizer's gradient type, which the next ``step``
+        takes where its gradient is given as None; calls before that step add
+        to it (micro-batches: give each its share in ``scale``).  dhidden
+        receives hidden's gradient.  Float32 hidden needs float32 gradients.
+        logits_dtype=torch.float8_e4m3fn takes the logits from the 8-bit
+        product of hidden and the parameter.
+        The buffer is written on ``stream`` (default: the current stream) and
+        read by the step on its own."""
+        torch = self.stacks[0].torch
+        w = self.params[index]
+        index = range(len(self.params))[index]
+        if w.dim() != 2:
+            raise ValueError("projection_loss: parameter %d has %d dimensions, not 2" % (index, w.dim()))
+        gdt = self.hp["grad_dtype"]
+        if hidden.dtype == torch.float32 and gdt != torch.float32:
+            raise ValueError("projection_loss: float32 hidden needs float32 gradients (grad_dtype)")
+        fresh = index not in self._pending
+        dw = self._kept.get(index)
+        if dw is None:
+            dw = torch.empty(w.shape, dtype=gdt, device=self.device)
+        loss = shampoo_linear_xent(hidden, w, targets, dhidden=dhidden, dweight=dw, row_scale=row_scale,
+                                   ignore_index=ignore_index, reduction=reduction, scale=scale,
+                                   accumulate=not fresh, panel_rows=panel_rows, logits_dtype=logits_dtype,
+                                   stream=stream)
+        self._kept[index] = dw
+        self._pending.add(index)
+        return loss
+
+    def _gradients(self, grads):
+        """One tensor per parameter: None stands for what projection_loss kept."""
+        grads = list(grads)
+        for i, g in enumerate(grads):
+            if g is None:
+                if i not in self._pending:
+                    raise ValueError("no gradient for parameter %d: projection_loss has not been called on it "
+                                     "since the last step" % i)
+                grads[i] = self._kept[i]
+        return grads
+
     def step(self, grads, stream=None):
-        """One step with gradients given per parameter (same order as params)."""
+        """One step with gradients given per parameter (same order as params);
+        None takes the gradient that ``projection_loss`` kept."""
+        grads = self._gradients(grads)
         self.t += 1
         recompute = (self.t - 1) % self.frequency == 0
         views = [g.reshape(v.shape) for g, v in zip(grads, self.views)]
         if not self._side:
             for st, idx in zip(self.stacks, self.members):
                 st.step([views[i] for i in idx], self.t, recompute, stream=stream)
+            self._pending.clear()
             return
         torch = self.stacks[0].torch
         cur = stream if stream is not None else torch.cuda.current_stream(self.device)
@@ -257,6 +313,7 @@ class Shampoo:
             joins.append(done)
         for done in joins:
             cur.wait_event(done)
+        self._pending.clear()
 
     def capture(self, grads):
         """Record one step on the gradient buffers ``grads`` into a graph and
@@ -281,6 +338,8 @@ class Shampoo:
             raise ValueError("capture: a coupled-Newton tolerance synchronises with the host")
         if self.t < 1:
             raise ValueError("capture: take one eager step first")
+        pending = set(self._pending)
+        grads = self._gradients(grads)
         views = [g.reshape(v.shape) for g, v in zip(grads, self.views)]
         # descriptor tables of these buffers, uploaded before the capture
         cur = torch.cuda.current_stream(self.device)
@@ -295,9 +354,11 @@ class Shampoo:
         with torch.cuda.graph(graph):
             self.step(grads)
         self.t = t_saved
+        self._pending = pending
 
         def replay():
             self.t += 1
+            self._pending.clear()
             graph.replay()
 
         replay.graph = graph

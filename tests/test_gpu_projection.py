@@ -1,0 +1,215 @@
+"""The paths over the 8-bit products and the projection's loss together: the
+loss with 8-bit logits, projection_loss feeding an optimizer step, and a whole
+training step of a small network on these operators."""
+
+import numpy as np
+import pytest
+
+import f8_reference as ref
+from helpers import log
+from test_gpu_xent import definition, make, check
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -23
+
+
+@pytest.fixture(scope="module")
+def mir():
+    import matrix_inverse_roots_amd as m
+    return m
+
+
+def code(q, s, rb, fmt):
+    """What quantised blocks stand for, in float64."""
+    import torch
+    return ref.stand_for(ref.code_values(fmt)[q.view(torch.uint8).cpu().numpy()], s.view(torch.uint8).cpu().numpy(), rb)
+
+
+@pytest.mark.parametrize("wdt", ["float32", "bfloat16"])
+@pytest.mark.parametrize("reduction", ["mean", "none"])
+@pytest.mark.parametrize("N,d,V", [(1, 1, 2), (3, 100, 129), (130, 96, 257), (300, 200, 5001), (257, 640, 700)])
+def test_loss_with_8_bit_logits(mir, N, d, V, reduction, wdt):
+    """The softmax, its loss and its gradient are those of the 8-bit logits;
+    the gradients' products use the bfloat16 operands.  The 8-bit products drop
+    what lies 2^-13 below the largest of an instruction's: dz = (2^-13 + d 2^-23)
+    |x| |w| on the quantised operands."""
+    import torch
+    h, w, t = make(N, d, V, "bfloat16", N + d)
+    w = w.float() * 1.001 if wdt == "float32" else w
+    dh, dw = torch.full_like(h, float("nan")), torch.full((V, d), float("nan"), dtype=torch.bfloat16, device="cuda")
+    loss = mir.shampoo_linear_xent(h, w, t, reduction=reduction, dhidden=dh, dweight=dw, logits_dtype=torch.float8_e4m3fn)
+    alone = mir.shampoo_linear_xent(h, w, t, reduction=reduction, logits_dtype=torch.float8_e4m3fn)
+    assert torch.equal(loss, alone)
+    X, W = code(*mir.shampoo_quantize_f8(h), 1, "e4m3"), code(*mir.shampoo_quantize_f8(w), 1, "e4m3")
+    z = X @ W.T
+    dz = ((2.0 ** -13 + (d + 1) * U) * (np.abs(X) @ np.abs(W).T)).max(axis=1)
+    tt = t.cpu().numpy()
+    kept, at, rows = tt != -100, np.where(tt != -100, tt, 0), np.arange(N)
+    m = z.max(axis=1, keepdims=True)
+    lse = np.log(np.exp(z - m).sum(axis=1)) + m[:, 0]
+    count = max(int(kept.sum()), 1)
+    each = np.where(kept, lse - z[rows, at], 0.0)
+    few = 2 * dz + 160 * U + 4 * U * (np.abs(lse) + np.abs(z[rows, at]))
+    if reduction == "mean":
+        check(loss, each.sum() / count, (few * kept).sum() / count + U * abs(each.sum()), "loss")
+    else:
+        check(loss, each, few * kept + 2 * U * np.abs(each), "loss")
+    g = kept / (count if reduction == "mean" else 1)
+    P = np.exp(z - lse[:, None])
+    rel = few[:, None] + 2.1 * 2.0 ** -8
+    dP = P * rel
+    p_t = P[rows, at].copy()
+    P[rows, at] -= 1.0
+    dP[rows, at] = p_t * rel[:, 0] + 2.0 ** -8 * np.abs(P[rows, at])
+    P, dP = P * g[:, None], dP * g[:, None]
+    x, y = h.double().cpu().numpy(), w.bfloat16().double().cpu().numpy()
+    for got, want, err in ((dh, P @ y, dP @ np.abs(y) + V * U * ((np.abs(P) + dP) @ np.abs(y))),
+                           (dw, P.T @ x, dP.T @ np.abs(x) + N * U * ((np.abs(P) + dP).T @ np.abs(x)))):
+        check(got, want, 1.01 * (err + 2.0 ** -8 * np.abs(want)) + 1e-37, "gradient")
+    # and the loss stays near the bfloat16 one: logits off by the operands' roundings
+    b = definition(h, w.bfloat16(), t, reduction)[0]
+    log(f"N {N} d {d} V {V} {wdt}: loss {np.mean(loss.cpu().numpy()):.4f}, with bfloat16 logits {np.mean(b):.4f}")
+
+
+def test_8_bit_logits_refusals(mir):
+    import torch
+    h, w, t = make(10, 64, 200, "float32", 1)
+    with pytest.raises(ValueError, match="bfloat16 hidden"):
+        mir.shampoo_linear_xent(h, w, t, logits_dtype=torch.float8_e4m3fn)
+    with pytest.raises(ValueError):
+        mir.shampoo_linear_xent(h.bfloat16(), w, t, logits_dtype=torch.float8_e5m2)
+
+
+def optimizer(mir, V, d, gdt, **kw):
+    import torch
+    g = torch.Generator(device="cuda")
+    g.manual_seed(3)
+    W = [torch.randn((96, 64), generator=g, device="cuda"), torch.randn((V, d), generator=g, device="cuda") / d ** 0.5]
+    hp = dict(block_size=128, beta2=0.9, eps=1e-4, root=mir.RootOpts(method="cn", iters=25, eps=1e-4), graft="sgd", lr=0.05,
+              grad_dtype=gdt)
+    return mir.Shampoo(W, **{**hp, **kw})
+
+
+@pytest.mark.parametrize("hdt,gdt", [("float32", "float32"), ("bfloat16", "float32"), ("bfloat16", "bfloat16")])
+def test_projection_loss_feeds_the_step(mir, hdt, gdt):
+    """Two micro-batches through projection_loss, then a step with None, give
+    the bits of the same step on the gradient computed by hand; the loss and
+    hidden's gradient match float64."""
+    import torch
+    V, d = 500, 64
+    hd, gd = getattr(torch, hdt), getattr(torch, gdt)
+    a, b = optimizer(mir, V, d, gd), optimizer(mir, V, d, gd)
+    for step in range(2):
+        g0 = torch.randn(96, 64, device="cuda").to(gd)
+        dw = torch.empty((V, d), dtype=gd, device="cuda")
+        for k in range(2):
+            h, _, t = make(70 + k, d, V, hdt, 10 * step + k)
+            dh = torch.empty_like(h)
+            loss = a.projection_loss(1, h, t, dhidden=dh, scale=0.5)
+            w = b.params[1]
+            wr = w if hd == torch.float32 else w.to(hd)
+            r = definition(h, wr, t, "mean", scale=0.5)
+            check(loss, r[0], r[4], "loss")
+            check(dh, r[1], r[5], "dhidden")
+            mir.shampoo_linear_xent(h, w, t, dweight=dw, scale=0.5, accumulate=k > 0)
+        a.step([g0, None])
+        b.step([g0, dw])
+        for x, y in zip(a.params, b.params):
+            assert torch.equal(x, y)
+    with pytest.raises(ValueError, match="projection_loss"):
+        a.step([g0, None])
+    a.step([g0, dw])
+
+
+def test_projection_loss_refusals(mir):
+    import torch
+    opt = optimizer(mir, 200, 64, torch.bfloat16)
+    h, _, t = make(10, 64, 200, "float32", 1)
+    with pytest.raises(ValueError, match="float32 gradients"):
+        opt.projection_loss(1, h, t)
+    with pytest.raises(ValueError):
+        opt.projection_loss(1, h.bfloat16()[:, :32], t)
+    with pytest.raises(IndexError):
+        opt.projection_loss(2, h.bfloat16(), t)
+    opt = mir.Shampoo([torch.zeros((4, 8, 8), device="cuda")], block_size=64)
+    with pytest.raises(ValueError, match="dimensions"):
+        opt.projection_loss(0, h, t)
+
+
+def test_captured_step_on_the_kept_gradient(mir):
+    """capture() with None replays on the buffer that projection_loss fills."""
+    import torch
+    V, d = 300, 64
+    a, b = (optimizer(mir, V, d, torch.float32) for _ in range(2))
+    g0 = torch.randn(96, 64, device="cuda")
+
+    def loss(o, k):
+        h, _, t = make(60, d, V, "bfloat16", k)
+        return o.projection_loss(1, h, t)
+
+    for o in (a, b):
+        loss(o, 0)
+        o.step([g0, None])
+    loss(a, 1)
+    replay = a.capture([g0, None])
+    for k in range(1, 5):
+        la = loss(a, k) if k > 1 else None
+        lb = loss(b, k)
+        torch.cuda.synchronize()
+        replay()
+        torch.cuda.synchronize()
+        b.step([g0, None])
+        assert la is None or torch.equal(la, lb)
+        for x, y in zip(a.params, b.params):
+            assert torch.equal(x, y)
+
+
+def test_float32_weight_beside_bfloat16_hidden(mir):
+    """The same bits as with the weight rounded beforehand, at every alignment."""
+    import torch
+    for d in (64, 33, 100):
+        h, w, t = make(50, d, 333, "bfloat16", d)
+        w32 = torch.randn(333, d, device="cuda")
+        out = []
+        for weight in (w32, w32.bfloat16()):
+            dh, dw = torch.empty_like(h), torch.empty(333, d, device="cuda")
+            out.append((mir.shampoo_linear_xent(h, weight, t, dhidden=dh, dweight=dw), dh, dw))
+        assert all(torch.equal(x, y) for x, y in zip(*out))
+
+
+def test_network_step_in_8_bits(mir):
+    """x -> x W0^T in 8 bits -> projection loss -> 8-bit gradients of the layer
+    with 8-bit logits -> 8-bit gradients of the layer -> a step: the layer's
+    products against float64 on the same operands, the rest finite and moving."""
+    import torch
+    T, K, d, V = 160, 96, 192, 700
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    W = [torch.randn((d, K), generator=g, device="cuda") / K ** 0.5, torch.randn((V, d), generator=g, device="cuda") / d ** 0.5]
+    opt = mir.Shampoo(W, block_size=128, beta2=0.9, eps=1e-4, root=mir.RootOpts(method="cn", iters=25, eps=1e-4), graft="sgd",
+                      lr=0.5, grad_dtype=torch.bfloat16, precondition_dtype=torch.bfloat16)
+    x = torch.randn((T, K), generator=g, device="cuda").bfloat16()
+    t = torch.randint(0, V, (T,), generator=g, device="cuda")
+    for step in range(3):
+        (xq, xt) = mir.shampoo_quantize_f8(x, transpose="both")
+        wq = mir.shampoo_quantize_f8(W[0], block_rows=128)
+        h = mir.shampoo_matmul_f8(*xq, *wq, torch.empty((T, d), dtype=torch.bfloat16, device="cuda"))
+        X, W0 = code(*xq, 1, "e4m3"), code(*wq, 128, "e4m3")
+        want = X @ W0.T
+        bound = 2.0 ** -8 * np.abs(want) + 2.0 ** -13 * (np.abs(X) @ np.abs(W0).T)
+        assert (np.abs(h.double().cpu().numpy() - want) <= bound).all()
+        dh = torch.empty_like(h)
+        loss = opt.projection_loss(1, h, t, dhidden=dh, logits_dtype=torch.float8_e4m3fn)
+        again = mir.shampoo_linear_xent(h, W[1], t, logits_dtype=torch.float8_e4m3fn)
+        assert torch.equal(loss, again) and torch.isfinite(loss) and torch.isfinite(dh).all()
+        dt = mir.shampoo_quantize_f8(dh, fmt="e5m2", transpose=True)
+        dw = mir.shampoo_matmul_f8(*dt, *xt, torch.empty((d, K), dtype=torch.bfloat16, device="cuda"))
+        D, Xt = code(*dt, 1, "e5m2"), code(*xt, 1, "e4m3")
+        want = D @ Xt.T
+        bound = 2.0 ** -8 * np.abs(want) + 2.0 ** -13 * (np.abs(D) @ np.abs(Xt).T)
+        assert (np.abs(dw.double().cpu().numpy() - want) <= bound).all()
+        before = [w.clone() for w in W]
+        opt.step([dw, None])
+        assert all(torch.isfinite(w).all() and not torch.equal(w, b) for w, b in zip(W, before))
+        log(f"step {step}: loss {loss.item():.4f}")
