@@ -411,13 +411,39 @@ def _on_device(*tensors):
             raise ValueError("expected device tensors")
         if dev is None:
             dev = t.device
-        elif t.device != dev:
+        elif t.get_device() != dev.index:
             raise ValueError("tensors are on different devices")
     return dev
 
 
+def _launch(fn, dev, stream, *args):
+    """fn(*args, stream) with ``dev`` current, on ``stream`` or the current one of that device."""
+    torch = _torch()
+    if torch.cuda.current_device() == dev.index:
+        if stream is None:
+            raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+            handle = raw(dev.index) if raw is not None else torch.cuda.current_stream().cuda_stream
+        else:
+            handle = stream.cuda_stream
+        _check(fn(*args, handle))
+    else:
+        with torch.cuda.device(dev):
+            _check(fn(*args, (stream if stream is not None else torch.cuda.current_stream()).cuda_stream))
+
+
 def _up(x, m):
     return -(-x // m) * m
+
+
+_FLOAT_CODES = {}
+
+
+def _float_codes():
+    """Types that are quantised, and that products write."""
+    if not _FLOAT_CODES:
+        torch = _torch()
+        _FLOAT_CODES.update({torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16})
+    return _FLOAT_CODES
 
 
 def _f8_code(t):
@@ -441,50 +467,55 @@ def shampoo_quantize_f8(x, fmt="e4m3", block_rows=1, transpose=False, out=None, 
     ((q, scale), (q_t, scale_t)) from one reading of x.  ``out``: tensors to
     write to, as returned."""
     torch = _torch()
-    if fmt not in FORMATS_F8:
+    code = FORMATS_F8.get(fmt)
+    if code is None:
         raise ValueError("fmt must be one of %s" % sorted(FORMATS_F8))
-    if block_rows not in (1, 128):
+    if block_rows != 1 and block_rows != 128:
         raise ValueError("block_rows must be 1 or 128")
-    if transpose not in (False, True, "both"):
+    if transpose is not False and transpose is not True and transpose != "both":
         raise ValueError("transpose must be False, True or 'both'")
-    if x.dim() not in (2, 3):
+    dim = x.dim()
+    if dim not in (2, 3):
         raise ValueError("x must have 2 or 3 dimensions")
-    if x.dtype not in (torch.float32, torch.float16, torch.bfloat16):
+    dt = _float_codes().get(x.dtype)
+    if dt is None:
         raise TypeError("unsupported dtype %s" % x.dtype)
     dev = _on_device(x)
-    if x.numel() and x.shape[-1] > 1 and x.stride(-1) != 1:
-        raise ValueError("x must have unit column stride")
-    n = x.shape[0] if x.dim() == 3 else 1
-    rows, cols = x.shape[-2], x.shape[-1]
-    ld = x.stride(-2) if rows > 1 else cols
-    if x.numel() and (ld < cols or (n > 1 and x.dim() == 3 and x.stride(0) < 0)):
-        raise ValueError("x must not overlap itself (row stride %d, %d columns)" % (ld, cols))
-    kind = torch.float8_e4m3fn if fmt == "e4m3" else torch.float8_e5m2
+    n, rows, cols = x.shape if dim == 3 else (1,) + tuple(x.shape)
+    ld, apart = cols, 0
+    if n and rows and cols:
+        strides = x.stride()
+        if cols > 1 and strides[-1] != 1:
+            raise ValueError("x must have unit column stride")
+        ld = strides[-2] if rows > 1 else cols
+        apart = strides[0] if n > 1 else 0
+        if ld < cols or apart < 0:
+            raise ValueError("x must not overlap itself (row stride %d, %d columns)" % (ld, cols))
+    kind = torch.float8_e4m3fn if code == E4M3 else torch.float8_e5m2
 
     def pair(r, k, given):
         K = _up(k, 128)
-        shapes = ((n, r, K), (n, -(-r // block_rows), _up(K // 128, 4)))
-        if x.dim() == 2:
-            shapes = tuple(s[1:] for s in shapes)
-        kinds = (kind, torch.float8_e8m0fnu)
+        shape, held = (r, K), (r if block_rows == 1 else -(-r // 128), _up(K // 128, 4))
+        if dim == 3:
+            shape, held = (n,) + shape, (n,) + held
         if given is None:
-            return tuple(torch.empty(s, dtype=d, device=dev) for s, d in zip(shapes, kinds))
-        for t, s, d in zip(given, shapes, kinds):
+            return (torch.empty(shape, dtype=kind, device=dev),
+                    torch.empty(held, dtype=torch.float8_e8m0fnu, device=dev))
+        for t, s, d in zip(given, (shape, held), (kind, torch.float8_e8m0fnu)):
             _dev(t, "out")
             if tuple(t.shape) != s or t.dtype != d or t.device != dev:
                 raise ValueError("out must be a %s tensor of shape %s on %s" % (d, s, dev))
         return tuple(given)
 
-    both = transpose == "both"
-    plain = pair(rows, cols, (out[0] if both else out) if out is not None else None) if transpose is not True else None
-    turned = pair(cols, rows, (out[1] if both else out) if out is not None else None) if transpose else None
-    q, s = plain if plain is not None else (None, None)
-    qt, st = turned if turned is not None else (None, None)
-    with torch.cuda.device(dev):
-        _check(lib.shampoo_quantize_f8(_ptr(x), _dtype_code(x), n, rows, cols, ld, x.stride(0) if x.dim() == 3 else 0,
-                                       FORMATS_F8[fmt], int(block_rows), _ptr(q), _ptr(s), _ptr(qt), _ptr(st),
-                                       _stream(stream)))
-    return (plain, turned) if both else turned if transpose else plain
+    q = s = qt = st = plain = turned = None
+    if transpose is not True:
+        plain = pair(rows, cols, out[0] if out is not None and transpose else out)
+        q, s = plain[0].data_ptr(), plain[1].data_ptr()
+    if transpose:
+        turned = pair(cols, rows, out[1] if out is not None and transpose == "both" else out)
+        qt, st = turned[0].data_ptr(), turned[1].data_ptr()
+    _launch(lib.shampoo_quantize_f8, dev, stream, x.data_ptr(), dt, n, rows, cols, ld, apart, code, block_rows, q, s, qt, st)
+    return (plain, turned) if transpose == "both" else turned if transpose else plain
 
 
 def shampoo_matmul_f8_workspace(n, M, N, K):
@@ -502,32 +533,40 @@ def shampoo_matmul_f8(a, a_scale, b, b_scale, c, ws=None, stream=None):
     torch = _torch()
     dev = _on_device(a, a_scale, b, b_scale, c, ws)
     for t, nm in ((a, "a"), (a_scale, "a_scale"), (b, "b"), (b_scale, "b_scale"), (c, "c")):
-        _dev(t, nm)
-    if not (a.dim() == b.dim() == c.dim() == a_scale.dim() == b_scale.dim()) or a.dim() not in (2, 3):
+        if not t.is_contiguous():
+            raise ValueError("%s must be contiguous" % nm)
+    dim = a.dim()
+    if dim not in (2, 3) or b.dim() != dim or c.dim() != dim or a_scale.dim() != dim or b_scale.dim() != dim:
         raise ValueError("a, b, c and the scales must all have 2, or all 3, dimensions")
-    if c.dtype not in (torch.float32, torch.float16, torch.bfloat16):
+    cdt = _float_codes().get(c.dtype)
+    if cdt is None:
         raise TypeError("unsupported result dtype %s" % c.dtype)
-    n = a.shape[0] if a.dim() == 3 else 1
-    M, K, N = a.shape[-2], a.shape[-1], b.shape[-2]
-    if b.shape[-1] != K or (a.dim() == 3 and b.shape[0] != n) or tuple(c.shape) != tuple(a.shape[:-2]) + (M, N):
+    n, M, K = a.shape if dim == 3 else (1,) + tuple(a.shape)
+    N = b.shape[-2]
+    lead = (n,) if dim == 3 else ()
+    if tuple(b.shape) != lead + (N, K) or tuple(c.shape) != lead + (M, N):
         raise ValueError("shapes do not match: a %s, b %s, c %s" % (tuple(a.shape), tuple(b.shape), tuple(c.shape)))
 
     def block_rows(t, s, rows):
-        if s.dtype not in (torch.float8_e8m0fnu, torch.uint8):
+        if s.dtype != torch.float8_e8m0fnu and s.dtype != torch.uint8:
             raise TypeError("scales must be float8_e8m0fnu")
-        for rb in (1, 128):
-            if tuple(s.shape) == tuple(t.shape[:-2]) + (-(-rows // rb), _up(K // 128, 4)):
-                return rb
-        raise ValueError("scales of shape %s do not fit %s" % (tuple(s.shape), tuple(t.shape)))
+        shape, Ks = tuple(s.shape), _up(K // 128, 4)
+        if shape == lead + (rows, Ks):
+            return 1
+        if shape == lead + (-(-rows // 128), Ks):
+            return 128
+        raise ValueError("scales of shape %s do not fit %s" % (shape, tuple(t.shape)))
 
     arb, brb = block_rows(a, a_scale, M), block_rows(b, b_scale, N)
+    room = 0
     if ws is None:
-        nb = shampoo_matmul_f8_workspace(n, M, N, K)
-        ws = torch.empty(nb, dtype=torch.uint8, device=dev) if nb else None
-    with torch.cuda.device(dev):
-        _check(lib.shampoo_matmul_f8(_ptr(a), _f8_code(a), _ptr(a_scale), arb, _ptr(b), _f8_code(b), _ptr(b_scale), brb,
-                                     n, M, N, K, _ptr(c), _dtype_code(c), _ptr(ws),
-                                     0 if ws is None else ws.numel() * ws.element_size(), _stream(stream)))
+        need = shampoo_matmul_f8_workspace(n, M, N, K)
+        ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    if ws is not None:
+        room = ws.numel() * ws.element_size()
+    _launch(lib.shampoo_matmul_f8, dev, stream, a.data_ptr(), _f8_code(a), a_scale.data_ptr(), arb, b.data_ptr(),
+            _f8_code(b), b_scale.data_ptr(), brb, n, M, N, K, c.data_ptr(), cdt,
+            None if ws is None else ws.data_ptr(), room)
     return c
 
 
@@ -624,8 +663,7 @@ def shampoo_linear_xent(hidden, weight, targets, loss=None, lse=None, dhidden=No
         _check(lib.shampoo_linear_xent_workspace(ctypes.byref(args), ctypes.byref(b)))
         ws = torch.empty(max(b.value, 1), dtype=torch.uint8, device=dev)
     args.ws, args.ws_bytes = ws.data_ptr(), ws.numel() * ws.element_size()
-    with torch.cuda.device(dev):
-        _check(lib.shampoo_linear_xent(ctypes.byref(args), _stream(stream)))
+    _launch(lib.shampoo_linear_xent, dev, stream, ctypes.byref(args))
     return loss
 
 

@@ -37,9 +37,16 @@ Shape plan_shape(int64_t batch, int64_t M, int64_t N, int64_t K, int es, bool ma
   s.nst = (int)((K * es + 127) / 128);
   const int64_t tl = batch * ((M + 255) / 256) * ((N + 255) / 256);
   const int64_t ts = batch * ((M + 127) / 128) * ((N + 127) / 128);
-  // rounds of the chip, a small round being half the work at 70% of the rate
+  // Tiles of the busiest compute unit, in large tiles' time.  A small tile is
+  // a quarter of the work, at 84% of the rate of a large one (8-bit 4096^3,
+  // 4 small per unit against 1 large: 80 and 71 us; bfloat16 8192 x 65536 x
+  // 1024: 1190 and 980 us), or 95% in float32, whose matrix instructions
+  // outlast the loads (2048 x 16384 x 1024: 543 and 522 us).  So small tiles
+  // win where they divide among the units better (8-bit 6144^2 x 2048, 9 small
+  // against 3 large: 95 and 102 us; float32 10007 x 1024 x 999: 617 and 727 us
+  // for the loss with both gradients).
   const double large_cost = (double)((tl + CUS - 1) / CUS);
-  const double small_cost = (double)((ts + 2 * CUS - 1) / (2 * CUS)) * 0.5 / 0.7;
+  const double small_cost = (double)((ts + CUS - 1) / CUS) * 0.25 / (es == 4 ? 0.95 : 0.84);
   s.large = large_cost <= small_cost;
   s.splits = 1;
   s.split_stages = s.nst;

@@ -62,7 +62,7 @@ struct RowArgs {
 template <int R, typename T>
 __global__ __launch_bounds__(1024) void xent_rows_kernel(RowArgs g) {
   __shared__ floatx2_t red[1024];
-  __shared__ float dots[1024];
+  __shared__ float dots[R == 1 ? 16 : R];
   const int tid = threadIdx.x, lr = tid % R, grp = tid / R;
   constexpr int G = 1024 / R;
   const int m = blockIdx.x * R + lr;
@@ -77,19 +77,23 @@ __global__ __launch_bounds__(1024) void xent_rows_kernel(RowArgs g) {
       mx = nm;
     }
   }
-  // z_t: threads of one row are R apart in `red`, so they are in the dot too
-  float dot = 0.f;
-  int64_t t = -1;
-  if (m < g.M) {
-    t = g.targets[m];
-    if (t != g.ignore && t >= 0 && t < g.V) {
-      const T* x = reinterpret_cast<const T*>(g.hidden) + m * g.ldh;
+  // z_t: a row to a wave (R rows), or the row to all waves (R = 1)
+  const int lane = tid & 63, wave = tid >> 6;
+  constexpr int STEP = R == 1 ? 1024 : 64, PER = R == 1 ? 1 : R / 16;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int row = blockIdx.x * R + (R == 1 ? 0 : wave * PER + i);
+    const int from = R == 1 ? tid : lane;
+    float dot = 0.f;
+    const int64_t t = row < g.M ? g.targets[row] : -1;
+    if (row < g.M && t != g.ignore && t >= 0 && t < g.V) {
+      const T* x = reinterpret_cast<const T*>(g.hidden) + row * g.ldh;
       const T* w = reinterpret_cast<const T*>(g.weight) + t * g.ldw;
       if constexpr (sizeof(T) == 1) {
-        const uint8_t* sx = g.hs + m * g.lds;
+        const uint8_t* sx = g.hs + row * g.lds;
         const uint8_t* sw = g.ws + t * g.lds;
-#pragma unroll 2
-        for (int k = grp; k < g.d / 4; k += G) {
+#pragma unroll 4
+        for (int k = from; k < g.d / 4; k += STEP) {
           const uint32_t a = reinterpret_cast<const uint32_t*>(x)[k], b = reinterpret_cast<const uint32_t*>(w)[k];
           float q = __builtin_amdgcn_cvt_f32_fp8(a, 0) * __builtin_amdgcn_cvt_f32_fp8(b, 0);
           q += __builtin_amdgcn_cvt_f32_fp8(a, 1) * __builtin_amdgcn_cvt_f32_fp8(b, 1);
@@ -98,15 +102,24 @@ __global__ __launch_bounds__(1024) void xent_rows_kernel(RowArgs g) {
           dot += ldexpf(q, (int)sx[k >> 5] + (int)sw[k >> 5] - 254);
         }
       } else {
+        // four elements a lane (operands of products start on 16 bytes, and
+        // a row's last run is whole or zeros follow it up to 8 elements)
+        struct Four { T v[4]; };
 #pragma unroll 4
-      for (int k = grp; k < g.d; k += G) {
-        if constexpr (sizeof(T) == 4) dot += x[k] * w[k];
-        else dot += __builtin_bit_cast(float, (uint32_t)x[k] << 16) * __builtin_bit_cast(float, (uint32_t)w[k] << 16);
-      }
+        for (int k = 4 * from; k < g.d; k += 4 * STEP) {
+          const Four a = *reinterpret_cast<const Four*>(x + k), b = *reinterpret_cast<const Four*>(w + k);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            if constexpr (sizeof(T) == 4) dot += a.v[e] * b.v[e];
+            else dot += __builtin_bit_cast(float, (uint32_t)a.v[e] << 16) * __builtin_bit_cast(float, (uint32_t)b.v[e] << 16);
+          }
+        }
       }
     }
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) dot += __shfl_xor(dot, d);
+    if (lane == 0) dots[R == 1 ? wave : wave * PER + i] = dot;
   }
-  dots[tid] = dot;
   red[tid] = floatx2_t{mx, s};
   __syncthreads();
   for (int d = G / 2; d > 0; d /= 2) {
@@ -117,14 +130,18 @@ __global__ __launch_bounds__(1024) void xent_rows_kernel(RowArgs g) {
       s = s * __expf(mx - ref) + o[1] * __expf(o[0] - ref);
       mx = nm;
       red[tid] = floatx2_t{mx, s};
-      dot += dots[tid + d * R];
-      dots[tid] = dot;
     }
     __syncthreads();
   }
   if (grp == 0 && m < g.M) {
     const float lse = mx + logf(s);
     g.lse[m] = lse;
+    const int64_t t = g.targets[m];
+    float dot = dots[lr];
+    if constexpr (R == 1) {
+#pragma unroll
+      for (int k = 1; k < 16; ++k) dot += dots[k];
+    }
     g.target_logit[m] = dot;
     float l = 0.f;
     if (t != g.ignore) {
