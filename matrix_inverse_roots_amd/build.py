@@ -17,7 +17,7 @@ LIB = os.path.join(PKG, "libshampoo.so")
 SOURCES = [os.path.join(PKG, "csrc", f) for f in ("shampoo.hip", "products.hip")]
 HEADERS = [os.path.join(PKG, "csrc", f) for f in ("gemm_common.hpp", "gemm.hpp", "gemm_hsym.hpp", "gemm_nn256.hpp",
                                                   "kernels.hpp", "host_common.hpp", "product_core.hpp",
-                                                  "f8_kernels.hpp", "xent_kernels.hpp")] + [
+                                                  "f8_kernels.hpp", "f8_rows.hpp", "xent_kernels.hpp")] + [
     os.path.join(ROOT, "include", "shampoo.h")]
 
 FLAGS = [

@@ -7,6 +7,7 @@
 #include <type_traits>
 
 #include "f8_kernels.hpp"
+#include "f8_rows.hpp"
 #include "host_common.hpp"
 #include "product_core.hpp"
 #include "shampoo.h"
@@ -209,8 +210,20 @@ hipError_t launch_f8(const ProductArgs& g, int a_dt, int b_dt, bool large, int64
   return launch_product<E, false, false, Epi::STORE, 1, 1>(g, large, n, st);
 }
 
+// Few rows: f8_rows_kernel.  Measured against the tiles: see there.
+bool few_rows(int64_t M) { return M <= F8_ROWS_MAX; }
+
+template <int MB>
+hipError_t launch_rows(const ProductArgs& g, int a_dt, int b_dt, int64_t n, hipStream_t st) {
+  const dim3 grid((unsigned)((g.N + 15) / 16), (unsigned)n);
+  const bool a5 = a_dt == SHAMPOO_E5M2, b5 = b_dt == SHAMPOO_E5M2;
+  const auto kernel = a5 ? (b5 ? f8_rows_kernel<MB, 1, 1> : f8_rows_kernel<MB, 1, 0>) : (b5 ? f8_rows_kernel<MB, 0, 1> : f8_rows_kernel<MB, 0, 0>);
+  hipLaunchKernelGGL(kernel, grid, dim3(256), 0, st, g);
+  return hipGetLastError();
+}
+
 size_t matmul_f8_bytes(int64_t n, int64_t M, int64_t N, int64_t K) {
-  if (n == 0 || M == 0 || N == 0) return 0;
+  if (n == 0 || M == 0 || N == 0 || few_rows(M)) return 0;
   return partial_bytes(plan_shape(n, M, N, K, 1, true), n, M, N);
 }
 
@@ -229,7 +242,7 @@ shampoo_status matmul_f8_impl(const void* a, int a_dt, const void* sa, int32_t a
   if (!aligned(a, 16) || !aligned(b, 16) || !aligned(sa, 4) || !aligned(sb, 4) || !aligned(c, size_of(c_dt)))
     return fail(SHAMPOO_E_INVALID, "misaligned pointer");
   const Shape s = plan_shape(n, M, N, K, 1, true);
-  const size_t need = partial_bytes(s, n, M, N);
+  const size_t need = matmul_f8_bytes(n, M, N, K);
   if (need && (!ws || ws_bytes < need)) return fail(SHAMPOO_E_WORKSPACE, "workspace %zu bytes < %zu needed", ws ? ws_bytes : 0, need);
   ProductArgs g{};
   g.A = a; g.B = b; g.sa = (const uint8_t*)sa; g.sb = (const uint8_t*)sb;
@@ -241,6 +254,12 @@ shampoo_status matmul_f8_impl(const void* a, int a_dt, const void* sa, int32_t a
   g.sb_shift = brb == 128 ? 7 : 0;
   g.strideSa = (arb == 128 ? (M + 127) / 128 : M) * g.ldsa;
   g.strideSb = (brb == 128 ? (N + 127) / 128 : N) * g.ldsb;
+  if (few_rows(M)) {
+    g.C = c; g.ldc = N; g.strideC = M * N; g.c_dt = out_code(c_dt);
+    HIP_TRY(M == 1 ? launch_rows<1>(g, a_dt, b_dt, n, st) : M == 2 ? launch_rows<2>(g, a_dt, b_dt, n, st)
+            : launch_rows<4>(g, a_dt, b_dt, n, st));
+    return SHAMPOO_OK;
+  }
   set_shape(g, s);
   const Out o{c, N, M * N, out_code(c_dt), rows_vec(c, N, n > 1 ? M * N : 0, c_dt), 0.f};
   point_output(g, s, o, (float*)ws, n);

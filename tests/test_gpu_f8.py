@@ -134,6 +134,15 @@ def test_product_matches_float64(mir, M, N, K, out):
     product_case(mir, 1, M, N, K, "e4m3", "e4m3", 1, 128, out)
 
 
+@pytest.mark.parametrize("M", [1, 2, 3, 4, 5, 8])
+@pytest.mark.parametrize("N,K,rbb", [(1, 128, 1), (13, 700, 1), (4096, 1024, 128), (301, 3000, 128)])
+def test_product_of_few_rows(mir, M, N, K, rbb):
+    """One to four rows take the kernel for few rows, more the tiles; every
+    pair of formats, two matrices, scales of A by row and by 128 rows."""
+    for k, (fa, fb) in enumerate((("e4m3", "e4m3"), ("e4m3", "e5m2"), ("e5m2", "e4m3"), ("e5m2", "e5m2"))):
+        product_case(mir, 2, M, N, K, fa, fb, 128 if k % 2 else 1, rbb, ("float32", "bfloat16", "float16", "float32")[k], seed=M)
+
+
 @pytest.mark.parametrize("fa,fb", [("e4m3", "e5m2"), ("e5m2", "e4m3"), ("e5m2", "e5m2")])
 @pytest.mark.parametrize("rba,rbb", [(1, 1), (128, 1), (128, 128)])
 def test_product_formats_and_blocks(mir, fa, fb, rba, rbb):
