@@ -160,9 +160,8 @@ __device__ __forceinline__ shortx4_t read_transposed(const lds_s4* __restrict__ 
 typedef __amdgpu_buffer_rsrc_t rsrc_t;
 constexpr uint32_t RSRC_FLAGS = 0x00027000;       // raw 32-bit buffer
 constexpr uint32_t RSRC_OUTSIDE = 0x80000000u;    // an offset outside every descriptor
-__device__ __forceinline__ rsrc_t rsrc_of(const unsigned char* p, int64_t bytes) {
-  const uint32_t n = bytes <= 0 ? 0u : bytes >= 0x7fffffff ? 0x7fffffffu : (uint32_t)bytes;
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<unsigned char*>(p), 0, n, RSRC_FLAGS);
+__device__ __forceinline__ rsrc_t rsrc_of(const unsigned char* p, uint32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<unsigned char*>(p), 0, bytes, RSRC_FLAGS);
 }
 
 template <Elem E, int FM, int FN, int WM, int WN, bool AS, bool BS, Epi EPI, int FA, int FB>
@@ -196,83 +195,113 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_kernel(ProductArgs g)
   const int l32 = lane & 31, half = lane >> 5;
 
   struct Item { int batch, split, tm, tn, k0, stages; };
-  // tiles in bands of 8 rows of tiles, column by column: the tiles that run
-  // at the same time on an XCD share the operands' panels in its L2
-  auto item_of = [&](int it) {
-    Item r;
-    const int64_t w = first + (int64_t)it * per;
+  // Tiles in bands of 8 rows of tiles, column by column: the tiles that run
+  // at the same time on an XCD share the operands' panels in its L2.  A place
+  // (matrix and range of k, band, tile of the band) is found by division once
+  // and then moved on by `per`: divisions at every tile would take as long as
+  // several stages.
+  struct Place { int bs, band, u; };
+  auto band_size = [&](int band) { return min(8, g.mt - 8 * band) * g.nt; };
+  auto place_of = [&](int64_t w) {
+    Place p;
     const int tiles = g.mt * g.nt;
-    const int bs = (int)(w / tiles);
-    int t = (int)(w - (int64_t)bs * tiles);
-    r.batch = bs / g.splits;
-    r.split = bs - r.batch * g.splits;
-    const int band = t / (8 * g.nt), rows = min(8, g.mt - 8 * band);
-    t -= band * 8 * g.nt;
-    r.tn = t / rows;
-    r.tm = 8 * band + t - r.tn * rows;
+    p.bs = (int)(w / tiles);
+    p.u = (int)(w - (int64_t)p.bs * tiles);
+    p.band = p.u / (8 * g.nt);
+    p.u -= p.band * 8 * g.nt;
+    return p;
+  };
+  auto move_on = [&](Place& p) {
+    p.u += per;
+    for (int size = band_size(p.band); p.u >= size; size = band_size(p.band)) {
+      p.u -= size;
+      if (8 * ++p.band >= g.mt) {
+        p.band = 0;
+        ++p.bs;
+      }
+    }
+  };
+  auto item_at = [&](const Place& p) {
+    Item r;
+    r.batch = g.splits == 1 ? p.bs : p.bs / g.splits;
+    r.split = p.bs - r.batch * g.splits;
+    const int rows = min(8, g.mt - 8 * p.band);
+    r.tn = rows == 8 ? p.u >> 3 : p.u / rows;
+    r.tm = 8 * p.band + p.u - r.tn * rows;
     r.k0 = r.split * g.split_stages;
     r.stages = min(g.split_stages, g.nst - r.k0);
     return r;
   };
 
   // ---- loads -------------------------------------------------------------
-  // offA, offB: this lane's bytes within a stage's part of the tile; PA, PB:
-  // where that part starts; leftA, leftB: bytes from there to the operand's
-  // end, past which a descriptor reads zeros
-  // (kA, kB: the k-row, or the byte of the row, within the stage)
-  uint32_t offA[NIA], offB[NIB], kA[NIA], kB[NIB];
-  auto offsets = [&](uint32_t* off, uint32_t* kk, int n, bool strided, int T, int64_t ld) {
+  // offA, offB: this lane's bytes within a stage's part of the tile; tailA,
+  // tailB: the same in the last stage, where what is past K lies outside.  PA,
+  // PB: where that part starts (k-contiguous: at the item's first stage, with
+  // the stage's distance in `ahead`); endA, endB: bytes from there to the end
+  // of the operand's last row or k-row, past which a descriptor reads zeros.
+  const int last = g.nst - 1, rest = g.K - last * SK;  // the last stage, and its k
+  uint32_t offA[NIA], offB[NIB], tailA[NIA], tailB[NIB];
+  auto offsets = [&](uint32_t* off, uint32_t* tail, int n, bool strided, int T, int64_t ld) {
 #pragma unroll
     for (int q = 0; q < n; ++q) {
       const int at = (wave * n + q) * 1024 + lane * 16;
       if (strided) {
         const int k = at / (T * ES), pos = at % (T * ES) / 16;
         off[q] = (uint32_t)(k * ld * ES) + 16 * (pos ^ (ES == 2 ? 4 * (k & 3) : 8 * ((k >> 2) & 1)));
-        kk[q] = k;
+        tail[q] = k < rest ? off[q] : RSRC_OUTSIDE;
       } else {
-        const int row = at >> 7;
-        kk[q] = 16 * ((lane & 7) ^ ((row >> 1) & 7));
-        off[q] = (uint32_t)(row * ld * ES) + kk[q];
+        const int row = at >> 7, byte = 16 * ((lane & 7) ^ ((row >> 1) & 7));
+        off[q] = (uint32_t)(row * ld * ES) + byte;
+        tail[q] = byte < rest * ES ? off[q] : RSRC_OUTSIDE;
       }
     }
   };
-  offsets(offA, kA, NIA, AS, TM, g.lda);
-  offsets(offB, kB, NIB, BS, TN, g.ldb);
+  offsets(offA, tailA, NIA, AS, TM, g.lda);
+  offsets(offB, tailB, NIB, BS, TN, g.ldb);
   const int Kb = (g.K * ES + 15) & ~15;  // k-contiguous: bytes of a row, in whole chunks
   const unsigned char *PA, *PB;
-  int64_t leftA, leftB;
+  int64_t endA, endB;
+  int ahead = 0;
+  Place lp = place_of(first);
+  // a descriptor's size: what is left, at most 2^31 - 1 and never below zero
+  auto clip = [](int64_t bytes) {
+    const int high = (int)(bytes >> 31);
+    return high < 0 ? 0u : high > 0 ? 0x7fffffffu : (uint32_t)bytes;
+  };
   int lit = 0, lk = 0, lend = 0, ls = 0, lg = 0;  // item, stage, its end, buffer, scale group of the next load
   Item li;
   auto begin_loads = [&]() {
-    li = item_of(lit);
+    li = item_at(lp);
     lk = li.k0;
+    ahead = 0;
     lend = li.k0 + li.stages;
     const int ra = li.tm * TM, rb = li.tn * TN;
     const int64_t ka = AS ? (int64_t)lk * SK * g.lda * ES : (int64_t)lk * 128, kb = BS ? (int64_t)lk * SK * g.ldb * ES : (int64_t)lk * 128;
     PA = reinterpret_cast<const unsigned char*>(g.A) + li.batch * g.strideA * ES + ka + (AS ? (int64_t)ra * ES : ra * g.lda * ES);
     PB = reinterpret_cast<const unsigned char*>(g.B) + li.batch * g.strideB * ES + kb + (BS ? (int64_t)rb * ES : rb * g.ldb * ES);
-    // strided: the last k-row's columns, in whole chunks (rows start on 16 bytes)
-    leftA = AS ? (g.K - 1) * g.lda * ES + (((g.M - ra) * ES + 15) & ~15) - ka : (g.M - 1 - ra) * g.lda * ES + Kb - ka;
-    leftB = BS ? (g.K - 1) * g.ldb * ES + (((g.N - rb) * ES + 15) & ~15) - kb : (g.N - 1 - rb) * g.ldb * ES + Kb - kb;
+    // strided: the last k-row's columns, in whole chunks (rows start on 16
+    // bytes); columns past the tile's read what follows, and nothing past that
+    endA = AS ? (g.K - 1) * g.lda * ES + (((g.M - ra) * ES + 15) & ~15) - ka : (g.M - 1 - ra) * g.lda * ES + Kb - ka;
+    endB = BS ? (g.K - 1) * g.ldb * ES + (((g.N - rb) * ES + 15) & ~15) - kb : (g.N - 1 - rb) * g.ldb * ES + Kb - kb;
   };
   // one stage into its buffer (zeros once every item's stages are issued)
   auto issue = [&]() {
-    const rsrc_t ra = rsrc_of(PA, leftA), rb = rsrc_of(PB, leftB);
+    const bool tail = lk == last;
+    const rsrc_t ra = rsrc_of(PA, clip(endA)), rb = rsrc_of(PB, clip(endB));
     lds_u8* const sa = lds + ls * STAGE + wave * (NIA * 1024);
     lds_u8* const sb = lds + ls * STAGE + OPA + wave * (NIB * 1024);
-    const bool whole = (lk + 1) * SK <= g.K;
-    // the last stage of a row or column may reach past K: zeros there
+    const int aheadA = AS ? 0 : ahead, aheadB = BS ? 0 : ahead;
 #pragma unroll
     for (int q = 0; q < NIA; ++q) {
       uint32_t o = offA[q];
-      if (!SCALED && !whole) o |= (AS ? lk * SK + (int)kA[q] < g.K : lk * 128 + (int)kA[q] < Kb) ? 0 : RSRC_OUTSIDE;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, sa + q * 1024, 16, o, 0, 0, 0);
+      if (!SCALED && tail) o = tailA[q];
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, sa + q * 1024, 16, o, aheadA, 0, 0);
     }
 #pragma unroll
     for (int q = 0; q < NIB; ++q) {
       uint32_t o = offB[q];
-      if (!SCALED && !whole) o |= (BS ? lk * SK + (int)kB[q] < g.K : lk * 128 + (int)kB[q] < Kb) ? 0 : RSRC_OUTSIDE;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, sb + q * 1024, 16, o, 0, 0, 0);
+      if (!SCALED && tail) o = tailB[q];
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, sb + q * 1024, 16, o, aheadB, 0, 0);
     }
   };
   auto issue_scales = [&]() {
@@ -296,13 +325,20 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_kernel(ProductArgs g)
     }
   };
   auto advance = [&]() {
-    const int64_t da = AS ? SK * g.lda * ES : 128, db = BS ? SK * g.ldb * ES : 128;
-    PA += da; leftA -= da;
-    PB += db; leftB -= db;
     ls ^= 1;
+    if (lend < 0) return;  // nothing left: the descriptors stay empty
+    if (AS) PA += SK * g.lda * ES, endA -= SK * g.lda * ES;
+    if (BS) PB += SK * g.ldb * ES, endB -= SK * g.ldb * ES;
+    ahead += 128;
     if (++lk == lend) {
-      if (++lit < nitem) begin_loads();
-      else leftA = leftB = 0, lend = -1;
+      if (++lit < nitem) {
+        move_on(lp);
+        begin_loads();
+      } else {
+        endA = endB = 0;  // descriptors of nothing: zeros
+        ahead = 0;
+        lend = -1;
+      }
     }
   };
 
@@ -411,9 +447,10 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_kernel(ProductArgs g)
   read_frags(0, 0);
   read_scales(0, 0, sc[0]);
 
+  Place cp = place_of(first);
 #pragma nounroll
   for (int it = 0; it < nitem; ++it) {
-    const Item cur = item_of(it);
+    const Item cur = item_at(cp);
 #pragma unroll
     for (int i = 0; i < FM; ++i)
 #pragma unroll
@@ -584,6 +621,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_kernel(ProductArgs g)
         }
       }
     }
+    move_on(cp);
   }
 }
 
