@@ -53,8 +53,8 @@ Shape plan_shape(int64_t batch, int64_t M, int64_t N, int64_t K, int es, bool ma
   s.split_stages = s.nst;
   const int64_t items = s.large ? tl : ts, slots = s.large ? CUS : 2 * CUS;
   if (may_split && items * 2 <= slots) {
-    // at least 8 stages a range
-    const int64_t want = std::min<int64_t>(slots / items, s.nst / 8);
+    // at least 4 stages a range
+    const int64_t want = std::min<int64_t>(slots / items, s.nst / 4);
     if (want >= 2) {
       s.split_stages = (int)up((s.nst + want - 1) / want, 4);
       s.splits = (s.nst + s.split_stages - 1) / s.split_stages;
@@ -131,10 +131,12 @@ void point_output(ProductArgs& g, const Shape& s, const Out& o, float* part, int
   }
 }
 hipError_t sum_splits(const float* part, int splits, int64_t split_stride, const Out& o, int64_t batch, int M, int N, hipStream_t st) {
-  const int64_t total = (int64_t)M * N;
-  const int64_t gx = std::max<int64_t>(1, std::min<int64_t>((total + 255) / 256, 8192));
-  hipLaunchKernelGGL(sum_splits_kernel, dim3((unsigned)gx, (unsigned)batch), dim3(256), 0, st, part, splits, split_stride, o.C, o.ldc,
-                     o.strideC, M, N, o.c_dt, o.alpha, o.alpha_dev, o.beta);
+  int tx = 0;
+  while (tx < 8 && (4 << tx) < N) ++tx;
+  const int gx = (N + (4 << tx) - 1) / (4 << tx);
+  const int gy = (int)std::max<int64_t>(1, std::min<int64_t>(((int64_t)M + (256 >> tx) - 1) / (256 >> tx), 65535));
+  hipLaunchKernelGGL(sum_splits_kernel, dim3(gx, gy, (unsigned)batch), dim3(256), 0, st, part, splits, split_stride, o.C, o.ldc, o.strideC, M,
+                     N, o.c_dt, o.alpha, o.alpha_dev, o.beta, tx, N % 4 == 0 ? 1 : 0);
   return hipGetLastError();
 }
 hipError_t finish_split(const ProductArgs& g, const Shape& s, const Out& o, const float* part, int64_t batch, hipStream_t st) {

@@ -230,29 +230,47 @@ __global__ __launch_bounds__(256) void xent_grad_kernel(GradArgs g) {
 }
 
 // C = alpha x the sum of `splits` float32 partial results (+ beta C), any output type
-// (0 float32, 1 half, 2 bfloat16); rows of N elements, ldc apart, batches
-// of M rows
+// (0 float32, 1 half, 2 bfloat16); rows of N elements, ldc apart, batches of M
+// rows.  2^tx threads of a workgroup go along a row, 4 columns each (vec: N
+// and the rows' starts allow 16-byte accesses); the others take further rows.
 __global__ __launch_bounds__(256) void sum_splits_kernel(const float* __restrict__ part, int splits, int64_t split_stride,
                                                          void* __restrict__ C, int64_t ldc, int64_t strideC, int M, int N,
-                                                         int c_dt, float alpha, const float* __restrict__ alpha_dev, float beta) {
+                                                         int c_dt, float alpha, const float* __restrict__ alpha_dev, float beta, int tx,
+                                                         int vec) {
   if (alpha_dev) alpha *= *alpha_dev;
-  const int64_t total = (int64_t)M * N;
-  const int64_t b = blockIdx.y;
-  for (int64_t i = blockIdx.x * (int64_t)256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-    float a = 0.f;
-    const float* p = part + b * total + i;
-    for (int s = 0; s < splits; ++s) a += p[s * split_stride];
-    a *= alpha;
-    const int64_t m = i / N, at = b * strideC + m * ldc + (i - m * N);
-    if (c_dt == 0) {
-      float* o = reinterpret_cast<float*>(C) + at;
-      *o = a + (beta != 0.f ? beta * *o : 0.f);
-    } else if (c_dt == 1) {
-      _Float16* o = reinterpret_cast<_Float16*>(C) + at;
-      *o = (_Float16)(a + (beta != 0.f ? beta * (float)*o : 0.f));
+  const int64_t b = blockIdx.z;
+  const int n = 4 * ((int)(threadIdx.x & ((1 << tx) - 1)) + ((int)blockIdx.x << tx));
+  if (n >= N) return;
+  for (int m = (blockIdx.y << (8 - tx)) + (threadIdx.x >> tx); m < M; m += gridDim.y << (8 - tx)) {
+    const float* p = part + (b * M + m) * (int64_t)N + n;
+    float a[4] = {0.f, 0.f, 0.f, 0.f};
+    if (vec) {
+#pragma unroll 4
+      for (int s = 0; s < splits; ++s) {
+        const floatx4 v = *reinterpret_cast<const floatx4*>(p + s * split_stride);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) a[e] += v[e];
+      }
     } else {
-      __bf16* o = reinterpret_cast<__bf16*>(C) + at;
-      *o = (__bf16)(a + (beta != 0.f ? beta * (float)*o : 0.f));
+      for (int s = 0; s < splits; ++s)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (n + e < N) a[e] += p[s * split_stride + e];
+    }
+    const int64_t at = b * strideC + m * ldc + n;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (n + e >= N) break;
+      if (c_dt == 0) {
+        float* o = reinterpret_cast<float*>(C) + at + e;
+        *o = alpha * a[e] + (beta != 0.f ? beta * *o : 0.f);
+      } else if (c_dt == 1) {
+        _Float16* o = reinterpret_cast<_Float16*>(C) + at + e;
+        *o = (_Float16)(alpha * a[e] + (beta != 0.f ? beta * (float)*o : 0.f));
+      } else {
+        __bf16* o = reinterpret_cast<__bf16*>(C) + at + e;
+        *o = (__bf16)(alpha * a[e] + (beta != 0.f ? beta * (float)*o : 0.f));
+      }
     }
   }
 }
