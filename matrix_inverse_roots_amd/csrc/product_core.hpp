@@ -24,10 +24,11 @@
 // of their XCD's share, so that the loads of the next tile run through the
 // end of the current one.  A stage is 128 bytes of k of every row of both
 // operands; stages go straight to LDS (buffer_load ... lds, 16 bytes a lane)
-// into two buffers.  Each wave reads one half of a stage's k into registers
+// into NB buffers (two, or four where a compute unit holds one small
+// workgroup).  Each wave reads one half of a stage's k into registers
 // while the matrix cores work on the half before it, so a stage's buffer is
-// free when its second half is multiplied, and takes the stage after next:
-// loads have the time of a whole stage to land.  One barrier per stage.
+// free when its second half is multiplied, and takes the stage NB on: loads
+// have the time of NB - 1 stages to land.  One barrier per stage.
 //
 // LDS layouts, conflict-free for the reads (16 lanes of a ds_read_b128 are
 // served together: lanes 0-3, 12-15, 20-23, 24-27 of each 32):
@@ -164,7 +165,7 @@ __device__ __forceinline__ rsrc_t rsrc_of(const unsigned char* p, uint32_t bytes
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<unsigned char*>(p), 0, bytes, RSRC_FLAGS);
 }
 
-template <Elem E, int FM, int FN, int WM, int WN, bool AS, bool BS, Epi EPI, int FA, int FB>
+template <Elem E, int FM, int FN, int WM, int WN, int NB, bool AS, bool BS, Epi EPI, int FA, int FB>
 __global__ __launch_bounds__(64 * WM * WN, 2) void product_kernel(ProductArgs g) {
   constexpr int ES = ElemTraits<E>::size;
   constexpr int W = WM * WN, TM = 32 * FM * WM, TN = 32 * FN * WN;
@@ -172,7 +173,9 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_kernel(ProductArgs g)
   constexpr int NIA = TM / 8 / W, NIB = TN / 8 / W;
   constexpr int SK = 128 / ES;  // k of one stage
   constexpr bool SCALED = E == Elem::F8 || E == Elem::F8W;
-  constexpr int SCALES = 2 * STAGE, SGROUP = 4 * (TM + TN);  // LDS: 4 groups of scales behind the buffers
+  // LDS: NB buffers, then groups of scales (a group each for NB stages ahead at most, and the current one)
+  constexpr int NI = NIA + NIB, NG = NB > 2 ? 8 : 4, SCALES = NB * STAGE, SGROUP = 4 * (TM + TN);
+  static_assert(NB == 2 || NB == 4, "buffers are counted with masks");
   static_assert(NIA * W * 8 == TM && NIB * W * 8 == TN, "loads divide among the waves");
   static_assert(!SCALED || (!AS && !BS), "8-bit operands are k-contiguous");
   static_assert(!SCALED || (TM + TN) % (64 * W) == 0, "each wave loads the scales of as many rows");
@@ -320,12 +323,12 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_kernel(ProductArgs g)
                                  : g.sb + li.batch * g.strideSb + (int64_t)row * g.ldsb;
           __builtin_amdgcn_global_load_lds((const void*)(p + lk), (void*)(smem + SCALES + lg * SGROUP + first_row * 4), 4, 0, 0);
         }
-        lg = (lg + 1) & 3;
+        lg = (lg + 1) & (NG - 1);
       }
     }
   };
   auto advance = [&]() {
-    ls ^= 1;
+    ls = NB == 2 ? ls ^ 1 : (ls + 1) & (NB - 1);
     if (lend < 0) return;  // nothing left: the descriptors stay empty
     if (AS) PA += SK * g.lda * ES, endA -= SK * g.lda * ES;
     if (BS) PB += SK * g.ldb * ES, endB -= SK * g.ldb * ES;
@@ -422,7 +425,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_kernel(ProductArgs g)
   // waits for them there.
   constexpr int NMMA = FM * FN * MMA_STEPS<E>;
   constexpr int NREAD = FM * (AS ? 4 : 2) + FN * (BS ? 4 : 2) + (SCALED ? FM + FN : 0);
-  constexpr int STEPS = NMMA * 3 / 4 < 16 ? NMMA * 3 / 4 : 16, RPS = (NREAD + STEPS - 1) / STEPS;
+  constexpr int STEPS = NMMA * 3 / 4 < 24 ? NMMA * 3 / 4 : 24, RPS = (NREAD + STEPS - 1) / STEPS;
   // loads over the whole half: a compute unit takes 16 cycles for each, and a
   // wave that meets a full queue stalls with its matrix-core instructions
   constexpr int LGAP = NMMA >= 2 * (NIA + NIB) ? NMMA / (NIA + NIB) : 1;
@@ -435,13 +438,13 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_kernel(ProductArgs g)
     }
   };
   begin_loads();
-  issue();
-  issue_scales();
-  advance();
-  issue();
-  issue_scales();
-  advance();
-  wait_stage<0>();
+#pragma nounroll
+  for (int s = 0; s < NB; ++s) {
+    issue();
+    issue_scales();
+    advance();
+  }
+  wait_stage<(NB - 1) * NI>();
   barrier_no_fence();
   int rb = 0, rg = 0;  // buffer and scale group of the stage being multiplied
   read_frags(0, 0);
@@ -463,21 +466,24 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_kernel(ProductArgs g)
       read_frags(rb, 1);
       multiply(0);
       interleave(false);
-      wait_stage<0>();  // this wave is done with the buffer, and its part of the next stage has landed
+      // this wave is done with the buffer, and its part of the next stage has
+      // landed; NB - 2 younger stages may be in flight
+      wait_stage<(NB - 2) * NI>();
       barrier_no_fence();
-      // second half; the buffer takes the stage after next (at the very end
-      // the other buffer is stale, and what is read from it unused)
+      // second half; the buffer takes the stage NB on (at the very end the
+      // next buffer is stale, and what is read from it unused)
       issue_scales();
       const bool last = s + 1 == cur.stages;
-      if (last || (s & 3) == 3) rg = (rg + 1) & 3;
+      if (last || (s & 3) == 3) rg = (rg + 1) & (NG - 1);
+      const int next = NB == 2 ? rb ^ 1 : (rb + 1) & (NB - 1);
       issue();
-      read_frags(rb ^ 1, 0);
+      read_frags(next, 0);
       read_scales(rg, last ? 0 : s + 1, sc[1]);
       multiply(1);
       interleave(true);
 #pragma unroll
       for (int i = 0; i < FM + FN; ++i) sc[0][i] = sc[1][i];
-      rb ^= 1;
+      rb = next;
       advance();
     }
 

@@ -51,7 +51,7 @@ Shape plan_shape(int64_t batch, int64_t M, int64_t N, int64_t K, int es, bool ma
   s.large = large_cost <= small_cost;
   s.splits = 1;
   s.split_stages = s.nst;
-  const int64_t items = s.large ? tl : ts, slots = s.large ? CUS : 2 * CUS;
+  const int64_t items = s.large ? tl : ts, slots = CUS;
   if (may_split && items * 2 <= slots) {
     // at least 4 stages a range
     const int64_t want = std::min<int64_t>(slots / items, s.nst / 4);
@@ -63,11 +63,11 @@ Shape plan_shape(int64_t batch, int64_t M, int64_t N, int64_t K, int es, bool ma
   return s;
 }
 
-template <Elem E, int FM, int FN, int WM, int WN, int PER_CU, bool AS, bool BS, Epi EPI, int FA, int FB>
+template <Elem E, int FM, int FN, int WM, int WN, int NB, int PER_CU, bool AS, bool BS, Epi EPI, int FA, int FB>
 hipError_t launch_tiles(ProductArgs g, int64_t batch, hipStream_t st) {
   constexpr int TM = 32 * FM * WM, TN = 32 * FN * WN;
-  constexpr int LDS = 2 * (TM + TN) * 128 + (E == Elem::F8 || E == Elem::F8W ? 16 * (TM + TN) : 0);  // two stages, 4 groups of scales
-  const auto kernel = product_kernel<E, FM, FN, WM, WN, AS, BS, EPI, FA, FB>;
+  constexpr int LDS = NB * (TM + TN) * 128 + (E == Elem::F8 || E == Elem::F8W ? (NB > 2 ? 32 : 16) * (TM + TN) : 0);  // stages, groups of scales
+  const auto kernel = product_kernel<E, FM, FN, WM, WN, NB, AS, BS, EPI, FA, FB>;
   static bool ready[MAX_DEVICES] = {false};
   int dev = 0, cus = 0;
   HIP_TRY_ERR(hipGetDevice(&dev));
@@ -86,8 +86,10 @@ hipError_t launch_tiles(ProductArgs g, int64_t batch, hipStream_t st) {
 
 template <Elem E, bool AS, bool BS, Epi EPI, int FA = 0, int FB = 0>
 hipError_t launch_product(const ProductArgs& g, bool large, int64_t batch, hipStream_t st) {
-  if (large) return launch_tiles<E, 2, 4, 4, 2, 1, AS, BS, EPI, FA, FB>(g, batch, st);
-  return launch_tiles<E, 1, 4, 4, 1, 2, AS, BS, EPI, FA, FB>(g, batch, st);
+  if (large) return launch_tiles<E, 2, 4, 4, 2, 2, 1, AS, BS, EPI, FA, FB>(g, batch, st);
+  const int64_t items = batch * g.splits * ((g.M + 127) / 128) * ((g.N + 127) / 128);
+  if (items <= CUS) return launch_tiles<E, 1, 4, 4, 1, 4, 1, AS, BS, EPI, FA, FB>(g, batch, st);
+  return launch_tiles<E, 1, 4, 4, 1, 2, 2, AS, BS, EPI, FA, FB>(g, batch, st);
 }
 
 void set_shape(ProductArgs& g, const Shape& s) {
