@@ -490,11 +490,13 @@ shampoo_status shampoo_matmul_f8(const void* a, shampoo_dtype a_dt, const void* 
  * Softmax cross entropy of a projection, with its gradients.
  *
  * z = hidden weight^T (hidden [N, d], weight [V, d]), and for row i with
- * target t_i:  loss_i = scale row_scale_i (log sum_v exp z_iv - z_it).  Rows
- * with t_i == ignore_index have loss 0 and gradient 0.  MEAN divides by the
- * number of kept rows (0 if there are none).  Gradients, of the reduced loss
- * (of the sum for NONE):  P_iv = g_i (softmax(z_i)_v - [v = t_i]),
- * dhidden = P weight,  dweight = P^T hidden.
+ * target t_i:  loss_i = log sum_v exp z_iv - z_it, and 0 for a row with t_i ==
+ * ignore_index, whose gradient is 0 too.  With g_i = scale row_scale_i, SUM
+ * gives sum_i g_i loss_i and MEAN that over the number of kept rows (0 if
+ * there are none).  NONE gives the loss_i themselves, and g_i is the gradient
+ * that arrives at them.  Gradients (g_i over the count for MEAN):
+ * P_iv = g_i (softmax(z_i)_v - [v = t_i]),  dhidden = P weight,
+ * dweight = P^T hidden.
  * Any other target outside [0, V) makes its row's loss and gradients NaN.
  * ------------------------------------------------------------------------- */
 typedef enum shampoo_reduction {

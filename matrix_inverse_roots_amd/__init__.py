@@ -644,9 +644,11 @@ def shampoo_linear_xent(hidden, weight, targets, loss=None, lse=None, dhidden=No
     stride; a float32 weight beside bfloat16 hidden is rounded to bfloat16),
     targets int64 [N]; rows with target ``ignore_index`` count for
     nothing.  reduction: "mean" over the other rows, "sum" or "none".
-    row_scale float32 [N] and scale multiply each row's loss.  dhidden, dweight:
-    tensors that receive the gradients of the (summed) loss; dweight may be
-    float32 beside bfloat16 inputs, and accumulate=True adds to it.  lse:
+    row_scale float32 [N] and scale multiply each row's loss before the
+    reduction; with "none" the losses come as they are, and row_scale times
+    scale is the gradient that arrives at them.  dhidden, dweight: tensors that
+    receive the gradients; dweight may be float32 beside bfloat16 inputs, and
+    accumulate=True adds to it.  lse:
     receives log sum exp of each row.  panel_rows bounds the rows whose
     exponentials the workspace holds at a time (0: up to 2 GiB of them).
     logits_dtype=torch.float8_e4m3fn (bfloat16 hidden only) quantises hidden

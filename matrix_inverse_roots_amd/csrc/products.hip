@@ -429,8 +429,9 @@ shampoo_status run_xent(const shampoo_xent_args* a, const XentLayout& L, hipStre
       HIP_TRY((product<E, false, false, Epi::SOFTMAX>(g, plan_shape(1, M, V, d, (int)es, false), st)));
     }
     float* lse = a->lse ? a->lse + r0 : (float*)(w + L.lse);
-    RowArgs ra{(const floatx2_t*)stats, g.A, g.B, g.lda, g.ldb, g.sa, g.sb, L.Ks, g.K, logit, a->targets + r0, a->row_scale ? a->row_scale + r0 : nullptr, lse, rows + r0,
-               a->ignore_index, (int)M, (int)V, (int)L.pieces, a->scale};
+    RowArgs ra{(const floatx2_t*)stats, g.A, g.B, g.lda, g.ldb, g.sa, g.sb, L.Ks, g.K, logit, a->targets + r0,
+               a->row_scale && !each ? a->row_scale + r0 : nullptr, lse, rows + r0, a->ignore_index, (int)M, (int)V, (int)L.pieces,
+               each ? 1.f : a->scale};
     const auto rows_kernel = L.f8 ? (M <= 256 ? xent_rows_kernel<1, uint8_t> : xent_rows_kernel<32, uint8_t>)
                                   : (M <= 256 ? xent_rows_kernel<1, TE> : xent_rows_kernel<32, TE>);
     hipLaunchKernelGGL(rows_kernel, dim3((unsigned)(M <= 256 ? M : (M + 31) / 32)), dim3(1024), 0, st, ra);

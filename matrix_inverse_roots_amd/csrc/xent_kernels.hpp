@@ -48,7 +48,7 @@ struct RowArgs {
   const int64_t* targets;      // [M]
   const float* row_scale;      // [M] or null
   float* lse;                  // [M]
-  float* loss;                 // [M] (scaled by row_scale and scale)
+  float* loss;                 // [M] (times row_scale and scale)
   int64_t ignore;
   int M, V, pieces;
   float scale;

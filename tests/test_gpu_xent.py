@@ -55,8 +55,9 @@ def definition(h, w, t, reduction, row_scale=None, scale=1.0):
     wide = dz.max(axis=1)
     # exp2 of (z - m) log2 e: the product's rounding is 2^-24 of an exponent of at most 130
     few = 160 * U
-    loss = np.where(kept, s * (lse - z[rows, at]), 0.0)
-    loss_err = np.where(kept, np.abs(s) * (2 * wide + few + 2 * U * (np.abs(lse) + np.abs(z[rows, at]))), 0.0) + 2 * U * np.abs(loss)
+    own = np.ones(N) if reduction == "none" else s   # "none" gives the rows' losses as they are
+    loss = np.where(kept, own * (lse - z[rows, at]), 0.0)
+    loss_err = np.where(kept, np.abs(own) * (2 * wide + few + 2 * U * (np.abs(lse) + np.abs(z[rows, at]))), 0.0) + 2 * U * np.abs(loss)
     g = np.where(kept, s, 0.0)
     if reduction == "mean":
         g = g / max(int(kept.sum()), 1)
