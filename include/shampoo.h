@@ -1,6 +1,8 @@
 /*
  * shampoo.h -- C ABI of the batched block preconditioner step of
- * block-diagonal Shampoo, for AMD Instinct MI355X (gfx950).
+ * block-diagonal Shampoo, for AMD Instinct MI355X (gfx950), and of two
+ * operators next to it: 8-bit block-scaled products and the softmax cross
+ * entropy of an output projection with its gradients.
  *
  * Sources cited below (titles of the pages; sections as named there):
  *   [DASH]  "DASH: Faster Shampoo via Batched Block Preconditioning and
@@ -476,10 +478,14 @@ shampoo_status shampoo_quantize_f8(const void* x, shampoo_dtype x_dt, int64_t n,
 /* C = A B^T of quantised stacks: a [n, M, K], b [n, N, K], K a positive
  * multiple of 128 (the padded width), scales as above with a_block_rows /
  * b_block_rows 1 or 128; formats in any mix.  c: [n, M, N] contiguous in c_dt
- * (F32, F16 or BF16).  The scales are applied exactly; sums run in float32 and
- * are rounded once to c_dt.  ws: shampoo_matmul_f8_workspace bytes (0 for
- * most shapes: float32 partial results where few outputs share a long K).
- * Results do not depend on the stream, the workspace's contents or the run. */
+ * (F32, F16 or BF16).  The scales (bytes 0 to 254) are applied exactly; sums
+ * run in float32 and are rounded once to c_dt.  For 16-bit results the 8-bit
+ * matrix instructions drop products some 2^13 below the largest of an
+ * instruction's (1.5e-5 relative on random operands); float32 results are
+ * summed without that.  ws: shampoo_matmul_f8_workspace bytes, 256-byte aligned
+ * (0 for most shapes: float32 partial results where few outputs share a long
+ * K).  Results do not depend on the stream, the workspace's contents or the
+ * run. */
 shampoo_status shampoo_matmul_f8_workspace(int64_t n, int64_t M, int64_t N, int64_t K, size_t* bytes);
 shampoo_status shampoo_matmul_f8(const void* a, shampoo_dtype a_dt, const void* a_scale, int32_t a_block_rows,
                                  const void* b, shampoo_dtype b_dt, const void* b_scale, int32_t b_block_rows,
@@ -520,7 +526,10 @@ typedef enum shampoo_reduction {
  * Logits are never kept: the vocabulary is walked in pieces of 128 columns
  * that leave a maximum and a sum each.  For gradients the rows are taken
  * panel_rows at a time (0: as many as keep the panel of exponentials within
- * 2 GiB), with the panel in the workspace. */
+ * 2 GiB), with the panel in the workspace (256-byte aligned).  V and the row
+ * strides of hidden and weight at most 2^20, d at most 2^18.  dhidden and
+ * dweight may not be hidden and weight themselves.  No atomics: two identical
+ * calls give identical bits. */
 typedef struct shampoo_xent_args {
   const void* hidden;
   const void* weight;

@@ -431,6 +431,16 @@ def _launch(fn, dev, stream, *args):
             _check(fn(*args, (stream if stream is not None else torch.cuda.current_stream()).cuda_stream))
 
 
+def _empty(shape, dtype, dev, stream):
+    """Device memory that belongs to the stream that will use it, so that the
+    allocator hands it on only behind that stream's work."""
+    torch = _torch()
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
 def _up(x, m):
     return -(-x // m) * m
 
@@ -499,8 +509,7 @@ def shampoo_quantize_f8(x, fmt="e4m3", block_rows=1, transpose=False, out=None, 
         if dim == 3:
             shape, held = (n,) + shape, (n,) + held
         if given is None:
-            return (torch.empty(shape, dtype=kind, device=dev),
-                    torch.empty(held, dtype=torch.float8_e8m0fnu, device=dev))
+            return _empty(shape, kind, dev, stream), _empty(held, torch.float8_e8m0fnu, dev, stream)
         for t, s, d in zip(given, (shape, held), (kind, torch.float8_e8m0fnu)):
             _dev(t, "out")
             if tuple(t.shape) != s or t.dtype != d or t.device != dev:
@@ -561,7 +570,7 @@ def shampoo_matmul_f8(a, a_scale, b, b_scale, c, ws=None, stream=None):
     room = 0
     if ws is None:
         need = shampoo_matmul_f8_workspace(n, M, N, K)
-        ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+        ws = _empty(need, torch.uint8, dev, stream) if need else None
     if ws is not None:
         room = ws.numel() * ws.element_size()
     _launch(lib.shampoo_matmul_f8, dev, stream, a.data_ptr(), _f8_code(a), a_scale.data_ptr(), arb, b.data_ptr(),
@@ -657,13 +666,13 @@ def shampoo_linear_xent(hidden, weight, targets, loss=None, lse=None, dhidden=No
     torch = _torch()
     dev = _on_device(hidden, weight, targets, loss, lse, dhidden, dweight, row_scale, ws)
     if loss is None:
-        loss = torch.empty((hidden.shape[0],) if reduction == "none" else (), dtype=torch.float32, device=dev)
+        loss = _empty((hidden.shape[0],) if reduction == "none" else (), torch.float32, dev, stream)
     args = _xent_args(hidden, weight, targets, loss, lse, dhidden, dweight, row_scale, ignore_index, reduction, scale,
                       accumulate, panel_rows, logits_dtype)
     if ws is None:
         b = ctypes.c_size_t(0)
         _check(lib.shampoo_linear_xent_workspace(ctypes.byref(args), ctypes.byref(b)))
-        ws = torch.empty(max(b.value, 1), dtype=torch.uint8, device=dev)
+        ws = _empty(max(b.value, 1), torch.uint8, dev, stream)
     args.ws, args.ws_bytes = ws.data_ptr(), ws.numel() * ws.element_size()
     _launch(lib.shampoo_linear_xent, dev, stream, ctypes.byref(args))
     return loss

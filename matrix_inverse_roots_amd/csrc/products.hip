@@ -247,7 +247,8 @@ shampoo_status matmul_f8_impl(const void* a, int a_dt, const void* sa, int32_t a
     return fail(SHAMPOO_E_INVALID, "misaligned pointer");
   const Shape s = plan_shape(n, M, N, K, 1, true);
   const size_t need = matmul_f8_bytes(n, M, N, K);
-  if (need && (!ws || ws_bytes < need)) return fail(SHAMPOO_E_WORKSPACE, "workspace %zu bytes < %zu needed", ws ? ws_bytes : 0, need);
+  if (need && (!ws || ws_bytes < need || !aligned(ws, 256)))
+    return fail(SHAMPOO_E_WORKSPACE, "workspace %zu bytes < %zu needed (256-byte aligned)", ws ? ws_bytes : 0, need);
   ProductArgs g{};
   g.A = a; g.B = b; g.sa = (const uint8_t*)sa; g.sb = (const uint8_t*)sb;
   g.M = (int)M; g.N = (int)N; g.K = (int)K;
@@ -520,6 +521,9 @@ shampoo_status shampoo_linear_xent(const shampoo_xent_args* a, hipStream_t strea
   if (!aligned(a->hidden, es) || !aligned(a->weight, size_of(a->weight_dt)) || !aligned(a->dhidden, es) || !aligned(a->targets, 8) || !aligned(a->loss, 4) ||
       (a->dweight && !aligned(a->dweight, size_of(a->dweight_dt))) || !aligned(a->row_scale, 4) || !aligned(a->lse, 4))
     return fail(SHAMPOO_E_INVALID, "misaligned pointer");
+  // a later panel reads what an earlier one's gradients would have replaced
+  if (a->N > 0 && ((a->dhidden && a->dhidden == a->hidden) || (a->dweight && a->dweight == a->weight)))
+    return fail(SHAMPOO_E_INVALID, "a gradient may not replace its operand");
   if (!a->ws || a->ws_bytes < L.total || !aligned(a->ws, 256))
     return fail(SHAMPOO_E_WORKSPACE, "workspace %zu bytes < %zu needed (256-byte aligned)", a->ws ? a->ws_bytes : 0, L.total);
   return a->dt == SHAMPOO_F32 ? run_xent<Elem::F32, float>(a, L, stream) : run_xent<Elem::BF16, uint16_t>(a, L, stream);

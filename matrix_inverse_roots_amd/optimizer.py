@@ -247,7 +247,8 @@ class Shampoo:
         rounded to bfloat16 for the products).  The parameter's gradient goes
         to a buffer of the optimizer's gradient type, which the next ``step``
         takes where its gradient is given as None; calls before that step add
-        to it (micro-batches: give each its share in ``scale``).  dhidden
+        to it (micro-batches: give each its share in ``scale``), and a step
+        that is given another gradient there drops it.  dhidden
         receives hidden's gradient.  Float32 hidden needs float32 gradients.
         logits_dtype=torch.float8_e4m3fn takes the logits from the 8-bit
         product of hidden and the parameter.

@@ -213,3 +213,43 @@ def test_network_step_in_8_bits(mir):
         opt.step([dw, None])
         assert all(torch.isfinite(w).all() and not torch.equal(w, b) for w, b in zip(W, before))
         log(f"step {step}: loss {loss.item():.4f}")
+
+
+def test_workspaces_belong_to_the_stream_that_uses_them(mir):
+    """Calls on a side stream that allocate for themselves, with allocations of
+    the same sizes filled on the current stream right behind them."""
+    import torch
+    h, w, t = make(1500, 512, 20001, "bfloat16", 3)
+    a = mir.shampoo_quantize_f8(h[:64].repeat(1, 16))
+    sizes = [mir.shampoo_linear_xent_workspace(h, w, t, h, w) // 4, mir.shampoo_matmul_f8_workspace(1, 64, 64, 8192) // 4]
+    assert min(sizes) > 0
+    want = []
+    for stream in (None, torch.cuda.Stream()):
+        dh, dw = torch.empty_like(h), torch.empty_like(w)
+        c = torch.empty((64, 64), device="cuda")
+        for k in range(3):
+            torch.cuda.synchronize()
+            loss = mir.shampoo_linear_xent(h, w, t, dhidden=dh, dweight=dw, stream=stream)
+            mir.shampoo_matmul_f8(*a, *a, c, stream=stream)
+            junk = [torch.full((n,), float("nan"), device="cuda") for n in sizes for _ in range(2)]
+            torch.cuda.synchronize()
+            del junk
+        want.append([x.clone() for x in (loss, dh, dw, c)])
+    assert all(torch.equal(x, y) for x, y in zip(*want))
+
+
+def test_two_calls_at_once(mir):
+    """Two streams, each with its own call in flight, give the bits of one after the other."""
+    import torch
+    data = [make(700, 256, 9001, "bfloat16", k) for k in range(2)]
+    out = []
+    for streams in ((None, None), (torch.cuda.Stream(), torch.cuda.Stream())):
+        torch.cuda.synchronize()
+        got = []
+        for (h, w, t), s in zip(data, streams):
+            dh, dw = torch.empty_like(h), torch.empty_like(w)
+            torch.cuda.synchronize() if s is None else None
+            got += [mir.shampoo_linear_xent(h, w, t, dhidden=dh, dweight=dw, stream=s), dh, dw]
+        torch.cuda.synchronize()
+        out.append(got)
+    assert all(torch.equal(x, y) for x, y in zip(*out))

@@ -75,6 +75,7 @@ def product(mir, **kw):
     (dict(M=1 << 23), 2), (dict(adt=0), 2), (dict(bdt=2), 2), (dict(cdt=3), 2), (dict(cdt=4), 2), (dict(arb=64), 2),
     (dict(brb=0), 2), (dict(a=None), 1), (dict(sb=None), 1), (dict(c=None), 1), (dict(a=P + 8), 1), (dict(sa=P + 1), 1),
     (dict(c=P + 2), 1), (dict(M=64, N=64, K=8192), 3), (dict(M=64, N=64, K=8192, ws=P, wsb=100), 3),
+    (dict(M=64, N=64, K=8192, ws=P + 64, wsb=1 << 30), 3),
 ])
 def test_product_refusals(mir, kw, status):
     assert product(mir, **kw) == status
@@ -117,9 +118,10 @@ def test_xent_refusals_of_both_calls(mir, kw, status):
 
 @pytest.mark.parametrize("kw,status", [
     (dict(hidden=None), 1), (dict(weight=None), 1), (dict(targets=None), 1), (dict(loss=None), 1), (dict(ld_hidden=63), 1),
-    (dict(ld_weight=0), 1), (dict(dhidden=P, ld_dhidden=32), 1), (dict(dweight=P, ld_dweight=32), 1),
+    (dict(ld_weight=0), 1), (dict(dhidden=2 * P, ld_dhidden=32), 1), (dict(dweight=2 * P, ld_dweight=32), 1),
     (dict(hidden=P + 1), 1), (dict(targets=P + 4), 1), (dict(loss=P + 2), 1), (dict(lse=P + 1), 1), (dict(row_scale=P + 2), 1),
-    (dict(dweight=P + 2, dweight_dt=0), 1), (dict(weight=P + 2, weight_dt=0), 1),
+    (dict(dweight=2 * P + 2, dweight_dt=0), 1), (dict(weight=P + 2, weight_dt=0), 1),
+    (dict(dhidden=P), 1), (dict(dweight=P), 1), (dict(dhidden=P, hidden=P, dweight=2 * P), 1),
     (dict(ws=None), 3), (dict(ws_bytes=100), 3), (dict(ws=P + 16), 3),
 ])
 def test_xent_refusals_of_the_call(mir, kw, status):
