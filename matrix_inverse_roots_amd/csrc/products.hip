@@ -278,7 +278,7 @@ shampoo_status matmul_f8_impl(const void* a, int a_dt, const void* sa, int32_t a
 // softmax cross entropy
 // ---------------------------------------------------------------------------
 constexpr int64_t XENT_MAX_ROW = int64_t(1) << 20;  // elements: 256 rows stay within 32-bit offsets
-constexpr int64_t XENT_PANEL_BYTES = int64_t(1) << 31;
+constexpr int64_t XENT_PANEL_BYTES = int64_t(9) << 28;
 constexpr int64_t XENT_STATS_BYTES = int64_t(1) << 28;
 
 struct XentLayout {
@@ -309,11 +309,18 @@ shampoo_status xent_layout(const shampoo_xent_args* a, XentLayout* L) {
   L->grads = a->dhidden || a->dweight;
   L->pieces = (a->V + 127) / 128;
   L->ldE = L->pieces * 128;
+  // rows a large power of two apart fall on the same cache channels (131072
+  // bfloat16 columns: the weight's gradient fetches 15.9 instead of 23.5 GB, the
+  // call 21.20 instead of 21.29 ms; at 32768 columns 167 instead of 165 us)
+  if (L->ldE * es % 131072 == 0) L->ldE += 128;
   int64_t rows = a->panel_rows;
   if (rows == 0) {
     rows = XENT_STATS_BYTES / (L->pieces * 8);
     if (L->grads) rows = std::min(rows, XENT_PANEL_BYTES / (L->ldE * es));
-    rows = std::max<int64_t>(rows / 256 * 256, 256);
+    rows = std::min<int64_t>(std::max<int64_t>(rows / 256 * 256, 256), 131072);
+    // panels of one size rather than a short last one
+    const int64_t count = (a->N + rows - 1) / rows;
+    if (count > 1) rows = up((a->N + count - 1) / count, 256);
   }
   rows = std::min<int64_t>(rows, 131072);
   L->panel = std::max<int64_t>(std::min(rows, a->N), 1);

@@ -307,3 +307,45 @@ def test_captured_and_replayed(mir):
         work()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, (loss, dh, dw, c)))
+
+
+def test_default_panels_of_a_long_batch(mir):
+    """More rows than one default panel holds (float32, a wide vocabulary):
+    equal panels, against float64 within the bounds of `definition`, which are
+    formed on the device here.  (A sum of 131072 float32 terms may be off by
+    131072 2^-23 of the sum of their magnitudes; the results of panels of 0,
+    700 and 5200 rows differ among themselves by 1e-5 of their size, as
+    a plain float32 product does from float64.)"""
+    import torch
+    N, d, V = 5200, 16, 131072
+    h, w, t = make(N, d, V, "float32", 13)
+    x, W = h.double(), w.double()
+    keep = t != -100
+    n = int(keep.sum())
+    dw, dw_err, loss, loss_err = torch.zeros_like(W), torch.zeros_like(W), 0.0, 0.0
+    dh, dh_err = torch.zeros_like(x), torch.zeros_like(x)
+    for r in range(0, N, 650):
+        X, k = x[r:r + 650], keep[r:r + 650].double()
+        at = t[r:r + 650].clamp(min=0)
+        rows = torch.arange(len(at), device="cuda")
+        z = X @ W.t()
+        wide = (d + 1) * U * (X.abs() @ W.abs().t()).amax(dim=1)
+        lse = torch.logsumexp(z, dim=1)
+        zt = z[rows, at]
+        loss += float(((lse - zt) * k).sum()) / n
+        loss_err += float(((2 * wide + 160 * U + 4 * U * (lse.abs() + zt.abs())) * k).sum()) / n
+        P = torch.softmax(z, dim=1)
+        dP = P * (2 * wide + 160 * U + 2 * U * lse.abs() + 2.1 * U)[:, None]
+        P[rows, at] -= 1.0
+        dP[rows, at] += U * P[rows, at].abs()
+        P, dP = P * (k / n)[:, None], dP * (k / n)[:, None]
+        A = P.abs() + dP
+        dh[r:r + 650], dh_err[r:r + 650] = P @ W, dP @ W.abs() + (V + 8) * U * (A @ W.abs())
+        dw += P.t() @ X
+        dw_err += dP.t() @ X.abs() + (N + 8) * U * (A.t() @ X.abs())
+    for panel in (0, 700):
+        gh, gw = torch.empty_like(h), torch.empty_like(w)
+        got = mir.shampoo_linear_xent(h, w, t, dhidden=gh, dweight=gw, panel_rows=panel)
+        assert abs(got.item() - loss) <= loss_err + U * abs(loss)
+        assert ((gh.double() - dh).abs() <= 1.01 * dh_err + U * dh.abs()).all()
+        assert ((gw.double() - dw).abs() <= 1.01 * dw_err + U * dw.abs()).all()
