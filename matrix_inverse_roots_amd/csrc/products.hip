@@ -408,7 +408,14 @@ shampoo_status run_xent(const shampoo_xent_args* a, const XentLayout& L, hipStre
       r = quantize_f8_impl(a->weight, a->weight_dt, 1, V, d, a->ld_weight, 0, SHAMPOO_E4M3, 1, w + L.wq, w + L.wsc, nullptr, nullptr, st);
     if (r != SHAMPOO_OK) return r;
   }
-  if (mean) {
+  // one panel: the reduction counts, ahead of the gradients' products
+  const bool single = N <= L.panel;
+  auto reduce = [&]() -> hipError_t {
+    hipLaunchKernelGGL(xent_reduce_kernel, dim3(1), dim3(1024), 0, st, rows, mean && single ? a->targets : nullptr, (int)N, a->ignore_index,
+                       mean && N > 0 ? inv_count : nullptr, a->loss);
+    return hipGetLastError();
+  };
+  if (mean && !single) {
     hipLaunchKernelGGL(xent_count_kernel, dim3(1), dim3(1024), 0, st, a->targets, (int)N, a->ignore_index, inv_count);
     LAUNCH_CHECK("xent_count");
   }
@@ -444,6 +451,7 @@ shampoo_status run_xent(const shampoo_xent_args* a, const XentLayout& L, hipStre
                                   : (M <= 256 ? xent_rows_kernel<1, TE> : xent_rows_kernel<32, TE>);
     hipLaunchKernelGGL(rows_kernel, dim3((unsigned)(M <= 256 ? M : (M + 31) / 32)), dim3(1024), 0, st, ra);
     LAUNCH_CHECK("xent_rows");
+    if (single && !each) HIP_TRY(reduce());
     if (!L.grads) continue;
     GradArgs ga{w + L.E, L.ldE, (const floatx2_t*)stats, logit, lse, a->targets + r0, a->row_scale ? a->row_scale + r0 : nullptr,
                 a->ignore_index, (int)M, (int)V, (int)L.pieces};
@@ -476,11 +484,12 @@ shampoo_status run_xent(const shampoo_xent_args* a, const XentLayout& L, hipStre
     }
   }
   if (L.dw_sum) HIP_TRY(sum_splits((const float*)(w + L.dw), 1, 0, dw, 1, (int)V, (int)d, st));
-  if (N == 0 && a->dweight) HIP_TRY(sum_splits(nullptr, 0, 0, dw, 1, (int)V, (int)d, st));  // zeros (or unchanged)
-  if (!each) {
-    hipLaunchKernelGGL(xent_reduce_kernel, dim3(1), dim3(1024), 0, st, rows, (int)N, mean ? inv_count : nullptr, a->loss);
-    LAUNCH_CHECK("xent_reduce");
+  if (N == 0 && a->dweight) {  // zeros (or unchanged)
+    Out none = dw;
+    none.alpha_dev = nullptr;
+    HIP_TRY(sum_splits(nullptr, 0, 0, none, 1, (int)V, (int)d, st));
   }
+  if (!each && (!single || N == 0)) HIP_TRY(reduce());
   return SHAMPOO_OK;
 }
 

@@ -18,7 +18,7 @@ namespace shampoo {
 
 typedef float floatx2_t __attribute__((ext_vector_type(2)));
 
-// out[0] = number of rows whose target is kept, as 1 / max(count, 1)
+// 1 / max(number of rows whose target is kept, 1)
 __global__ __launch_bounds__(1024) void xent_count_kernel(const int64_t* __restrict__ targets, int N, int64_t ignore,
                                                           float* __restrict__ inv_count) {
   __shared__ int red[16];
@@ -154,19 +154,37 @@ __global__ __launch_bounds__(1024) void xent_rows_kernel(RowArgs g) {
   }
 }
 
-// sum of the row losses (float64, fixed order), times 1 / count for the mean
-__global__ __launch_bounds__(1024) void xent_reduce_kernel(const float* __restrict__ rows, int N, const float* __restrict__ inv_count,
-                                                           float* __restrict__ out) {
+// Sum of the row losses (float64, fixed order), times 1 / count for the mean
+// (inv_count not null): read from there, or, with `targets`, counted here and
+// left there, which saves a call of one panel the counting launch.
+__global__ __launch_bounds__(1024) void xent_reduce_kernel(const float* __restrict__ rows, const int64_t* __restrict__ targets, int N,
+                                                           int64_t ignore, float* __restrict__ inv_count, float* __restrict__ out) {
   __shared__ double red[16];
+  __shared__ int kept[16];
   double a = 0.0;
-  for (int i = threadIdx.x; i < N; i += 1024) a += (double)rows[i];
+  int c = 0;
+  for (int i = threadIdx.x; i < N; i += 1024) {
+    a += (double)rows[i];
+    if (targets) c += targets[i] != ignore;
+  }
 #pragma unroll
-  for (int d = 1; d < 64; d *= 2) a += __shfl_xor(a, d);
-  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = a;
+  for (int d = 1; d < 64; d *= 2) {
+    a += __shfl_xor(a, d);
+    c += __shfl_xor(c, d);
+  }
+  if ((threadIdx.x & 63) == 0) {
+    red[threadIdx.x >> 6] = a;
+    kept[threadIdx.x >> 6] = c;
+  }
   __syncthreads();
   if (threadIdx.x == 0) {
     double t = 0.0;
-    for (int w = 0; w < 16; ++w) t += red[w];
+    int k = 0;
+    for (int w = 0; w < 16; ++w) {
+      t += red[w];
+      k += kept[w];
+    }
+    if (targets) *inv_count = 1.0f / (float)max(k, 1);
     *out = (float)(inv_count ? t * (double)*inv_count : t);
   }
 }
