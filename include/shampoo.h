@@ -497,7 +497,8 @@ shampoo_status shampoo_matmul_f8(const void* a, shampoo_dtype a_dt, const void* 
  *
  * z = hidden weight^T (hidden [N, d], weight [V, d]), and for row i with
  * target t_i:  loss_i = log sum_v exp z_iv - z_it, and 0 for a row with t_i ==
- * ignore_index, whose gradient is 0 too.  With g_i = scale row_scale_i, SUM
+ * ignore_index, whose gradient is 0 too, whatever its row of hidden and its
+ * row_scale hold (NaN and infinities included).  With g_i = scale row_scale_i, SUM
  * gives sum_i g_i loss_i and MEAN that over the number of kept rows (0 if
  * there are none).  NONE gives the loss_i themselves, and g_i is the gradient
  * that arrives at them.  Gradients (g_i over the count for MEAN):

@@ -285,7 +285,7 @@ struct XentLayout {
   int64_t panel, pieces, ldE, dp;
   int64_t Kp, Ks;  // 8-bit logits: padded width, scales of a row
   bool f8, grads, copy_hidden, copy_weight, dw_sum;  // dw_sum: float32 sum of the panels' bfloat16 gradients
-  size_t count, stats, logit, lse, rows, E, hidden, weight, hq, hs, wq, wsc, part, dw, total;
+  size_t count, stats, logit, lse, rows, E, hidden, kept, weight, hq, hs, wq, wsc, part, dw, total;
   Shape dx, dwp;
 };
 
@@ -349,6 +349,8 @@ shampoo_status xent_layout(const shampoo_xent_args* a, XentLayout* L) {
   L->rows = take((size_t)std::max<int64_t>(a->N, 1) * 4);
   L->E = take(L->grads ? (size_t)L->panel * L->ldE * es : 0);
   L->hidden = take(L->copy_hidden ? (size_t)a->N * L->dp * es : 0);
+  // hidden's rows with the ignored ones zeroed: a panel's, or the copy in place
+  L->kept = take(a->dweight && !L->copy_hidden ? (size_t)L->panel * L->dp * es : 0);
   L->weight = take(L->copy_weight ? (size_t)a->V * L->dp * es : 0);
   L->hq = take(L->f8 ? a->N * L->Kp : 0);
   L->hs = take(L->f8 ? a->N * L->Ks : 0);
@@ -453,9 +455,11 @@ shampoo_status run_xent(const shampoo_xent_args* a, const XentLayout& L, hipStre
     LAUNCH_CHECK("xent_rows");
     if (single && !each) HIP_TRY(reduce());
     if (!L.grads) continue;
+    const int first = (int)((L.ldE + 2047) / 2048), more = a->dweight ? (int)((d + 2047) / 2048) : 0;
+    unsigned char* kept = L.copy_hidden ? w + L.hidden + r0 * L.dp * es : w + L.kept;
     GradArgs ga{w + L.E, L.ldE, (const floatx2_t*)stats, logit, lse, a->targets + r0, a->row_scale ? a->row_scale + r0 : nullptr,
-                a->ignore_index, (int)M, (int)V, (int)L.pieces};
-    hipLaunchKernelGGL((xent_grad_kernel<TE>), dim3((unsigned)((L.ldE + 2047) / 2048), (unsigned)((M + 3) / 4)), dim3(256), 0, st, ga);
+                a->ignore_index, (int)M, (int)V, (int)L.pieces, hidden + r0 * ldh * es, ldh, kept, L.dp, (int)d, first};
+    hipLaunchKernelGGL((xent_grad_kernel<TE>), dim3((unsigned)(first + more), (unsigned)((M + 3) / 4)), dim3(256), 0, st, ga);
     LAUNCH_CHECK("xent_grad");
     float* part = (float*)(w + L.part);
     if (a->dhidden) {
@@ -476,7 +480,7 @@ shampoo_status run_xent(const shampoo_xent_args* a, const XentLayout& L, hipStre
       Shape s = plan_shape(1, V, d, M, (int)es, true);
       if (partial_bytes(s, 1, V, d) > partial_bytes(L.dwp, 1, V, d)) s = plan_shape(1, V, d, M, (int)es, false);
       ProductArgs p{};
-      p.A = w + L.E; p.B = hidden + r0 * ldh * es; p.lda = L.ldE; p.ldb = ldh;
+      p.A = w + L.E; p.B = kept; p.lda = L.ldE; p.ldb = L.dp;
       p.M = (int)V; p.N = (int)d; p.K = (int)M;
       point_output(p, s, o, part, 1);
       HIP_TRY((product<E, true, true, Epi::STORE>(p, s, st)));

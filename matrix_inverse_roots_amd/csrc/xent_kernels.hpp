@@ -199,12 +199,20 @@ struct GradArgs {
   const float* row_scale;
   int64_t ignore;
   int M, V, pieces;
+  const void* hidden;         // [M][ldh], 16-byte aligned rows
+  int64_t ldh;
+  void* kept;                 // [M][ldk]; may be hidden itself
+  int64_t ldk;
+  int d, first;               // d entries, by the workgroups from `first` on
 };
 
 // P from E, in place: a workgroup of 4 waves takes 4 rows x 2048 columns, 16
 // bytes a lane at a time.  Bound by memory: 8192 x 131072 (2.1 GB read and
 // written) 0.76 ms = 5.6 TB/s.  It cannot join the product that makes E: a
 // row's lse is known only after all of its pieces.  T: float, or uint16_t for bfloat16.
+// Workgroups from `first` on leave hidden's rows for the weight's gradient,
+// zeros where the target is ignored: a zero of P times a NaN or an infinity in
+// a padding row would be NaN in every row of that gradient.
 template <typename T>
 __global__ __launch_bounds__(256) void xent_grad_kernel(GradArgs g) {
   constexpr int VE = 16 / sizeof(T);
@@ -212,6 +220,17 @@ __global__ __launch_bounds__(256) void xent_grad_kernel(GradArgs g) {
   if (m >= g.M) return;
   const int64_t t = g.targets[m];
   const bool skip = t == g.ignore, bad = !skip && (t < 0 || t >= g.V);
+  if ((int)blockIdx.x >= g.first) {
+    const T* from = reinterpret_cast<const T*>(g.hidden) + (int64_t)m * g.ldh;
+    T* to = reinterpret_cast<T*>(g.kept) + (int64_t)m * g.ldk;
+    if (!skip && from == to) return;
+#pragma unroll
+    for (int u = 0; u < 2048 / (64 * VE); ++u) {
+      const int c = ((int)blockIdx.x - g.first) * 2048 + (u * 64 + lane) * VE;
+      if (c < g.d) *reinterpret_cast<u32x4*>(to + c) = skip ? u32x4{0, 0, 0, 0} : *reinterpret_cast<const u32x4*>(from + c);
+    }
+    return;
+  }
   // 1 / count and the caller's scale wait for the products' float32 results:
   // here they would round every -1 of an unlikely target the same way
   float w = g.row_scale ? g.row_scale[m] : 1.f;

@@ -349,3 +349,31 @@ def test_default_panels_of_a_long_batch(mir):
         assert abs(got.item() - loss) <= loss_err + U * abs(loss)
         assert ((gh.double() - dh).abs() <= 1.01 * dh_err + U * dh.abs()).all()
         assert ((gw.double() - dw).abs() <= 1.01 * dw_err + U * dw.abs()).all()
+
+
+@pytest.mark.parametrize("dt", ["float32", "bfloat16"])
+@pytest.mark.parametrize("N,d,V,panel", [(90, 64, 300, 0), (90, 64, 300, 32), (300, 33, 700, 0), (300, 33, 700, 100), (70, 2200, 257, 0)])
+def test_ignored_rows_may_hold_anything(mir, dt, N, d, V, panel):
+    """NaN and infinities in ignored rows (padding) reach no gradient and no
+    loss: bit for bit what zeros there give.  The rows themselves stay as
+    they were, and dhidden's are zero."""
+    import torch
+    h, w, t = make(N, d, V, dt, 14)
+    t[5] = -100
+    skip = t == -100
+    got = []
+    for fill in (0.0, float("nan"), float("inf"), -float("inf")):
+        x = h.clone()
+        x[skip] = fill
+        before = x.clone()
+        rs = torch.ones(N, device="cuda")
+        rs[skip] = fill
+        for kind in ((None, torch.float8_e4m3fn) if dt == "bfloat16" else (None,)):
+            dh, dw = torch.full_like(h, 7.0), torch.full_like(w, 7.0)
+            loss = mir.shampoo_linear_xent(x, w, t, dhidden=dh, dweight=dw, row_scale=rs, panel_rows=panel, logits_dtype=kind)
+            assert torch.equal(x.view(torch.uint8), before.view(torch.uint8))
+            assert not dh[skip].any()
+            got.append((kind, loss, dh, dw))
+    for kind, *r in got:
+        first = next(g for g in got if g[0] == kind)[1:]
+        assert all(torch.isfinite(a).all() and torch.equal(a, b) for a, b in zip(r, first))
