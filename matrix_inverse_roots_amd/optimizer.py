@@ -15,7 +15,7 @@ import math
 import numpy as np
 
 from . import (RootOpts, StepArgsC, GRAFTS, FALLBACKS, F32, F64, BF16, shampoo_linear_xent,
-               shampoo_plan_blocks, shampoo_step, shampoo_step_workspace, table_to_device, _ptr)
+               shampoo_plan_blocks, shampoo_step, shampoo_step_workspace, table_to_device, _empty, _ptr)
 
 
 def reshape_2d(shape):
@@ -265,7 +265,7 @@ class Shampoo:
         fresh = index not in self._pending
         dw = self._kept.get(index)
         if dw is None:
-            dw = torch.empty(w.shape, dtype=gdt, device=self.device)
+            dw = _empty(w.shape, gdt, self.device, stream)
         loss = shampoo_linear_xent(hidden, w, targets, dhidden=dhidden, dweight=dw, row_scale=row_scale,
                                    ignore_index=ignore_index, reduction=reduction, scale=scale,
                                    accumulate=not fresh, panel_rows=panel_rows, logits_dtype=logits_dtype,

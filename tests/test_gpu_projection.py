@@ -253,3 +253,25 @@ def test_two_calls_at_once(mir):
         torch.cuda.synchronize()
         out.append(got)
     assert all(torch.equal(x, y) for x, y in zip(*out))
+
+
+def test_kept_gradient_belongs_to_its_stream(mir):
+    """The kept gradient's first call on a side stream, while the current
+    stream still fills memory of that size that it has given back."""
+    import torch
+    h, w, t = make(300, 64, 5001, "bfloat16", 5)
+    want = torch.empty_like(w)
+    mir.shampoo_linear_xent(h, w.float(), t, dweight=want)
+    side = torch.cuda.Stream()
+    for k in range(3):
+        opt = mir.Shampoo([w.float()], block_size=64, grad_dtype=torch.bfloat16)
+        torch.cuda.synchronize()
+        busy = torch.empty((64, 1 << 20), device="cuda")
+        junk = torch.empty_like(w)
+        for _ in range(20):
+            busy.fill_(1.0)
+        junk.fill_(float("nan"))
+        del junk
+        opt.projection_loss(0, h, t, stream=side)
+        torch.cuda.synchronize()
+        assert torch.equal(opt._kept[0], want)
