@@ -92,6 +92,8 @@ struct ProductArgs {
   int64_t items;                      // batch * splits * mt * nt
   // SOFTMAX
   floatx2* stats;                     // [pieces][M]: (max, sum of exp(z - max)) of 128 columns
+  const int64_t* targets;             // [M]
+  float* target_logit;                // [M]: the logit at each row's target, where that is a column
 };
 
 template <Elem E> struct ElemTraits;
@@ -173,6 +175,10 @@ __device__ __forceinline__ rsrc_t rsrc_of(const unsigned char* p, uint32_t bytes
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<unsigned char*>(p), 0, bytes, RSRC_FLAGS);
 }
 
+// Groups of scales (or targets) in LDS: for the current stage and the NB (NB +
+// 1) ahead, a power of two.
+constexpr int scale_groups(int nb) { return nb > 2 ? 8 : 4; }
+
 template <Elem E, int FM, int FN, int WM, int WN, int NB, bool AS, bool BS, Epi EPI, int FA, int FB>
 __global__ __launch_bounds__(64 * WM * WN, 2) void product_kernel(ProductArgs g) {
   constexpr int ES = ElemTraits<E>::size;
@@ -181,12 +187,15 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_kernel(ProductArgs g)
   constexpr int NIA = TM / 8 / W, NIB = TN / 8 / W;
   constexpr int SK = 128 / ES;  // k of one stage
   constexpr bool SCALED = E == Elem::F8 || E == Elem::F8W;
-  // LDS: NB buffers, then groups of scales (a group each for NB stages ahead at most, and the current one)
-  constexpr int NI = NIA + NIB, NG = NB > 2 ? 8 : 4, SCALES = NB * STAGE, SGROUP = 4 * (TM + TN);
+  // LDS: NB buffers, then groups of scales (a group each for NB stages ahead at
+  // most, and the current one), then as many groups of targets
+  constexpr int NI = NIA + NIB, NG = scale_groups(NB), SCALES = NB * STAGE, SGROUP = 4 * (TM + TN);
+  constexpr int TARGETS = SCALES + (SCALED ? NG * SGROUP : 0);
   static_assert(NB == 2 || NB == 4, "buffers are counted with masks");
   static_assert(NIA * W * 8 == TM && NIB * W * 8 == TN, "loads divide among the waves");
   static_assert(!SCALED || (!AS && !BS), "8-bit operands are k-contiguous");
   static_assert(!SCALED || (TM + TN) % (64 * W) == 0, "each wave loads the scales of as many rows");
+  static_assert(TM % 64 == 0 && TM <= 64 * W, "a wave loads the targets of 64 rows");
   static_assert(!(AS && TM < 64) && !(BS && TN < 64), "k-strided swizzles need 64 columns");
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
   typedef __attribute__((address_space(3))) unsigned char lds_u8;
@@ -294,6 +303,15 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_kernel(ProductArgs g)
     // bytes); columns past the tile's read what follows, and nothing past that
     endA = AS ? (g.K - 1) * g.lda * ES + (((g.M - ra) * ES + 15) & ~15) - ka : (g.M - 1 - ra) * g.lda * ES + Kb - ka;
     endB = BS ? (g.K - 1) * g.ldb * ES + (((g.N - rb) * ES + 15) & ~15) - kb : (g.N - 1 - rb) * g.ldb * ES + Kb - kb;
+    if constexpr (EPI == Epi::SOFTMAX) {
+      // the low halves of the rows' targets (a column fits; what else matches
+      // one there, the row pass does not read), ahead of the item's first
+      // stage and waited for with it: one item more than there are buffers
+      if (wave * 64 < TM) {
+        const int64_t* p = g.targets + min(ra + wave * 64 + lane, g.M - 1);
+        __builtin_amdgcn_global_load_lds((const void*)p, (void*)(smem + TARGETS + ((lit & (NG - 1)) * TM + wave * 64) * 4), 4, 0, 0);
+      }
+    }
   };
   // one stage into its buffer (zeros once every item's stages are issued)
   auto issue = [&]() {
@@ -579,6 +597,10 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_kernel(ProductArgs g)
       // where the caller wants gradients
       static_assert(FN == 4 || EPI != Epi::SOFTMAX, "a piece is 128 columns");
       constexpr float L2E = 1.4426950408889634f;
+      uint32_t target[FM];
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+        target[i] = reinterpret_cast<const uint32_t*>(smem + TARGETS)[(it & (NG - 1)) * TM + (wm * FM + i) * 32 + el32];
 #pragma unroll
       for (int i = 0; i < FM; ++i) {
         const int m = m0 + 32 * i + el32;
@@ -589,6 +611,19 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_kernel(ProductArgs g)
 #pragma unroll
             for (int v = 0; v < 16; ++v)
               if (32 * j + 8 * (v >> 2) + (v & 3) >= edge) acc[i][j][v] = -INFINITY;
+        }
+        // The target's logit: the very number that enters the row's sum, so
+        // that its rounding drops out of the loss.  One piece of a row has it.
+        const uint32_t col = target[i] - (uint32_t)n0;
+        const bool here = col < 128u && (int)(col >> 2 & 1) == ehalf && m < g.M;
+        if (__any(here)) {
+          float zt = 0.f;
+#pragma unroll
+          for (int j = 0; j < FN; ++j)
+#pragma unroll
+            for (int v = 0; v < 16; ++v)
+              if ((col & ~4u) == 32u * j + 8 * (v >> 2) + (v & 3)) zt = acc[i][j][v];
+          if (here) g.target_logit[m] = zt;
         }
         float mx = -INFINITY;
 #pragma unroll

@@ -66,7 +66,8 @@ Shape plan_shape(int64_t batch, int64_t M, int64_t N, int64_t K, int es, bool ma
 template <Elem E, int FM, int FN, int WM, int WN, int NB, int PER_CU, bool AS, bool BS, Epi EPI, int FA, int FB>
 hipError_t launch_tiles(ProductArgs g, int64_t batch, hipStream_t st) {
   constexpr int TM = 32 * FM * WM, TN = 32 * FN * WN;
-  constexpr int LDS = NB * (TM + TN) * 128 + (E == Elem::F8 || E == Elem::F8W ? (NB > 2 ? 32 : 16) * (TM + TN) : 0);  // stages, groups of scales
+  constexpr int LDS = NB * (TM + TN) * 128 +  // stages, groups of scales, groups of targets
+                      4 * scale_groups(NB) * ((E == Elem::F8 || E == Elem::F8W ? TM + TN : 0) + (EPI == Epi::SOFTMAX ? TM : 0));
   const auto kernel = product_kernel<E, FM, FN, WM, WN, NB, AS, BS, EPI, FA, FB>;
   static bool ready[MAX_DEVICES] = {false};
   int dev = 0, cus = 0;
@@ -285,7 +286,7 @@ struct XentLayout {
   int64_t panel, pieces, ldE, dp;
   int64_t Kp, Ks;  // 8-bit logits: padded width, scales of a row
   bool f8, grads, copy_hidden, copy_weight, dw_sum;  // dw_sum: float32 sum of the panels' bfloat16 gradients
-  size_t count, stats, logit, lse, rows, E, hidden, kept, weight, hq, hs, wq, wsc, part, dw, total;
+  size_t count, stats, nll, norm, rows, E, hidden, kept, weight, hq, hs, wq, wsc, part, dw, total;
   Shape dx, dwp;
 };
 
@@ -344,8 +345,8 @@ shampoo_status xent_layout(const shampoo_xent_args* a, XentLayout* L) {
   };
   L->count = take(4);
   L->stats = take((size_t)L->pieces * L->panel * 8);
-  L->logit = take((size_t)L->panel * 4);
-  L->lse = take((size_t)L->panel * 4);
+  L->nll = take((size_t)L->panel * 4);
+  L->norm = take((size_t)L->panel * 8);
   L->rows = take((size_t)std::max<int64_t>(a->N, 1) * 4);
   L->E = take(L->grads ? (size_t)L->panel * L->ldE * es : 0);
   L->hidden = take(L->copy_hidden ? (size_t)a->N * L->dp * es : 0);
@@ -379,7 +380,8 @@ shampoo_status run_xent(const shampoo_xent_args* a, const XentLayout& L, hipStre
   const int64_t es = sizeof(T);
   float* inv_count = (float*)(w + L.count);
   floatx2* stats = (floatx2*)(w + L.stats);
-  float* logit = (float*)(w + L.logit);
+  float* nll = (float*)(w + L.nll);
+  floatx2_t* norm = (floatx2_t*)(w + L.norm);
   const bool mean = a->reduction == SHAMPOO_REDUCE_MEAN, each = a->reduction == SHAMPOO_REDUCE_NONE;
   float* rows = each ? a->loss : (float*)(w + L.rows);
   const unsigned char* hidden = (const unsigned char*)a->hidden;
@@ -435,6 +437,8 @@ shampoo_status run_xent(const shampoo_xent_args* a, const XentLayout& L, hipStre
     g.C = L.grads ? w + L.E : nullptr;
     g.ldc = L.ldE;
     g.stats = stats;
+    g.targets = a->targets + r0;
+    g.target_logit = nll;
     if (L.f8) {
       g.A = w + L.hq + r0 * L.Kp; g.sa = w + L.hs + r0 * L.Ks;
       g.B = w + L.wq; g.sb = w + L.wsc;
@@ -445,19 +449,16 @@ shampoo_status run_xent(const shampoo_xent_args* a, const XentLayout& L, hipStre
     } else {
       HIP_TRY((product<E, false, false, Epi::SOFTMAX>(g, plan_shape(1, M, V, d, (int)es, false), st)));
     }
-    float* lse = a->lse ? a->lse + r0 : (float*)(w + L.lse);
-    RowArgs ra{(const floatx2_t*)stats, g.A, g.B, g.lda, g.ldb, g.sa, g.sb, L.Ks, g.K, logit, a->targets + r0,
-               a->row_scale && !each ? a->row_scale + r0 : nullptr, lse, rows + r0, a->ignore_index, (int)M, (int)V, (int)L.pieces,
-               each ? 1.f : a->scale};
-    const auto rows_kernel = L.f8 ? (M <= 256 ? xent_rows_kernel<1, uint8_t> : xent_rows_kernel<32, uint8_t>)
-                                  : (M <= 256 ? xent_rows_kernel<1, TE> : xent_rows_kernel<32, TE>);
-    hipLaunchKernelGGL(rows_kernel, dim3((unsigned)(M <= 256 ? M : (M + 31) / 32)), dim3(1024), 0, st, ra);
+    RowArgs ra{(const floatx2_t*)stats, nll, a->targets + r0, a->row_scale && !each ? a->row_scale + r0 : nullptr, norm,
+               a->lse ? a->lse + r0 : nullptr, rows + r0, a->ignore_index, (int)M, (int)V, (int)L.pieces, each ? 1.f : a->scale};
+    if (M <= 256) hipLaunchKernelGGL(xent_rows_kernel<1>, dim3((unsigned)M), dim3(1024), 0, st, ra);
+    else hipLaunchKernelGGL(xent_rows_kernel<32>, dim3((unsigned)((M + 31) / 32)), dim3(1024), 0, st, ra);
     LAUNCH_CHECK("xent_rows");
     if (single && !each) HIP_TRY(reduce());
     if (!L.grads) continue;
     const int first = (int)((L.ldE + 2047) / 2048), more = a->dweight ? (int)((d + 2047) / 2048) : 0;
     unsigned char* kept = L.copy_hidden ? w + L.hidden + r0 * L.dp * es : w + L.kept;
-    GradArgs ga{w + L.E, L.ldE, (const floatx2_t*)stats, logit, lse, a->targets + r0, a->row_scale ? a->row_scale + r0 : nullptr,
+    GradArgs ga{w + L.E, L.ldE, (const floatx2_t*)stats, nll, norm, a->targets + r0, a->row_scale ? a->row_scale + r0 : nullptr,
                 a->ignore_index, (int)M, (int)V, (int)L.pieces, hidden + r0 * ldh * es, ldh, kept, L.dp, (int)d, first};
     hipLaunchKernelGGL((xent_grad_kernel<TE>), dim3((unsigned)(first + more), (unsigned)((M + 3) / 4)), dim3(256), 0, st, ga);
     LAUNCH_CHECK("xent_grad");

@@ -2,11 +2,14 @@
 // are in product_core.hpp.
 //
 // With logits z = x W^T, the product's epilogue leaves for each row and each
-// piece of 128 columns the maximum m_j and s_j = sum exp(z - m_j), and, for
-// gradients, E = exp(z - m_j).  Then
-//     lse = M + log sum_j s_j exp(m_j - M),  M = max_j m_j,
-//     loss = lse - z_t,
-//     P = g (softmax - onehot) = E g exp(m_j - lse), and g (p_t - 1) at t.
+// piece of 128 columns the maximum m_j and s_j = sum exp(z - m_j), for the row
+// its target's logit z_t, and, for gradients, E = exp(z - m_j).  Then
+//     M = max_j m_j,  s = sum_j s_j exp(m_j - M),  lse = M + log s,
+//     loss = (M - z_t) + log s,
+//     P = g (softmax - onehot) = E g exp(m_j - M) / s, and g (exp(-loss) - 1) at t.
+// Nothing large is subtracted: M - z_t is a difference of two logits of the
+// same sum (zero where the target leads), s at least 1, so a loss is never
+// negative and keeps its digits where the target's probability is near one.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -37,34 +40,22 @@ __global__ __launch_bounds__(1024) void xent_count_kernel(const int64_t* __restr
 
 struct RowArgs {
   const floatx2_t* stats;      // [pieces][M]
-  const void* hidden;          // [M][ldh]
-  const void* weight;          // [V][ldw]
-  int64_t ldh, ldw;
-  const uint8_t* hs;           // 8-bit operands: their scales, lds bytes a row
-  const uint8_t* ws;
-  int64_t lds;
-  int d;
-  float* target_logit;         // [M]
+  float* nll;                  // [M]: the target's logit; replaced by -log of its probability
   const int64_t* targets;      // [M]
   const float* row_scale;      // [M] or null
-  float* lse;                  // [M]
+  floatx2_t* norm;             // [M]: (M, 1 / s)
+  float* lse;                  // [M] or null
   float* loss;                 // [M] (times row_scale and scale)
   int64_t ignore;
   int M, V, pieces;
   float scale;
 };
 
-// 8192 rows of 1024 pieces and 4096 entries: 42 us (a thread to each row's
-// whole dot product, uncoalesced, took 152).
 // R rows per workgroup of 1024 threads: thread t joins pieces t / R, + 1024 /
-// R, ... of row t % R.  The target's logit is a product of two rows of its
-// own, by 1024 / R threads: cheaper than to look for it among the logits in
-// the large product's epilogue.  T: float, uint16_t for bfloat16, or uint8_t
-// for 8-bit operands (d their padded width).
-template <int R, typename T>
+// R, ... of row t % R.
+template <int R>
 __global__ __launch_bounds__(1024) void xent_rows_kernel(RowArgs g) {
   __shared__ floatx2_t red[1024];
-  __shared__ float dots[R == 1 ? 16 : R];
   const int tid = threadIdx.x, lr = tid % R, grp = tid / R;
   constexpr int G = 1024 / R;
   const int m = blockIdx.x * R + lr;
@@ -78,49 +69,6 @@ __global__ __launch_bounds__(1024) void xent_rows_kernel(RowArgs g) {
       s = s * __expf(mx - ref) + v[1] * __expf(v[0] - ref);
       mx = nm;
     }
-  }
-  // z_t: a row to a wave (R rows), or the row to all waves (R = 1)
-  const int lane = tid & 63, wave = tid >> 6;
-  constexpr int STEP = R == 1 ? 1024 : 64, PER = R == 1 ? 1 : R / 16;
-#pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    const int row = blockIdx.x * R + (R == 1 ? 0 : wave * PER + i);
-    const int from = R == 1 ? tid : lane;
-    float dot = 0.f;
-    const int64_t t = row < g.M ? g.targets[row] : -1;
-    if (row < g.M && t != g.ignore && t >= 0 && t < g.V) {
-      const T* x = reinterpret_cast<const T*>(g.hidden) + row * g.ldh;
-      const T* w = reinterpret_cast<const T*>(g.weight) + t * g.ldw;
-      if constexpr (sizeof(T) == 1) {
-        const uint8_t* sx = g.hs + row * g.lds;
-        const uint8_t* sw = g.ws + t * g.lds;
-#pragma unroll 4
-        for (int k = from; k < g.d / 4; k += STEP) {
-          const uint32_t a = reinterpret_cast<const uint32_t*>(x)[k], b = reinterpret_cast<const uint32_t*>(w)[k];
-          float q = __builtin_amdgcn_cvt_f32_fp8(a, 0) * __builtin_amdgcn_cvt_f32_fp8(b, 0);
-          q += __builtin_amdgcn_cvt_f32_fp8(a, 1) * __builtin_amdgcn_cvt_f32_fp8(b, 1);
-          q += __builtin_amdgcn_cvt_f32_fp8(a, 2) * __builtin_amdgcn_cvt_f32_fp8(b, 2);
-          q += __builtin_amdgcn_cvt_f32_fp8(a, 3) * __builtin_amdgcn_cvt_f32_fp8(b, 3);
-          dot += ldexpf(q, (int)sx[k >> 5] + (int)sw[k >> 5] - 254);
-        }
-      } else {
-        // four elements a lane (operands of products start on 16 bytes, and
-        // a row's last run is whole or zeros follow it up to 8 elements)
-        struct Four { T v[4]; };
-#pragma unroll 4
-        for (int k = 4 * from; k < g.d; k += 4 * STEP) {
-          const Four a = *reinterpret_cast<const Four*>(x + k), b = *reinterpret_cast<const Four*>(w + k);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            if constexpr (sizeof(T) == 4) dot += a.v[e] * b.v[e];
-            else dot += __builtin_bit_cast(float, (uint32_t)a.v[e] << 16) * __builtin_bit_cast(float, (uint32_t)b.v[e] << 16);
-          }
-        }
-      }
-    }
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) dot += __shfl_xor(dot, d);
-    if (lane == 0) dots[R == 1 ? wave : wave * PER + i] = dot;
   }
   red[tid] = floatx2_t{mx, s};
   __syncthreads();
@@ -136,19 +84,15 @@ __global__ __launch_bounds__(1024) void xent_rows_kernel(RowArgs g) {
     __syncthreads();
   }
   if (grp == 0 && m < g.M) {
-    const float lse = mx + logf(s);
-    g.lse[m] = lse;
+    const float ls = logf(s);
+    g.norm[m] = floatx2_t{mx, 1.f / s};
+    if (g.lse) g.lse[m] = mx + ls;
     const int64_t t = g.targets[m];
-    float dot = dots[lr];
-    if constexpr (R == 1) {
-#pragma unroll
-      for (int k = 1; k < 16; ++k) dot += dots[k];
-    }
-    g.target_logit[m] = dot;
     float l = 0.f;
     if (t != g.ignore) {
-      l = t >= 0 && t < g.V ? lse - dot : __builtin_nanf("");
-      l *= g.scale * (g.row_scale ? g.row_scale[m] : 1.f);
+      const float nll = t >= 0 && t < g.V ? (mx - g.nll[m]) + ls : __builtin_nanf("");
+      g.nll[m] = nll;
+      l = nll * (g.scale * (g.row_scale ? g.row_scale[m] : 1.f));
     }
     g.loss[m] = l;
   }
@@ -193,8 +137,8 @@ struct GradArgs {
   void* E;                    // [M][ld], in place
   int64_t ld;
   const floatx2_t* stats;     // [pieces][M]
-  const float* target_logit;
-  const float* lse;
+  const float* nll;
+  const floatx2_t* norm;
   const int64_t* targets;
   const float* row_scale;
   int64_t ignore;
@@ -235,7 +179,7 @@ __global__ __launch_bounds__(256) void xent_grad_kernel(GradArgs g) {
   // here they would round every -1 of an unlikely target the same way
   float w = g.row_scale ? g.row_scale[m] : 1.f;
   if (bad) w = __builtin_nanf("");
-  const float lse = g.lse[m];
+  const floatx2_t norm = g.norm[m];
   T* row = reinterpret_cast<T*>(g.E) + (int64_t)m * g.ld;
 #pragma unroll
   for (int u = 0; u < 2048 / (64 * VE); ++u) {
@@ -243,7 +187,7 @@ __global__ __launch_bounds__(256) void xent_grad_kernel(GradArgs g) {
     if (c >= g.ld || c >= g.pieces * 128) continue;
     u32x4 out = u32x4{0, 0, 0, 0};
     if (!skip) {
-      const float f = w * __expf(g.stats[(int64_t)(c >> 7) * g.M + m][0] - lse);
+      const float f = w * (__expf(g.stats[(int64_t)(c >> 7) * g.M + m][0] - norm[0]) * norm[1]);
       const u32x4 in = *reinterpret_cast<const u32x4*>(row + c);
       struct Pack { T v[VE]; };
       Pack p = __builtin_bit_cast(Pack, in);
@@ -254,12 +198,8 @@ __global__ __launch_bounds__(256) void xent_grad_kernel(GradArgs g) {
         else y = __builtin_bit_cast(float, (uint32_t)p.v[e] << 16);
         // a piece of nothing (maximum -inf) holds zeros
         y = y == 0.f ? (f == f ? 0.f : f) : y * f;
-        if (c + e == t) {
-          // p_t - 1; from the float32 logit where the exponential is rounded,
-          // which would lose it where p_t is near one
-          if constexpr (sizeof(T) == 4) y -= w;
-          else y = w * expm1f(g.target_logit[m] - lse);
-        }
+        // p_t - 1 from the loss: the difference would lose it where p_t is near one
+        if (c + e == t) y = w * expm1f(-g.nll[m]);
         if (c + e >= g.V) y = 0.f;
         if constexpr (sizeof(T) == 4) p.v[e] = y;
         else p.v[e] = __builtin_bit_cast(uint16_t, (__bf16)y);
