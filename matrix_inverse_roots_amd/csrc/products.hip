@@ -412,11 +412,12 @@ shampoo_status run_xent(const shampoo_xent_args* a, const XentLayout& L, hipStre
       r = quantize_f8_impl(a->weight, a->weight_dt, 1, V, d, a->ld_weight, 0, SHAMPOO_E4M3, 1, w + L.wq, w + L.wsc, nullptr, nullptr, st);
     if (r != SHAMPOO_OK) return r;
   }
-  // one panel: the reduction counts, ahead of the gradients' products
-  const bool single = N <= L.panel;
+  // one panel: the reduction counts, ahead of the gradients' products (an
+  // empty batch has none, and nothing in it is read)
+  const bool single = N > 0 && N <= L.panel;
   auto reduce = [&]() -> hipError_t {
     hipLaunchKernelGGL(xent_reduce_kernel, dim3(1), dim3(1024), 0, st, rows, mean && single ? a->targets : nullptr, (int)N, a->ignore_index,
-                       mean && N > 0 ? inv_count : nullptr, a->loss);
+                       mean ? inv_count : nullptr, a->loss);
     return hipGetLastError();
   };
   if (mean && !single) {
@@ -494,7 +495,7 @@ shampoo_status run_xent(const shampoo_xent_args* a, const XentLayout& L, hipStre
     none.alpha_dev = nullptr;
     HIP_TRY(sum_splits(nullptr, 0, 0, none, 1, (int)V, (int)d, st));
   }
-  if (!each && (!single || N == 0)) HIP_TRY(reduce());
+  if (!each && !single) HIP_TRY(reduce());
   return SHAMPOO_OK;
 }
 

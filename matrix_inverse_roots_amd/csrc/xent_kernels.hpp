@@ -99,8 +99,9 @@ __global__ __launch_bounds__(1024) void xent_rows_kernel(RowArgs g) {
 }
 
 // Sum of the row losses (float64, fixed order), times 1 / count for the mean
-// (inv_count not null): read from there, or, with `targets`, counted here and
-// left there, which saves a call of one panel the counting launch.
+// (inv_count not null): read from there, or, with `targets` (for the mean
+// only), counted here and left there, which saves a call of one panel the
+// counting launch.
 __global__ __launch_bounds__(1024) void xent_reduce_kernel(const float* __restrict__ rows, const int64_t* __restrict__ targets, int N,
                                                            int64_t ignore, float* __restrict__ inv_count, float* __restrict__ out) {
   __shared__ double red[16];
@@ -128,7 +129,7 @@ __global__ __launch_bounds__(1024) void xent_reduce_kernel(const float* __restri
       t += red[w];
       k += kept[w];
     }
-    if (targets) *inv_count = 1.0f / (float)max(k, 1);
+    if (targets && inv_count) *inv_count = 1.0f / (float)max(k, 1);
     *out = (float)(inv_count ? t * (double)*inv_count : t);
   }
 }

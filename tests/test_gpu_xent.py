@@ -175,6 +175,33 @@ def test_no_row_kept_and_no_rows(mir, dt):
     assert (dw == 2.0).all()
 
 
+@pytest.mark.parametrize("reduction", ["none", "sum", "mean"])
+@pytest.mark.parametrize("with_dweight", [False, True])
+def test_no_rows_with_a_pointer_to_targets(mir, with_dweight, reduction):
+    """The C call with N = 0 and every pointer valid (an empty tensor's is
+    null, so the binding does not come this way): loss 0, dweight 0 or, accumulated, as it was."""
+    import ctypes
+    import torch
+    w = torch.ones(70, 64, device="cuda")
+    h, dw = torch.ones(3, 64, device="cuda"), torch.full_like(w, 3.0)
+    t, loss = torch.zeros(3, dtype=torch.int64, device="cuda"), torch.full((), 9.0, device="cuda")
+    a = mir.XentArgsC(hidden=h.data_ptr(), weight=w.data_ptr(), targets=t.data_ptr(), loss=loss.data_ptr(), ld_hidden=64,
+                      ld_weight=64, ld_dhidden=64, ld_dweight=64, N=0, V=70, d=64, ignore_index=-100, dt=mir.F32,
+                      weight_dt=mir.F32, dweight_dt=mir.F32, logits_dt=mir.F32, reduction=mir.REDUCTIONS[reduction], scale=1.0,
+                      dweight=dw.data_ptr() if with_dweight else None)
+    need = ctypes.c_size_t(0)
+    assert mir.lib.shampoo_linear_xent_workspace(ctypes.byref(a), ctypes.byref(need)) == mir.OK
+    ws = torch.empty(need.value, dtype=torch.uint8, device="cuda")
+    a.ws, a.ws_bytes = ws.data_ptr(), need.value
+    stream = torch.cuda.current_stream().cuda_stream
+    for accumulate in (1, 0):
+        a.accumulate = accumulate
+        assert mir.lib.shampoo_linear_xent(ctypes.byref(a), stream) == mir.OK
+        torch.cuda.synchronize()
+        assert loss.item() == (9.0 if reduction == "none" else 0.0)
+        assert (dw == (3.0 if accumulate or not with_dweight else 0.0)).all()
+
+
 @pytest.mark.parametrize("dt", ["float32", "bfloat16"])
 def test_targets_outside_the_vocabulary(mir, dt):
     """Loud, and only where they are: NaN in that row's loss and gradient."""
