@@ -12,8 +12,9 @@
 // largest of them and drop what lies some 13 bits below (measured: 1.5e-5
 // relative on random operands, at every K), which a 16-bit result does not
 // show and a float32 result does.  F8W, for float32 results, widens the
-// operands with their scales to bfloat16 in registers (exactly) and
-// multiplies those (5e-9 relative), at half the matrix-core rate.
+// operands with their scales to bfloat16 in registers (exactly; blocks whose
+// scales are at the ends of their range apart, see there) and multiplies
+// those, at half the matrix-core rate (results 1.7e-7 from float64).
 //
 // Operand layouts.  "k-contiguous": row r at r * ld, k along the row.
 // "k-strided" (template flags AS, BS; bfloat16 and float32): element (r, k)
@@ -446,6 +447,64 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_kernel(ProductArgs g)
             acc[i][j] = mma_step<E, FB, FA>(st, fb[hh][j], fa[hh][i], acc[i][j], SCALED ? sc[0][FM + j] : 0, SCALED ? sc[0][i] : 0);
     }
   };
+  // F8W: scale bytes from 17 to 239 keep every value of either format times its
+  // scale a normal bfloat16 number (2^-16 at byte 17, 1.75 2^15 at 239).  A
+  // wave that meets another among the scales of an item notes the item, and
+  // at the end makes its part of those tiles anew, from memory: values widened
+  // alone, each block's sum times both scales at once, so that only the
+  // results' own range is left.  Behind the loop because its registers are
+  // full: the same inside it spilled 73 of them.  The noting costs 0.7% (144 x
+  // 1024^3: 363 to 366 us).
+  constexpr uint32_t FIRST_SAFE = 17, SAFE_SPAN = 239 - FIRST_SAFE;
+  uint32_t extreme = 0;
+  uint64_t again = 0;  // items to make anew; bit 63 stands for all from 63 on
+  auto note_scales = [&]() {
+    if constexpr (E == Elem::F8W) {
+#pragma unroll
+      for (int i = 0; i < FM + FN; ++i) extreme = max(extreme, (uint32_t)sc[0][i] - FIRST_SAFE);
+    }
+  };
+  auto store_apart = [&](const Item& item) {
+    const uint8_t* const A = reinterpret_cast<const uint8_t*>(g.A) + item.batch * g.strideA + (int64_t)item.k0 * SK;
+    const uint8_t* const B = reinterpret_cast<const uint8_t*>(g.B) + item.batch * g.strideB + (int64_t)item.k0 * SK;
+    const uint8_t* const SA = g.sa + item.batch * g.strideSa + item.k0;
+    const uint8_t* const SB = g.sb + item.batch * g.strideSb + item.k0;
+    float* const C = reinterpret_cast<float*>(g.C) + item.batch * g.strideC + item.split * g.split_stride;
+#pragma nounroll
+    for (int i = 0; i < FM; ++i) {
+      const int m = item.tm * TM + (wm * FM + i) * 32 + l32, ma = min(m, g.M - 1);
+      const uint8_t* const sa = SA + (int64_t)(ma >> g.sa_shift) * g.ldsa;
+#pragma nounroll
+      for (int j = 0; j < FN; ++j) {
+        const int n0 = item.tn * TN + (wn * FN + j) * 32, nb = min(n0 + l32, g.N - 1);
+        const uint8_t* const sb = SB + (int64_t)(nb >> g.sb_shift) * g.ldsb;
+        const uint8_t* a = A + ma * g.lda + 8 * half;
+        const uint8_t* b = B + nb * g.ldb + 8 * half;
+        float sum[16];
+#pragma unroll
+        for (int v = 0; v < 16; ++v) sum[v] = 0.f;
+#pragma nounroll
+        for (int s = 0; s < item.stages; ++s, a += SK, b += SK) {
+          floatx16 t;
+#pragma unroll
+          for (int v = 0; v < 16; ++v) t[v] = 0.f;
+#pragma unroll
+          for (int st = 0; st < SK / 16; ++st) {
+            const u32x2 x = *reinterpret_cast<const u32x2*>(a + 16 * st), y = *reinterpret_cast<const u32x2*>(b + 16 * st);
+            t = __builtin_amdgcn_mfma_f32_32x32x16_bf16(widen_f8<FB>((int)y[0], (int)y[1], 127), widen_f8<FA>((int)x[0], (int)x[1], 127), t, 0, 0, 0);
+          }
+          const int ea = (int)sa[s] - 254, eb = sb[s];
+#pragma unroll
+          for (int v = 0; v < 16; ++v) sum[v] += ldexpf(t[v], ea + __shfl(eb, 8 * (v >> 2) + 4 * half + (v & 3)));
+        }
+#pragma unroll
+        for (int v = 0; v < 16; ++v) {
+          const int n = n0 + 8 * (v >> 2) + 4 * half + (v & 3);
+          if (m < g.M && n < g.N) C[m * g.ldc + n] = sum[v];  // by the lane that wrote it before
+        }
+      }
+    }
+  };
   // The reads (and loads) of a half go between its first matrix-core
   // instructions: left to itself the compiler puts them behind the last and
   // waits for them there.
@@ -488,6 +547,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_kernel(ProductArgs g)
         for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
 #pragma nounroll
     for (int s = 0; s < cur.stages; ++s) {
+      note_scales();
       // first half of the stage's k; its second half into registers
       read_frags(rb, 1);
       multiply(0);
@@ -511,6 +571,11 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_kernel(ProductArgs g)
       for (int i = 0; i < FM + FN; ++i) sc[0][i] = sc[1][i];
       rb = next;
       advance();
+    }
+
+    if constexpr (E == Elem::F8W) {
+      if (__any(extreme > SAFE_SPAN)) again |= uint64_t(1) << min(it, 63);
+      extreme = 0;
     }
 
     // ---- epilogue --------------------------------------------------------
@@ -671,6 +736,13 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_kernel(ProductArgs g)
       }
     }
     move_on(cp);
+  }
+  if constexpr (E == Elem::F8W) {
+    if (again == 0) return;
+    cp = place_of(first);
+#pragma nounroll
+    for (int it = 0; it < nitem; ++it, move_on(cp))
+      if (again >> min(it, 63) & 1) store_apart(item_at(cp));
   }
 }
 

@@ -208,3 +208,97 @@ def test_linear_layer_gradients(mir):
     assert abs(float(np.sum(dx * u)) - slope) <= float(np.sum(bound(D, e5, W, e4) * np.abs(u)))
     rel = [np.linalg.norm(a - b) / np.linalg.norm(b) for a, b in ((y, x @ w.T), (dx, dy @ w), (dw, dy.T @ x))]
     log("linear layer in 8 bits, relative: y %.3f dx %.3f dw %.3f" % tuple(rel))
+
+
+def held(mir, g, n, rows, K, fmt, scales):
+    """Random finite 8-bit values, the largest and smallest among them, and these scale bytes."""
+    import torch
+    ok = np.flatnonzero(np.isfinite(ref.code_values(fmt)))
+    q = g.choice(ok, size=(n, rows, K)).astype(np.uint8)
+    q[:, :, ::7] = ok[np.argmax(ref.code_values(fmt)[ok])]
+    q[:, :, 3::11] = 1   # the smallest subnormal number
+    s = np.full((n, scales.shape[1], ref.up(K // 128, 4)), 127, dtype=np.uint8)
+    s[:, :, :K // 128] = scales
+    kind = torch.float8_e4m3fn if fmt == "e4m3" else torch.float8_e5m2
+    return torch.from_numpy(q).cuda().view(kind), torch.from_numpy(s).cuda().view(torch.float8_e8m0fnu), q, s
+
+
+@pytest.mark.parametrize("out", ["float32", "bfloat16", "float16"])
+@pytest.mark.parametrize("fa,fb", [("e4m3", "e4m3"), ("e4m3", "e5m2"), ("e5m2", "e4m3"), ("e5m2", "e5m2")])
+@pytest.mark.parametrize("M,N", [(4, 70), (5, 70), (300, 257)])
+def test_scales_over_their_whole_range(mir, M, N, fa, fb, out):
+    """Scales of 2^-127 to 2^127 on one side against the opposite on the other,
+    all blocks alike, block by block, and row by row (where a huge row meets a
+    huge one the result overflows in any arithmetic; those are not compared).
+    16-bit results: the instructions drop what lies 2^-13 below the largest."""
+    import torch
+    g = np.random.default_rng(M)
+    K = 640
+    for kind in ("same", "blocks", "rows"):
+        ends = np.array([0, 1, 7, 16, 17, 120, 127, 239, 240, 247, 254])
+        if kind == "same":
+            e = np.broadcast_to(ends[:, None, None], (len(ends), 1, K // 128))
+            a_e, b_e = np.repeat(e, M, 1), np.repeat(254 - e, N, 1)
+        elif kind == "blocks":
+            e = g.choice(ends, size=(3, 1, K // 128))
+            a_e, b_e = np.repeat(e, M, 1), np.repeat(254 - e, N, 1)
+        else:
+            a_e = np.repeat(g.choice(ends, size=(3, M, 1)), K // 128, 2)
+            b_e = np.repeat(g.choice(ends, size=(3, N, 1)), K // 128, 2)
+        n = len(a_e)
+        a, sa, qa, ha = held(mir, g, n, M, K, fa, a_e)
+        b, sb, qb, hb = held(mir, g, n, N, K, fb, b_e)
+        c = torch.full((n, M, N), float("nan"), dtype=getattr(torch, out), device="cuda")
+        got = mir.shampoo_matmul_f8(a, sa, b, sb, c).double().cpu().numpy()
+        lim = torch.finfo(c.dtype)
+        for i in range(n):
+            A, B = ref.stand_for(ref.code_values(fa)[qa[i]], ha[i], 1), ref.stand_for(ref.code_values(fb)[qb[i]], hb[i], 1)
+            want, size = A @ B.T, np.abs(A) @ np.abs(B).T
+            # no partial sum overflows; below the smallest normal numbers the
+            # result's and the sums' absolute steps count
+            safe = size < lim.max
+            assert kind == "rows" or out == "float16" or safe.all()
+            bound = (K * 2.0 ** -23 + (2.0 ** -13 if out != "float32" else 0.0)) * size + lim.eps / 2 * np.abs(want)
+            bound += lim.smallest_normal * lim.eps + K * 2.0 ** -126
+            err = np.abs(got[i] - want)
+            assert (err <= bound)[safe].all(), (kind, i, float(np.nanmax((err / bound)[safe])), int(np.isnan(got[i][safe]).sum()))
+
+
+def test_quantised_values_near_the_largest_float32(mir):
+    """Entries just below 2^128 round up to it; their products with small numbers are ordinary."""
+    import torch
+    x = torch.full((40, 256), 3.4e38, device="cuda")
+    x[::2] *= -0.99
+    w = torch.full((70, 256), 2.0 ** -100, device="cuda")
+    a, b = mir.shampoo_quantize_f8(x), mir.shampoo_quantize_f8(w)
+    A = ref.stand_for(values_of(a[0], "e4m3"), bytes_of(a[1]), 1)
+    B = ref.stand_for(values_of(b[0], "e4m3"), bytes_of(b[1]), 1)
+    assert np.abs(A).max() == 2.0 ** 128
+    for rows in (4, 5, 40):
+        for out in (torch.float32, torch.bfloat16):
+            c = mir.shampoo_matmul_f8(a[0][:rows], a[1][:rows], *b, torch.empty((rows, 70), dtype=out, device="cuda"))
+            want = A[:rows] @ B.T
+            assert (np.abs(c.double().cpu().numpy() - want) <= 2.0 ** (-8 if out == torch.bfloat16 else -14) * np.abs(want)).all()
+
+
+def test_extreme_blocks_of_many_tiles_and_split_k(mir):
+    """A few extreme blocks among ordinary ones: tiles of every shape, several
+    a workgroup, and a k that is split; the other results keep their bits."""
+    import torch
+    g = np.random.default_rng(1)
+    for n, M, N, K in ((3, 150, 260, 512), (9, 1500, 1030, 256), (1, 64, 64, 8192)):
+        a = torch.from_numpy(g.standard_normal((n, M, K))).float().cuda()
+        b = torch.from_numpy(g.standard_normal((n, N, K))).float().cuda()
+        (qa, sa), (qb, sb) = mir.shampoo_quantize_f8(a), mir.shampoo_quantize_f8(b)
+        plain = mir.shampoo_matmul_f8(qa, sa, qb, sb, torch.empty((n, M, N), device="cuda"))
+        ha, hb = sa.view(torch.uint8), sb.view(torch.uint8)
+        # block 1 of a few rows of A at 2^120, and of every row of B of those matrices at 2^-120
+        rows = g.integers(0, M, 5)
+        ha[0, torch.from_numpy(rows).cuda(), 1] = 247
+        hb[0, :, 1] = 7
+        c = mir.shampoo_matmul_f8(qa, sa, qb, sb, torch.full((n, M, N), float("nan"), device="cuda"))
+        assert torch.equal(c[1:], plain[1:])
+        A, B = (ref.stand_for(values_of(q, "e4m3")[0], bytes_of(s)[0], 1) for q, s in ((qa, sa), (qb, sb)))
+        want, size = A @ B.T, np.abs(A) @ np.abs(B).T
+        err = np.abs(c[0].double().cpu().numpy() - want)
+        assert (err <= K * 2.0 ** -23 * size + 2.0 ** -24 * np.abs(want)).all()
