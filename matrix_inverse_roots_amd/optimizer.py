@@ -228,6 +228,8 @@ class Shampoo:
             self.members.append(idx)
         self._kept = {}         # parameter index -> gradient buffer that projection_loss writes
         self._pending = set()   # those written since the last step
+        self._reads = {}        # parameter index -> mark behind its last projection_loss since the last step
+        self._stepped = None    # mark behind the last step
         self.frequency = int(precondition_frequency)
         self.t = 0
         self.device = params[0].device
@@ -252,8 +254,11 @@ class Shampoo:
         receives hidden's gradient.  Float32 hidden needs float32 gradients.
         logits_dtype=torch.float8_e4m3fn takes the logits from the 8-bit
         product of hidden and the parameter.
-        The buffer is written on ``stream`` (default: the current stream) and
-        read by the step on its own."""
+        The work runs on ``stream`` (default: the current stream), behind the
+        last step and the calls on this parameter before it, and the next
+        step runs behind it, whichever streams these were given.  In a
+        stream capture, and for what a captured graph replays, the caller
+        orders them."""
         torch = self.stacks[0].torch
         w = self.params[index]
         index = range(len(self.params))[index]
@@ -262,6 +267,10 @@ class Shampoo:
         gdt = self.hp["grad_dtype"]
         if hidden.dtype == torch.float32 and gdt != torch.float32:
             raise ValueError("projection_loss: float32 hidden needs float32 gradients (grad_dtype)")
+        cur = self._stream(stream)
+        ordered = not self._capturing(cur)
+        if ordered:
+            self._wait(cur, self._stepped, self._reads.get(index))
         fresh = index not in self._pending
         dw = self._kept.get(index)
         if dw is None:
@@ -272,7 +281,41 @@ class Shampoo:
                                    stream=stream)
         self._kept[index] = dw
         self._pending.add(index)
+        if ordered:
+            self._reads[index] = self._mark(cur, self._reads.get(index))
         return loss
+
+    # A mark: (event, stream) behind work that others have to follow.  Events
+    # of a capture belong to its graph, so captured work takes and leaves none.
+    def _stream(self, stream):
+        return stream if stream is not None else self.stacks[0].torch.cuda.current_stream(self.device)
+
+    def _capturing(self, stream):
+        torch = self.stacks[0].torch
+        with torch.cuda.stream(stream):
+            return torch.cuda.is_current_stream_capturing()
+
+    def _mark(self, stream, old):
+        event = old[0] if old is not None else self.stacks[0].torch.cuda.Event()
+        event.record(stream)
+        return event, stream
+
+    def _wait(self, stream, *marks):
+        for mark in marks:
+            if mark is not None and mark[1] != stream:
+                stream.wait_event(mark[0])
+
+    def _before_step(self, cur, kept):
+        """``cur`` behind every projection_loss since the last step: they read the
+        parameters, and wrote the gradients that the step takes (``kept``)."""
+        self._wait(cur, *self._reads.values())
+        for i in kept:
+            if i in self._reads and self._reads[i][1] != cur:
+                self._kept[i].record_stream(cur)
+
+    def _after_step(self, cur):
+        self._reads.clear()
+        self._stepped = self._mark(cur, self._stepped)
 
     def _gradients(self, grads):
         """One tensor per parameter: None stands for what projection_loss kept."""
@@ -288,7 +331,12 @@ class Shampoo:
     def step(self, grads, stream=None):
         """One step with gradients given per parameter (same order as params);
         None takes the gradient that ``projection_loss`` kept."""
-        grads = self._gradients(grads)
+        given = list(grads)
+        grads = self._gradients(given)
+        cur = self._stream(stream)
+        ordered = not self._capturing(cur)
+        if ordered:
+            self._before_step(cur, [i for i, g in enumerate(given) if g is None])
         self.t += 1
         recompute = (self.t - 1) % self.frequency == 0
         views = [g.reshape(v.shape) for g, v in zip(grads, self.views)]
@@ -296,9 +344,10 @@ class Shampoo:
             for st, idx in zip(self.stacks, self.members):
                 st.step([views[i] for i in idx], self.t, recompute, stream=stream)
             self._pending.clear()
+            if ordered:
+                self._after_step(cur)
             return
         torch = self.stacks[0].torch
-        cur = stream if stream is not None else torch.cuda.current_stream(self.device)
         for st, idx in zip(self.stacks, self.members):
             st.prepare([views[i] for i in idx], self.t, recompute, stream=cur)
         fork = torch.cuda.Event()
@@ -315,6 +364,8 @@ class Shampoo:
         for done in joins:
             cur.wait_event(done)
         self._pending.clear()
+        if ordered:
+            self._after_step(cur)
 
     def capture(self, grads):
         """Record one step on the gradient buffers ``grads`` into a graph and
@@ -340,6 +391,8 @@ class Shampoo:
         if self.t < 1:
             raise ValueError("capture: take one eager step first")
         pending = set(self._pending)
+        grads = list(grads)
+        kept = [i for i, g in enumerate(grads) if g is None]
         grads = self._gradients(grads)
         views = [g.reshape(v.shape) for g, v in zip(grads, self.views)]
         # descriptor tables of these buffers, uploaded before the capture
@@ -358,9 +411,15 @@ class Shampoo:
         self._pending = pending
 
         def replay():
+            cur = self._stream(None)
+            ordered = not self._capturing(cur)
+            if ordered:
+                self._before_step(cur, kept)
             self.t += 1
             self._pending.clear()
             graph.replay()
+            if ordered:
+                self._after_step(cur)
 
         replay.graph = graph
         replay.tables = tables

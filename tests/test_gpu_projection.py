@@ -275,3 +275,51 @@ def test_kept_gradient_belongs_to_its_stream(mir):
         opt.projection_loss(0, h, t, stream=side)
         torch.cuda.synchronize()
         assert torch.equal(opt._kept[0], want)
+
+
+def busy(stream, ms=10):
+    """Some milliseconds of work on ``stream``, so that what follows there starts late."""
+    import torch
+    with torch.cuda.stream(stream):
+        x = torch.empty((64, 1 << 20), device="cuda")
+        for _ in range(10 * ms):
+            x.fill_(1.0)
+
+
+@pytest.mark.parametrize("captured", [False, True])
+def test_loss_and_step_on_different_streams(mir, captured):
+    """Micro-batches on two side streams, steps on the current one, each in turn
+    held up, with no synchronisation by the caller: the bits of the same calls
+    one after the other."""
+    import torch
+    V, d, steps = 500, 64, 5
+    a, b = (optimizer(mir, V, d, torch.bfloat16) for _ in range(2))
+    g0 = torch.randn(96, 64, device="cuda").bfloat16()
+    data = [[make(70 + k, d, V, "bfloat16", 10 * s + k)[::2] for k in range(2)] for s in range(steps)]
+    want, got = [], []
+    for s in range(steps):
+        for h, t in data[s]:
+            want.append(a.projection_loss(1, h, t, scale=0.5))
+            torch.cuda.synchronize()
+        a.step([g0, None])
+        torch.cuda.synchronize()
+    sides = [torch.cuda.Stream() for _ in range(2)]
+    cur = torch.cuda.current_stream()
+    step = lambda: b.step([g0, None])  # noqa: E731
+    torch.cuda.synchronize()
+    for s in range(steps):
+        if s == 1 and captured:
+            for h, t in data[s]:
+                got.append(b.projection_loss(1, h, t, scale=0.5, stream=sides[0]))
+            step = b.capture([g0, None])
+        else:
+            for k, (h, t) in enumerate(data[s]):
+                if (s + k) % 3 == 0:
+                    busy(sides[k])
+                got.append(b.projection_loss(1, h, t, scale=0.5, stream=sides[k]))
+        if s % 2:
+            busy(cur)
+        step()
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(want, got))
+    assert all(torch.equal(x, y) for x, y in zip(a.params, b.params))
