@@ -317,14 +317,17 @@ class Shampoo:
         self._reads.clear()
         self._stepped = self._mark(cur, self._stepped)
 
+    def _need(self, i):
+        if i not in self._pending:
+            raise ValueError("no gradient for parameter %d: projection_loss has not been called on it "
+                             "since the last step" % i)
+
     def _gradients(self, grads):
         """One tensor per parameter: None stands for what projection_loss kept."""
         grads = list(grads)
         for i, g in enumerate(grads):
             if g is None:
-                if i not in self._pending:
-                    raise ValueError("no gradient for parameter %d: projection_loss has not been called on it "
-                                     "since the last step" % i)
+                self._need(i)
                 grads[i] = self._kept[i]
         return grads
 
@@ -370,7 +373,9 @@ class Shampoo:
     def capture(self, grads):
         """Record one step on the gradient buffers ``grads`` into a graph and
         return a function that replays it (and advances the step count).
-        Refill the buffers in place before each replay.  The graph replays
+        Refill the buffers in place before each replay; None stands, as in
+        ``step``, for what ``projection_loss`` keeps, and each replay needs a
+        call of it since the last step.  The graph replays
         the launches of an eager step with the same arguments, so it needs a
         step whose kernels do not change with the step count: SGD, momentum
         or no grafting (Adam's bias correction depends on it), roots every
@@ -411,6 +416,8 @@ class Shampoo:
         self._pending = pending
 
         def replay():
+            for i in kept:
+                self._need(i)
             cur = self._stream(None)
             ordered = not self._capturing(cur)
             if ordered:

@@ -323,3 +323,26 @@ def test_loss_and_step_on_different_streams(mir, captured):
     torch.cuda.synchronize()
     assert all(torch.equal(x, y) for x, y in zip(want, got))
     assert all(torch.equal(x, y) for x, y in zip(a.params, b.params))
+
+
+def test_replay_needs_a_gradient_of_its_own(mir):
+    """A replay without a projection_loss since the last step raises, as a step
+    does, and changes nothing; with one it goes on."""
+    import torch
+    V, d = 300, 64
+    opt = optimizer(mir, V, d, torch.float32)
+    g0 = torch.randn(96, 64, device="cuda")
+    h, _, t = make(60, d, V, "bfloat16", 1)
+    opt.projection_loss(1, h, t)
+    opt.step([g0, None])
+    opt.projection_loss(1, h, t)
+    replay = opt.capture([g0, None])
+    replay()
+    before, steps = [p.clone() for p in opt.params], opt.t
+    for _ in range(2):
+        with pytest.raises(ValueError, match="projection_loss"):
+            replay()
+    assert opt.t == steps and all(torch.equal(p, q) for p, q in zip(opt.params, before))
+    opt.projection_loss(1, h, t)
+    replay()
+    assert opt.t == steps + 1 and not torch.equal(opt.params[1], before[1])
