@@ -228,6 +228,7 @@ class Shampoo:
             self.members.append(idx)
         self._kept = {}         # parameter index -> gradient buffer that projection_loss writes
         self._pending = set()   # those written since the last step
+        self._recorded = set()  # those that a stream capture writes, since the last step in it or call outside
         self._reads = {}        # parameter index -> mark behind its last projection_loss since the last step
         self._stepped = None    # mark behind the last step
         self.frequency = int(precondition_frequency)
@@ -258,7 +259,10 @@ class Shampoo:
         last step and the calls on this parameter before it, and the next
         step runs behind it, whichever streams these were given.  In a
         stream capture, and for what a captured graph replays, the caller
-        orders them."""
+        orders them.  A call in a capture runs with the graph's replays: it
+        counts for a step in the same capture, not for one outside, and
+        replays add to the buffer if at the capture a call was waiting for
+        its step."""
         torch = self.stacks[0].torch
         w = self.params[index]
         index = range(len(self.params))[index]
@@ -271,16 +275,19 @@ class Shampoo:
         ordered = not self._capturing(cur)
         if ordered:
             self._wait(cur, self._stepped, self._reads.get(index))
-        fresh = index not in self._pending
+            self._recorded.clear()
+        fresh = index not in self._pending and (ordered or index not in self._recorded)
         dw = self._kept.get(index)
         if dw is None:
             dw = _empty(w.shape, gdt, self.device, stream)
+        elif ordered:
+            dw.record_stream(cur)
         loss = shampoo_linear_xent(hidden, w, targets, dhidden=dhidden, dweight=dw, row_scale=row_scale,
                                    ignore_index=ignore_index, reduction=reduction, scale=scale,
                                    accumulate=not fresh, panel_rows=panel_rows, logits_dtype=logits_dtype,
                                    stream=stream)
         self._kept[index] = dw
-        self._pending.add(index)
+        (self._pending if ordered else self._recorded).add(index)
         if ordered:
             self._reads[index] = self._mark(cur, self._reads.get(index))
         return loss
@@ -310,34 +317,37 @@ class Shampoo:
         parameters, and wrote the gradients that the step takes (``kept``)."""
         self._wait(cur, *self._reads.values())
         for i in kept:
-            if i in self._reads and self._reads[i][1] != cur:
-                self._kept[i].record_stream(cur)
+            self._kept[i].record_stream(cur)
 
-    def _after_step(self, cur):
-        self._reads.clear()
-        self._stepped = self._mark(cur, self._stepped)
+    def _after_step(self, cur, ordered):
+        self._recorded.clear()
+        if ordered:
+            self._pending.clear()
+            self._reads.clear()
+            self._stepped = self._mark(cur, self._stepped)
 
-    def _need(self, i):
-        if i not in self._pending:
+    def _need(self, i, ordered=True):
+        if i not in self._pending and (ordered or i not in self._recorded):
             raise ValueError("no gradient for parameter %d: projection_loss has not been called on it "
                              "since the last step" % i)
 
-    def _gradients(self, grads):
-        """One tensor per parameter: None stands for what projection_loss kept."""
+    def _gradients(self, grads, ordered=True):
+        """One tensor per parameter: None stands for what projection_loss kept
+        (``ordered``: outside a capture)."""
         grads = list(grads)
         for i, g in enumerate(grads):
             if g is None:
-                self._need(i)
+                self._need(i, ordered)
                 grads[i] = self._kept[i]
         return grads
 
     def step(self, grads, stream=None):
         """One step with gradients given per parameter (same order as params);
         None takes the gradient that ``projection_loss`` kept."""
-        given = list(grads)
-        grads = self._gradients(given)
         cur = self._stream(stream)
         ordered = not self._capturing(cur)
+        given = list(grads)
+        grads = self._gradients(given, ordered)
         if ordered:
             self._before_step(cur, [i for i, g in enumerate(given) if g is None])
         self.t += 1
@@ -346,9 +356,7 @@ class Shampoo:
         if not self._side:
             for st, idx in zip(self.stacks, self.members):
                 st.step([views[i] for i in idx], self.t, recompute, stream=stream)
-            self._pending.clear()
-            if ordered:
-                self._after_step(cur)
+            self._after_step(cur, ordered)
             return
         torch = self.stacks[0].torch
         for st, idx in zip(self.stacks, self.members):
@@ -366,9 +374,7 @@ class Shampoo:
             joins.append(done)
         for done in joins:
             cur.wait_event(done)
-        self._pending.clear()
-        if ordered:
-            self._after_step(cur)
+        self._after_step(cur, ordered)
 
     def capture(self, grads):
         """Record one step on the gradient buffers ``grads`` into a graph and
@@ -395,7 +401,6 @@ class Shampoo:
             raise ValueError("capture: a coupled-Newton tolerance synchronises with the host")
         if self.t < 1:
             raise ValueError("capture: take one eager step first")
-        pending = set(self._pending)
         grads = list(grads)
         kept = [i for i, g in enumerate(grads) if g is None]
         grads = self._gradients(grads)
@@ -413,7 +418,6 @@ class Shampoo:
         with torch.cuda.graph(graph):
             self.step(grads)
         self.t = t_saved
-        self._pending = pending
 
         def replay():
             for i in kept:
@@ -423,10 +427,8 @@ class Shampoo:
             if ordered:
                 self._before_step(cur, kept)
             self.t += 1
-            self._pending.clear()
             graph.replay()
-            if ordered:
-                self._after_step(cur)
+            self._after_step(cur, ordered)
 
         replay.graph = graph
         replay.tables = tables

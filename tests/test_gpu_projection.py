@@ -346,3 +346,62 @@ def test_replay_needs_a_gradient_of_its_own(mir):
     opt.projection_loss(1, h, t)
     replay()
     assert opt.t == steps + 1 and not torch.equal(opt.params[1], before[1])
+
+
+def test_loss_in_a_graph_of_the_caller(mir):
+    """A capture of the loss with its step replays as the eager calls run; a
+    capture of the loss alone is no gradient for a step outside, until an
+    eager call has made one, to which its replays then add."""
+    import torch
+    V, d = 300, 64
+    a, b = (optimizer(mir, V, d, torch.float32) for _ in range(2))
+    g0 = torch.randn(96, 64, device="cuda")
+    h, _, t = make(60, d, V, "bfloat16", 1)
+    for o in (a, b):
+        o.projection_loss(1, h, t)
+        o.step([g0, None])
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        loss = a.projection_loss(1, h, t)
+        a.step([g0, None])
+    for k in range(4):
+        h2, _, t2 = make(60, d, V, "bfloat16", 10 + k)
+        h.copy_(h2)
+        t.copy_(t2)
+        graph.replay()
+        torch.cuda.synchronize()
+        want = b.projection_loss(1, h, t)
+        b.step([g0, None])
+        torch.cuda.synchronize()
+        assert torch.equal(loss, want)
+        assert all(torch.equal(p, q) for p, q in zip(a.params, b.params))
+    alone = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(alone):
+        a.projection_loss(1, h, t)
+    with pytest.raises(ValueError, match="projection_loss"):
+        a.step([g0, None])
+    # two more micro-batches by replays behind an eager one
+    for o in (a, b):
+        o.projection_loss(1, h, t, scale=0.25)
+    torch.cuda.synchronize()
+    more = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(more):
+        a.projection_loss(1, h, t, scale=0.25)
+    for _ in range(2):
+        more.replay()
+        b.projection_loss(1, h, t, scale=0.25)
+    for o in (a, b):
+        o.step([g0, None])
+    torch.cuda.synchronize()
+    assert all(torch.equal(p, q) for p, q in zip(a.params, b.params))
+    # none of these leaves the next capture anything to add to
+    again = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(again):
+        a.projection_loss(1, h, t)
+        a.step([g0, None])
+    again.replay()
+    b.projection_loss(1, h, t)
+    b.step([g0, None])
+    torch.cuda.synchronize()
+    assert all(torch.equal(p, q) for p, q in zip(a.params, b.params))
