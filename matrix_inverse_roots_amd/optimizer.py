@@ -289,28 +289,31 @@ class Shampoo:
         self._kept[index] = dw
         (self._pending if ordered else self._recorded).add(index)
         if ordered:
-            self._reads[index] = self._mark(cur, self._reads.get(index))
+            self._reads[index] = self._mark(cur)
         return loss
 
     # A mark: (event, stream) behind work that others have to follow.  Events
     # of a capture belong to its graph, so captured work takes and leaves none.
+    # The default stream, which outlives every mark and is never captured, gets
+    # its event only when another stream has to wait: one that records and asks
+    # nothing costs a small loss on it 3 us instead of 13.
     def _stream(self, stream):
         return stream if stream is not None else self.stacks[0].torch.cuda.current_stream(self.device)
 
     def _capturing(self, stream):
+        if stream.cuda_stream == 0:
+            return False
         torch = self.stacks[0].torch
         with torch.cuda.stream(stream):
             return torch.cuda.is_current_stream_capturing()
 
-    def _mark(self, stream, old):
-        event = old[0] if old is not None else self.stacks[0].torch.cuda.Event()
-        event.record(stream)
-        return event, stream
+    def _mark(self, stream):
+        return None if stream.cuda_stream == 0 else stream.record_event(), stream
 
     def _wait(self, stream, *marks):
         for mark in marks:
             if mark is not None and mark[1] != stream:
-                stream.wait_event(mark[0])
+                stream.wait_event(mark[0] if mark[0] is not None else mark[1].record_event())
 
     def _before_step(self, cur, kept):
         """``cur`` behind every projection_loss since the last step: they read the
@@ -324,7 +327,7 @@ class Shampoo:
         if ordered:
             self._pending.clear()
             self._reads.clear()
-            self._stepped = self._mark(cur, self._stepped)
+            self._stepped = self._mark(cur)
 
     def _need(self, i, ordered=True):
         if i not in self._pending and (ordered or i not in self._recorded):
