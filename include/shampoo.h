@@ -470,7 +470,8 @@ shampoo_status shampoo_mfma_peak(shampoo_dtype dt, void* sink_dev, hipStream_t s
  * [n, cols, Rp] with blocks along the rows (block_rows then counts columns
  * of x); either pair may be null.  fmt: SHAMPOO_E4M3 or SHAMPOO_E5M2.
  * q, qt: 16-byte aligned; s, st: 4-byte aligned.  n at most 65535; rows and
- * cols at most 2^23 - 128.  Empty matrices return at once. */
+ * cols at most 2^23 - 128.  The outputs may not overlap x or one another.
+ * Empty matrices return at once. */
 shampoo_status shampoo_quantize_f8(const void* x, shampoo_dtype x_dt, int64_t n, int64_t rows, int64_t cols,
                                    int64_t ld, int64_t stride, shampoo_dtype fmt, int32_t block_rows,
                                    void* q, void* s, void* qt, void* st, hipStream_t stream);
@@ -484,7 +485,7 @@ shampoo_status shampoo_quantize_f8(const void* x, shampoo_dtype x_dt, int64_t n,
  * instruction's (1.5e-5 relative on random operands); float32 results are
  * summed without that.  ws: shampoo_matmul_f8_workspace bytes, 256-byte aligned
  * (0 for most shapes: float32 partial results where few outputs share a long
- * K).  Results do not depend on the stream, the workspace's contents or the
+ * K).  c and ws may not overlap the operands.  Results do not depend on the stream, the workspace's contents or the
  * run. */
 shampoo_status shampoo_matmul_f8_workspace(int64_t n, int64_t M, int64_t N, int64_t K, size_t* bytes);
 shampoo_status shampoo_matmul_f8(const void* a, shampoo_dtype a_dt, const void* a_scale, int32_t a_block_rows,
@@ -528,9 +529,10 @@ typedef enum shampoo_reduction {
  * that leave a maximum and a sum each.  For gradients the rows are taken
  * panel_rows at a time (0: as many as keep the panel of exponentials within
  * 2.25 GiB), with the panel in the workspace (256-byte aligned).  V and the row
- * strides of hidden and weight at most 2^20, d at most 2^18.  dhidden and
- * dweight may not be hidden and weight themselves.  No atomics: two identical
- * calls give identical bits. */
+ * strides of hidden and weight at most 2^20, d at most 2^18.  What the call
+ * writes (dhidden, dweight, loss, lse, the workspace) may overlap nothing else
+ * of it (E_INVALID); rows may lie between rows of the same stride.  No atomics:
+ * two identical calls give identical bits. */
 typedef struct shampoo_xent_args {
   const void* hidden;
   const void* weight;

@@ -21,6 +21,37 @@ inline int64_t up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 inline bool aligned(const void* p, size_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 inline size_t size_of(int dt) { return dt == SHAMPOO_F32 ? 4 : dt == SHAMPOO_E4M3 || dt == SHAMPOO_E5M2 ? 1 : 2; }
 
+// Memory of a call: `rows` of `width` bytes, `apart` bytes from one to the next.
+struct Span {
+  const char* name;
+  const void* p;
+  int64_t rows, width, apart;
+};
+Span run_of(const char* name, const void* p, int64_t bytes) { return {name, p, 1, bytes, bytes}; }
+Span rows_of(const char* name, const void* p, int64_t rows, int64_t cols, int64_t ld, int dt) {
+  const int64_t es = (int64_t)size_of(dt);
+  return {name, p, rows, cols * es, rows > 1 ? ld * es : cols * es};
+}
+// Rows of the same distance may lie between one another (views of one wider
+// matrix); otherwise the spans' whole extents count.
+bool overlap(const Span& a, const Span& b) {
+  if (!a.p || !b.p || a.rows <= 0 || b.rows <= 0 || a.width <= 0 || b.width <= 0) return false;
+  const uintptr_t pa = (uintptr_t)a.p, pb = (uintptr_t)b.p;
+  const uintptr_t ea = pa + (uintptr_t)((a.rows - 1) * a.apart + a.width), eb = pb + (uintptr_t)((b.rows - 1) * b.apart + b.width);
+  if (ea <= pb || eb <= pa) return false;
+  if (a.rows > 1 && b.rows > 1 && a.apart != b.apart) return true;
+  const int64_t apart = a.rows > 1 ? a.apart : b.apart;
+  const int64_t at = pb >= pa ? (int64_t)((pb - pa) % (uintptr_t)apart) : (apart - (int64_t)((pa - pb) % (uintptr_t)apart)) % apart;
+  return at < a.width || at + b.width > apart;
+}
+// What a call writes (the first `written` spans) may overlap nothing else of it.
+template <size_t COUNT> shampoo_status check_apart(const Span (&spans)[COUNT], size_t written) {
+  for (size_t i = 0; i < written; ++i)
+    for (size_t j = i + 1; j < COUNT; ++j)
+      if (overlap(spans[i], spans[j])) return fail(SHAMPOO_E_INVALID, "%s overlaps %s", spans[i].name, spans[j].name);
+  return SHAMPOO_OK;
+}
+
 // ---------------------------------------------------------------------------
 // products
 // ---------------------------------------------------------------------------
@@ -183,6 +214,12 @@ shampoo_status quantize_f8_impl(const void* x, int x_dt, int64_t n, int64_t rows
   if (!aligned(q, 16) || !aligned(qt, 16) || !aligned(s, 4) || !aligned(st_, 4) || !aligned(x, size_of(x_dt)))
     return fail(SHAMPOO_E_INVALID, "misaligned pointer");
   if ((rows + 127) / 128 > 65535) return fail(SHAMPOO_E_UNSUPPORTED, "matrix too large to quantise");
+  const int64_t Kp = up(cols, 128), Rp = up(rows, 128), part = n * (block_rows == 1 ? rows : Rp / 128), part_t = n * (block_rows == 1 ? cols : Kp / 128);
+  const Span spans[] = {run_of("q", q, n * rows * Kp), run_of("s", s, part * up(Kp / 128, 4)), run_of("qt", qt, n * cols * Rp),
+                        run_of("st", st_, part_t * up(Rp / 128, 4)),
+                        run_of("x", x, (((n - 1) * stride) + (rows - 1) * ld + cols) * (int64_t)size_of(x_dt))};
+  const shampoo_status apart = check_apart(spans, 4);
+  if (apart != SHAMPOO_OK) return apart;
   QuantArgs g;
   g.x = x; g.ld = ld; g.stride = n > 1 ? stride : 0;
   g.q = (uint8_t*)q; g.s = (uint8_t*)s; g.qt = (uint8_t*)qt; g.st = (uint8_t*)st_;
@@ -260,6 +297,10 @@ shampoo_status matmul_f8_impl(const void* a, int a_dt, const void* sa, int32_t a
   g.sb_shift = brb == 128 ? 7 : 0;
   g.strideSa = (arb == 128 ? (M + 127) / 128 : M) * g.ldsa;
   g.strideSb = (brb == 128 ? (N + 127) / 128 : N) * g.ldsb;
+  const Span spans[] = {run_of("c", c, n * M * N * (int64_t)size_of(c_dt)), run_of("the workspace", ws, (int64_t)need), run_of("a", a, n * M * K),
+                        run_of("b", b, n * N * K), run_of("a_scale", sa, n * g.strideSa), run_of("b_scale", sb, n * g.strideSb)};
+  r = check_apart(spans, 2);
+  if (r != SHAMPOO_OK) return r;
   if (few_rows(M)) {
     g.C = c; g.ldc = N; g.strideC = M * N; g.c_dt = out_code(c_dt);
     HIP_TRY(M == 1 ? launch_rows<1>(g, a_dt, b_dt, n, st) : M == 2 ? launch_rows<2>(g, a_dt, b_dt, n, st)
@@ -543,11 +584,20 @@ shampoo_status shampoo_linear_xent(const shampoo_xent_args* a, hipStream_t strea
   if (!aligned(a->hidden, es) || !aligned(a->weight, size_of(a->weight_dt)) || !aligned(a->dhidden, es) || !aligned(a->targets, 8) || !aligned(a->loss, 4) ||
       (a->dweight && !aligned(a->dweight, size_of(a->dweight_dt))) || !aligned(a->row_scale, 4) || !aligned(a->lse, 4))
     return fail(SHAMPOO_E_INVALID, "misaligned pointer");
-  // a later panel reads what an earlier one's gradients would have replaced
-  if (a->N > 0 && ((a->dhidden && a->dhidden == a->hidden) || (a->dweight && a->dweight == a->weight)))
-    return fail(SHAMPOO_E_INVALID, "a gradient may not replace its operand");
   if (!a->ws || a->ws_bytes < L.total || !aligned(a->ws, 256))
     return fail(SHAMPOO_E_WORKSPACE, "workspace %zu bytes < %zu needed (256-byte aligned)", a->ws ? a->ws_bytes : 0, L.total);
+  // a later panel reads what an earlier one's gradients would have replaced
+  const Span spans[] = {rows_of("dhidden", a->dhidden, a->N, a->d, a->ld_dhidden, a->dt),
+                        rows_of("dweight", a->dweight, a->V, a->d, a->ld_dweight, a->dweight_dt),
+                        run_of("loss", a->loss, a->reduction == SHAMPOO_REDUCE_NONE ? 4 * a->N : 4),
+                        run_of("lse", a->lse, 4 * a->N),
+                        run_of("the workspace", a->ws, (int64_t)L.total),
+                        rows_of("hidden", a->hidden, a->N, a->d, a->ld_hidden, a->dt),
+                        rows_of("weight", a->weight, a->V, a->d, a->ld_weight, a->weight_dt),
+                        run_of("targets", a->targets, 8 * a->N),
+                        run_of("row_scale", a->row_scale, 4 * a->N)};
+  const shampoo_status apart = check_apart(spans, 5);
+  if (apart != SHAMPOO_OK) return apart;
   return a->dt == SHAMPOO_F32 ? run_xent<Elem::F32, float>(a, L, stream) : run_xent<Elem::BF16, uint16_t>(a, L, stream);
 }
 

@@ -129,6 +129,68 @@ def test_xent_refusals_of_the_call(mir, kw, status):
     assert mir.lib.shampoo_last_error()
 
 
+A, B, C, D, E, F, G, H = (k << 24 for k in range(1, 9))   # addresses 16 MiB apart
+
+
+def xent_apart(mir, **kw):
+    """A call whose memory lies apart but for what `kw` says (no GPU here: E_HIP once it is let through)."""
+    lib = mir.lib
+    status = xent(mir, True, **{**dict(hidden=A, weight=B, targets=C, loss=D, dhidden=E, dweight=F, lse=G, ws=H, ws_bytes=1 << 22), **kw})
+    return status, lib.shampoo_last_error().decode()
+
+
+@pytest.mark.parametrize("kw,names", [
+    (dict(dhidden=A), "dhidden overlaps hidden"), (dict(dhidden=A + 128), "dhidden overlaps hidden"),
+    (dict(dhidden=A - 128), "dhidden overlaps hidden"), (dict(dhidden=A + 10 * 128 - 2), "dhidden overlaps hidden"),
+    (dict(dhidden=B + 256), "dhidden overlaps weight"), (dict(dweight=B + 2), "dweight overlaps weight"),
+    (dict(dweight=A - 99 * 128), "dweight overlaps hidden"), (dict(dhidden=F + 640), "dhidden overlaps dweight"),
+    (dict(dweight=B - 4, dweight_dt=0), "dweight overlaps weight"), (dict(loss=A), "loss overlaps hidden"),
+    (dict(loss=C + 76), "loss overlaps targets"), (dict(row_scale=G + 36), "lse overlaps row_scale"),
+    (dict(ws=A & ~255), "the workspace overlaps hidden"), (dict(lse=D - 36), "loss overlaps lse"),
+    # views of one wider matrix: a window that meets the other's, and rows of another distance
+    (dict(ld_hidden=128, ld_dhidden=128, dhidden=A + 126), "dhidden overlaps hidden"),
+    (dict(ld_hidden=128, ld_dhidden=128, dhidden=A + 256 + 130), "dhidden overlaps hidden"),
+    (dict(ld_hidden=128, ld_dhidden=192, dhidden=A + 128), "dhidden overlaps hidden"),
+    (dict(N=1, dhidden=A + 2), "dhidden overlaps hidden"),
+])
+def test_xent_refuses_overlaps(mir, kw, names):
+    status, message = xent_apart(mir, **kw)
+    assert status == mir.E_INVALID and message == names
+
+
+@pytest.mark.parametrize("kw", [
+    dict(), dict(dhidden=A + 10 * 128), dict(dhidden=A - 10 * 128), dict(hidden=B), dict(weight=A),
+    dict(ld_hidden=128, ld_dhidden=128, dhidden=A + 128), dict(ld_hidden=128, ld_dhidden=128, dhidden=A - 128),
+    dict(ld_hidden=200, ld_dhidden=200, dhidden=A + 128 + 400), dict(N=1, ld_hidden=64, dhidden=A + 128), dict(dweight=None, dhidden=None),
+    dict(ld_dhidden=128, dhidden=E, ld_dweight=128, dweight=E + 128), dict(lse=None, row_scale=G),
+])
+def test_xent_lets_neighbours_through(mir, kw):
+    import torch
+    if torch.cuda.is_available():
+        pytest.skip("made-up addresses: for a machine without a GPU")
+    status, message = xent_apart(mir, **kw)
+    assert status == mir.E_HIP and "overlaps" not in message
+
+
+@pytest.mark.parametrize("kw,names", [
+    (dict(q=A + 16), "q overlaps x"), (dict(s=A), "s overlaps x"), (dict(q=B, s=B + 508), "q overlaps s"),
+    (dict(q=None, s=None, qt=A - 16, st=E), "qt overlaps x"), (dict(q=B, s=C, qt=B + 256, st=E), "q overlaps qt"),
+    (dict(n=3, stride=1 << 20, q=A + (2 << 22)), "q overlaps x"),
+])
+def test_quantize_refuses_overlaps(mir, kw, names):
+    assert quantize(mir, **{**dict(x=A, q=B, s=C), **kw}) == mir.E_INVALID
+    assert mir.lib.shampoo_last_error().decode() == names
+
+
+@pytest.mark.parametrize("kw,names", [
+    (dict(c=A), "c overlaps a"), (dict(c=B + 1020), "c overlaps b"), (dict(c=C - 124), "c overlaps a_scale"), (dict(c=D), "c overlaps b_scale"),
+    (dict(M=64, N=64, K=8192, ws=A, wsb=1 << 30), "the workspace overlaps a"), (dict(M=64, N=64, K=8192, c=F, ws=F, wsb=1 << 30), "c overlaps the workspace"),
+])
+def test_product_refuses_overlaps(mir, kw, names):
+    assert product(mir, **{**dict(a=A, b=B, sa=C, sb=D, c=E), **kw}) == mir.E_INVALID
+    assert mir.lib.shampoo_last_error().decode() == names
+
+
 def test_xent_workspace_is_bounded_by_the_panel(mir):
     """The exponentials of panel_rows rows, not of all; none without gradients."""
     big = dict(N=1 << 16, V=131072, d=64, dhidden=P, dweight=P)
