@@ -528,7 +528,7 @@ typedef enum shampoo_reduction {
  * Logits are never kept: the vocabulary is walked in pieces of 128 columns
  * that leave a maximum and a sum each.  For gradients the rows are taken
  * panel_rows at a time (0: as many as keep the panel of exponentials within
- * 2.25 GiB), with the panel in the workspace (256-byte aligned).  V and the row
+ * 2 GiB), with the panel in the workspace (256-byte aligned).  V and the row
  * strides of hidden and weight at most 2^20, d at most 2^18.  What the call
  * writes (dhidden, dweight, loss, lse, the workspace) may overlap nothing else
  * of it (E_INVALID); rows may lie between rows of the same stride.  No atomics:

@@ -659,7 +659,7 @@ def shampoo_linear_xent(hidden, weight, targets, loss=None, lse=None, dhidden=No
     receive the gradients; dweight may be float32 beside bfloat16 inputs, and
     accumulate=True adds to it.  lse:
     receives log sum exp of each row.  panel_rows bounds the rows whose
-    exponentials the workspace holds at a time (0: up to 2.25 GiB of them).
+    exponentials the workspace holds at a time (0: up to 2 GiB of them).
     logits_dtype=torch.float8_e4m3fn (bfloat16 hidden only) quantises hidden
     and weight as ``shampoo_quantize_f8`` does and takes the logits from their
     8-bit product; the gradients' products stay in bfloat16."""

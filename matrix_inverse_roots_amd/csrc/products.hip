@@ -320,7 +320,12 @@ shampoo_status matmul_f8_impl(const void* a, int a_dt, const void* sa, int32_t a
 // softmax cross entropy
 // ---------------------------------------------------------------------------
 constexpr int64_t XENT_MAX_ROW = int64_t(1) << 20;  // elements: 256 rows stay within 32-bit offsets
-constexpr int64_t XENT_PANEL_BYTES = int64_t(9) << 28;
+// The default panel's exponentials.  Every further panel reads and writes the
+// weight's float32 gradient again.  From 2 to 1 GiB a call with both gradients
+// loses 7-13% (8192 x 4096 x 131072 21.6 to 23.0 ms, 16384 x 2048 x 131072 23.6 to
+// 26.5, 16384 x 1024 x 65536 6.5 to 7.1), from 4 to 2 GiB 2% (16384 x 2048 x
+// 131072) and from 6 to 3 GiB 4% (32768 x 512 x 100003).
+constexpr int64_t XENT_PANEL_BYTES = int64_t(1) << 31;
 constexpr int64_t XENT_STATS_BYTES = int64_t(1) << 28;
 
 struct XentLayout {
@@ -351,14 +356,17 @@ shampoo_status xent_layout(const shampoo_xent_args* a, XentLayout* L) {
   L->grads = a->dhidden || a->dweight;
   L->pieces = (a->V + 127) / 128;
   L->ldE = L->pieces * 128;
-  // rows a large power of two apart fall on the same cache channels (131072
-  // bfloat16 columns: the weight's gradient fetches 15.9 instead of 23.5 GB, the
-  // call 21.20 instead of 21.29 ms; at 32768 columns 167 instead of 165 us)
+  // rows a multiple of 128 KiB apart fall on the same cache channels when the
+  // weight's gradient reads them across (131072 bfloat16 columns: 15.9 instead
+  // of 23.5 GB fetched).  The call, apart against not, in bfloat16: 131072 columns
+  // 6.84 and 7.07 ms (8192 rows, d 1024), 1.90 and 1.98 (2048, 1024), 21.39 and
+  // 21.50 (8192, 4096); 196608: 9.29 and 9.40; 65536: 3.43 and 3.45, 10.74 and
+  // 10.79; 262144: 7.46 and 7.42; float32 at 32768 to 131072 within 0.5%.
   if (L->ldE * es % 131072 == 0) L->ldE += 128;
   int64_t rows = a->panel_rows;
   if (rows == 0) {
     rows = XENT_STATS_BYTES / (L->pieces * 8);
-    if (L->grads) rows = std::min(rows, XENT_PANEL_BYTES / (L->ldE * es));
+    if (L->grads) rows = std::min(rows, XENT_PANEL_BYTES / (L->pieces * 128 * es));
     rows = std::min<int64_t>(std::max<int64_t>(rows / 256 * 256, 256), 131072);
     // panels of one size rather than a short last one
     const int64_t count = (a->N + rows - 1) / rows;

@@ -204,6 +204,16 @@ def test_xent_workspace_is_bounded_by_the_panel(mir):
     assert st == mir.OK and none < 1 << 16
 
 
+@pytest.mark.parametrize("V", [65536, 100000, 131072, 131073, 262144])
+def test_xent_default_panel(mir, V):
+    """2 GiB of exponentials at every width: a batch that they hold is one panel, 256 rows more are two."""
+    rows = (1 << 31) // (-(-V // 128) * 256) // 256 * 256
+    for N, panel in ((rows, rows), (rows + 256, (rows + 256 + 511) // 512 * 256)):
+        kw = dict(N=N, V=V, dhidden=P, dweight=P)
+        assert xent(mir, **kw)[1] == xent(mir, panel_rows=panel, **kw)[1] > 0
+        assert xent(mir, **kw)[1] != xent(mir, panel_rows=panel - 256, **kw)[1]
+
+
 def test_python_checks_need_no_gpu(mir):
     import torch
     x = torch.zeros(4, 256)
