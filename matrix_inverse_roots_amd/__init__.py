@@ -416,8 +416,14 @@ def _on_device(*tensors):
     return dev
 
 
+def _own_stream(stream, dev):
+    if stream is not None and stream.device.index != dev.index:
+        raise ValueError("stream of %s for tensors on %s" % (stream.device, dev))
+
+
 def _launch(fn, dev, stream, *args):
     """fn(*args, stream) with ``dev`` current, on ``stream`` or the current one of that device."""
+    _own_stream(stream, dev)
     torch = _torch()
     if torch.cuda.current_device() == dev.index:
         if stream is None:
@@ -437,6 +443,7 @@ def _empty(shape, dtype, dev, stream):
     torch = _torch()
     if stream is None:
         return torch.empty(shape, dtype=dtype, device=dev)
+    _own_stream(stream, dev)
     with torch.cuda.stream(stream):
         return torch.empty(shape, dtype=dtype, device=dev)
 

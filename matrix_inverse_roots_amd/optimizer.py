@@ -15,7 +15,7 @@ import math
 import numpy as np
 
 from . import (RootOpts, StepArgsC, GRAFTS, FALLBACKS, F32, F64, BF16, shampoo_linear_xent,
-               shampoo_plan_blocks, shampoo_step, shampoo_step_workspace, table_to_device, _empty, _ptr)
+               shampoo_plan_blocks, shampoo_step, shampoo_step_workspace, table_to_device, _empty, _own_stream, _ptr)
 
 
 def reshape_2d(shape):
@@ -271,6 +271,7 @@ class Shampoo:
         gdt = self.hp["grad_dtype"]
         if hidden.dtype == torch.float32 and gdt != torch.float32:
             raise ValueError("projection_loss: float32 hidden needs float32 gradients (grad_dtype)")
+        _own_stream(stream, self.device)
         cur = self._stream(stream)
         ordered = not self._capturing(cur)
         if ordered:

@@ -233,3 +233,16 @@ def test_python_checks_need_no_gpu(mir):
     with pytest.raises(ValueError):
         mir.shampoo_linear_xent_workspace(x, x, torch.zeros(4, dtype=torch.int32))
     assert mir.shampoo_linear_xent_workspace(x, x, torch.zeros(4, dtype=torch.int64)) > 0
+
+
+def test_stream_of_another_device_is_refused(mir):
+    import types
+    import torch
+    there = types.SimpleNamespace(device=torch.device("cuda:1"), cuda_stream=0)
+    here = torch.device("cuda:0")
+    launched = []
+    with pytest.raises(ValueError, match="stream of cuda:1"):
+        mir._launch(lambda *a: launched.append(a), here, there)
+    with pytest.raises(ValueError, match="stream of cuda:1"):
+        mir._empty((4,), torch.float32, here, there)
+    assert not launched
