@@ -483,7 +483,8 @@ shampoo_status shampoo_quantize_f8(const void* x, shampoo_dtype x_dt, int64_t n,
  * run in float32 and are rounded once to c_dt.  For 16-bit results the 8-bit
  * matrix instructions drop products some 2^13 below the largest of an
  * instruction's (1.5e-5 relative on random operands); float32 results are
- * summed without that.  ws: shampoo_matmul_f8_workspace bytes, 256-byte aligned
+ * summed without that, as are all results of M <= 4 (so a row's 16-bit result
+ * may differ in its last bit between a call of four rows and one of five).  ws: shampoo_matmul_f8_workspace bytes, 256-byte aligned
  * (0 for most shapes: float32 partial results where few outputs share a long
  * K).  c and ws may not overlap the operands.  Results do not depend on the stream, the workspace's contents or the
  * run. */
@@ -516,7 +517,9 @@ typedef enum shampoo_reduction {
 /* dt: F32 or BF16, the type of hidden and dhidden; weight_dt: dt, or F32
  * beside BF16 (the weight is then rounded to bfloat16 in the workspace: an
  * optimizer's float32 parameter); ld_*: elements between rows.  Products run on that type's matrix cores and sum in float32;
- * for BF16 the softmax enters the gradients' products rounded to bfloat16.
+ * for BF16 the softmax, times row_scale, enters the gradients' products rounded to
+ * bfloat16.  The loss is formed from differences of the logits themselves:
+ * never negative, and with its digits kept where the target's probability is close to one.
  * logits_dt: dt, or E4M3 beside BF16: hidden and weight are quantised as
  * shampoo_quantize_f8 does (a scale for each 128 entries of a row) and the
  * logits are their 8-bit product; the softmax and its gradient are those of
@@ -525,10 +528,12 @@ typedef enum shampoo_reduction {
  * (F32 only for dt F32); accumulate: dweight += instead of =.
  * lse: float32 [N], the rows' log sum exp, or null.
  * row_scale: float32 [N] or null (all ones).
- * Logits are never kept: the vocabulary is walked in pieces of 128 columns
- * that leave a maximum and a sum each.  For gradients the rows are taken
- * panel_rows at a time (0: as many as keep the panel of exponentials within
- * 2 GiB), with the panel in the workspace (256-byte aligned).  V and the row
+ * Logits are not kept: the vocabulary is walked in pieces of 128 columns that
+ * leave a maximum and a sum each, and a loss alone needs no more.  For
+ * gradients the pieces' exponentials are kept, in type dt: rows are taken
+ * panel_rows at a time (0: as many as keep that panel within 2 GiB; a batch
+ * below that keeps as many bytes as its logits would be), with the panel in
+ * the workspace (256-byte aligned).  V and the row
  * strides of hidden and weight at most 2^20, d at most 2^18.  What the call
  * writes (dhidden, dweight, loss, lse, the workspace) may overlap nothing else
  * of it (E_INVALID); rows may lie between rows of the same stride.  No atomics:

@@ -654,7 +654,8 @@ def shampoo_linear_xent(hidden, weight, targets, loss=None, lse=None, dhidden=No
                         ignore_index=-100, reduction="mean", scale=1.0, accumulate=False, panel_rows=0, logits_dtype=None,
                         ws=None, stream=None):
     """Softmax cross entropy of the projection hidden weight^T against
-    ``targets``, without keeping its logits; returns the loss.
+    ``targets``; returns the loss.  Alone it keeps no logits; with gradients
+    the exponentials of a panel of rows, in hidden's type.
 
     hidden [N, d] and weight [V, d] (float32 or bfloat16, unit column
     stride; a float32 weight beside bfloat16 hidden is rounded to bfloat16),

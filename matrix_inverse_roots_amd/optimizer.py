@@ -243,14 +243,15 @@ class Shampoo:
     def projection_loss(self, index, hidden, targets, dhidden=None, row_scale=None, ignore_index=-100,
                         reduction="mean", scale=1.0, panel_rows=0, logits_dtype=None, stream=None):
         """Softmax cross entropy of hidden params[index]^T against ``targets``
-        (``shampoo_linear_xent``: the logits are never kept); returns the loss.
+        (``shampoo_linear_xent``); returns the loss.
 
         params[index] is the output projection [vocabulary, width]; hidden
         [tokens, width] is float32, or bfloat16 (the parameter is then
         rounded to bfloat16 for the products).  The parameter's gradient goes
         to a buffer of the optimizer's gradient type, which the next ``step``
         takes where its gradient is given as None; calls before that step add
-        to it (micro-batches: give each its share in ``scale``), and a step
+        to it in that type (micro-batches: give each its share in ``scale``;
+        bfloat16 gradients are rounded at each, float32 ones are not), and a step
         that is given another gradient there drops it.  dhidden
         receives hidden's gradient.  Float32 hidden needs float32 gradients.
         logits_dtype=torch.float8_e4m3fn takes the logits from the 8-bit
