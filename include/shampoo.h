@@ -484,10 +484,11 @@ shampoo_status shampoo_quantize_f8(const void* x, shampoo_dtype x_dt, int64_t n,
  * matrix instructions drop products some 2^13 below the largest of an
  * instruction's (1.5e-5 relative on random operands); float32 results are
  * summed without that, as are all results of M <= 4 (so a row's 16-bit result
- * may differ in its last bit between a call of four rows and one of five).  ws: shampoo_matmul_f8_workspace bytes, 256-byte aligned
- * (0 for most shapes: float32 partial results where few outputs share a long
- * K).  c and ws may not overlap the operands.  Results do not depend on the stream, the workspace's contents or the
- * run. */
+ * may differ in its last bit between a call of four rows and one of five).
+ * ws: shampoo_matmul_f8_workspace bytes, 256-byte aligned (0 for most shapes:
+ * float32 partial results where few outputs share a long K).  c and ws may not
+ * overlap the operands.  Results do not depend on the stream, the workspace's
+ * contents or the run. */
 shampoo_status shampoo_matmul_f8_workspace(int64_t n, int64_t M, int64_t N, int64_t K, size_t* bytes);
 shampoo_status shampoo_matmul_f8(const void* a, shampoo_dtype a_dt, const void* a_scale, int32_t a_block_rows,
                                  const void* b, shampoo_dtype b_dt, const void* b_scale, int32_t b_block_rows,
@@ -516,10 +517,11 @@ typedef enum shampoo_reduction {
 
 /* dt: F32 or BF16, the type of hidden and dhidden; weight_dt: dt, or F32
  * beside BF16 (the weight is then rounded to bfloat16 in the workspace: an
- * optimizer's float32 parameter); ld_*: elements between rows.  Products run on that type's matrix cores and sum in float32;
- * for BF16 the softmax, times row_scale, enters the gradients' products rounded to
- * bfloat16.  The loss is formed from differences of the logits themselves:
- * never negative, and with its digits kept where the target's probability is close to one.
+ * optimizer's float32 parameter); ld_*: elements between rows.  Products run
+ * on that type's matrix cores and sum in float32; for BF16 the softmax, times
+ * row_scale, enters the gradients' products rounded to bfloat16.  loss_i is
+ * formed from differences of the logits themselves: never negative, and with
+ * its digits kept where the target's probability is close to one.
  * logits_dt: dt, or E4M3 beside BF16: hidden and weight are quantised as
  * shampoo_quantize_f8 does (a scale for each 128 entries of a row) and the
  * logits are their 8-bit product; the softmax and its gradient are those of
@@ -533,8 +535,8 @@ typedef enum shampoo_reduction {
  * gradients the pieces' exponentials are kept, in type dt: rows are taken
  * panel_rows at a time (0: as many as keep that panel within 2 GiB; a batch
  * below that keeps as many bytes as its logits would be), with the panel in
- * the workspace (256-byte aligned).  V and the row
- * strides of hidden and weight at most 2^20, d at most 2^18.  What the call
+ * the workspace (256-byte aligned).  V and the row strides of hidden and
+ * weight at most 2^20, d at most 2^18.  What the call
  * writes (dhidden, dweight, loss, lse, the workspace) may overlap nothing else
  * of it (E_INVALID); rows may lie between rows of the same stride.  No atomics:
  * two identical calls give identical bits. */
