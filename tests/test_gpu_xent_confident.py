@@ -102,6 +102,24 @@ def test_loss_of_confident_rows_with_8_bit_logits(mir, N, d, V, wdt):
     assert (np.abs(got - want) <= bound)[sure].all(), float((np.abs(got - want) / bound)[sure].max())
 
 
+@pytest.mark.parametrize("kind", ["float32", "bfloat16", "8-bit"])
+@pytest.mark.parametrize("N,V", [(1280, 13312), (2048, 32768)])
+def test_every_target_is_found_over_many_tiles(mir, N, V, kind):
+    """Several tiles for each workgroup, small and large ones, of one to two
+    stages of k each: every row's own target, a few of them in each tile."""
+    import torch
+    d = 64
+    h, w, t = make(N, d, V, "float32" if kind == "float32" else "bfloat16", N, level=100.0)
+    X, W = h.double().cpu().numpy(), w.double().cpu().numpy()
+    if kind == "8-bit":
+        X, W = (ref.stand_for(ref.code_values("e4m3")[q.view(torch.uint8).cpu().numpy()], s.view(torch.uint8).cpu().numpy(), 1)
+                for q, s in (mir.shampoo_quantize_f8(m) for m in (h, w)))
+    got = mir.shampoo_linear_xent(h, w, t, reduction="none", logits_dtype=torch.float8_e4m3fn if kind == "8-bit" else None)
+    want, bound, _, _ = definition(X, W, t.cpu().numpy(), drop=2.0 ** -13 if kind == "8-bit" else 0.0)
+    err = np.abs(got.double().cpu().numpy() - want)
+    assert (got >= 0).all() and (err <= bound).all(), float((err / bound).max())
+
+
 @pytest.mark.parametrize("logits", ["own", "8-bit"])
 @pytest.mark.parametrize("dt", ["float32", "bfloat16"])
 def test_a_vocabulary_of_one(mir, dt, logits):
