@@ -1,8 +1,8 @@
 /*
  * shampoo.h -- C ABI of the batched block preconditioner step of
- * block-diagonal Shampoo, for AMD Instinct MI355X (gfx950), and of two
- * operators next to it: 8-bit block-scaled products and the softmax cross
- * entropy of an output projection with its gradients.
+ * block-diagonal Shampoo, for AMD Instinct MI355X (gfx950), and of operators
+ * next to it: 8-bit block-scaled products, the softmax cross entropy of an
+ * output projection with its gradients, and feed-forward layers with theirs.
  *
  * Sources cited below (titles of the pages; sections as named there):
  *   [DASH]  "DASH: Faster Shampoo via Batched Block Preconditioning and
@@ -567,6 +567,172 @@ typedef struct shampoo_xent_args {
 /* Workspace bytes for these arguments (ws fields ignored). */
 shampoo_status shampoo_linear_xent_workspace(const shampoo_xent_args* args, size_t* bytes);
 shampoo_status shampoo_linear_xent(const shampoo_xent_args* args, hipStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Feed-forward layers: a product with bias, activation and residual in its
+ * epilogue, and the gated block, with their gradients and with what the
+ * backward pass needs kept in 8 bits.
+ *
+ * Layer:  z = x w^T + bias,  y = act(z) + residual,
+ *   x [M, K], w [N, K], bias [N], z, y, residual [M, N];
+ *   dz = dy act'(z),  dx = dz w,  dw = dz^T x,  dbias = sum of dz's rows
+ *   (the residual's gradient is dy itself).
+ * Block:  g = x w_gate^T,  u = x w_up^T,  h = act(g) u,  y = h w_down^T + residual,
+ *   x, y, residual [T, d], w_gate, w_up [f, d], w_down [d, f], g, u, h [T, f];
+ *   dh = dy w_down,  du = dh act(g),  dg = dh u act'(g),
+ *   dx = dg w_gate + du w_up,  dw_gate = dg^T x,  dw_up = du^T x,  dw_down = dy^T h.
+ *
+ * Types.  dt: F32 or BF16, of x, dy and dx; products run on that type's matrix
+ * cores and sum in float32; bias, activation, products of activations,
+ * residual and sums over rows are float32, rounded once where they are
+ * stored.  Weights are in dt, or F32 beside BF16 (rounded to bfloat16 for the
+ * products).  Between two products h, dz, dg and du are rounded to dt (h of at
+ * most 4 rows stays float32).  Formulas are followed where values are not
+ * finite: silu and gelu of minus infinity are NaN.
+ *
+ * Kept.  What a forward call keeps for the backward one, z or g and u, is
+ * written by the products' epilogues and is one of
+ *   dt:   rows ld elements apart;
+ *   E4M3: uint8 values [rows, cols rounded up to 32], zeros behind the
+ *         columns, and uint8 scales, byte e + 127 of 2^e for each 32 columns of
+ *         a row, [rows, that / 32]: 2^e is the least power of two that keeps
+ *         the block's largest finite magnitude within 448 (e = 0 for zeros, e >=
+ *         -127), and a value is rounded once, from float32, to nearest even
+ *         (NaN and infinities: NaN).  Half of bfloat16's bytes, a quarter of
+ *         float32's.
+ * A gradient is that of the formulas at the kept values; y is computed from
+ * the unrounded ones.  x of a weight's gradient may be in 8 bits too: E4M3 as
+ * shampoo_quantize_f8 gives it with block_rows 1 (x_scale), widened exactly in
+ * the workspace.
+ *
+ * Rows may be any stride apart; rows that do not start on 16 bytes, and row
+ * lengths that are no multiple of 16 bytes, cost a copy in the workspace.  M, T
+ * at most 2^29, other sizes at most 2^18, row strides at most 2^20.  An empty batch
+ * leaves weight gradients zero (or unchanged where accumulated).  What a call
+ * writes may overlap nothing else of it (E_INVALID), but y may be residual
+ * itself.  Results do not depend on the stream, the workspace's contents or the
+ * run; a row's result may differ in its last bits between batches of other
+ * sizes.
+ * ------------------------------------------------------------------------- */
+typedef enum shampoo_activation {
+  SHAMPOO_ACT_NONE = 0,
+  SHAMPOO_ACT_RELU = 1,
+  SHAMPOO_ACT_GELU = 2,      /* z Phi(z) */
+  SHAMPOO_ACT_GELU_TANH = 3, /* z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2 */
+  SHAMPOO_ACT_SILU = 4       /* z / (1 + exp(-z)) */
+} shampoo_activation;
+
+/* bias, residual, keep: null for none.  bias_dt: F32, or dt; y_dt (y and
+ * residual): dt or F32; keep_dt: dt or E4M3 (then keep_scale; 16-byte aligned
+ * values, ld_keep unused). */
+typedef struct shampoo_linear_args {
+  const void* x;
+  const void* w;
+  const void* bias;
+  const void* residual;
+  void* y;
+  void* keep;
+  void* keep_scale;
+  int64_t ld_x, ld_w, ld_residual, ld_y, ld_keep;
+  int64_t M, N, K;
+  shampoo_dtype dt;
+  shampoo_dtype w_dt;
+  shampoo_dtype bias_dt;
+  shampoo_dtype y_dt;
+  shampoo_dtype keep_dt;
+  int32_t activation;
+  void* ws;
+  size_t ws_bytes;
+} shampoo_linear_args;
+
+/* dx, dw, dbias: null where not wanted.  kept: z, as kept_dt says (may be null
+ * without an activation); x_dt: dt or E4M3 (read for dw only); dw_dt, dbias_dt: dt or F32;
+ * accumulate: dw and dbias += instead of =. */
+typedef struct shampoo_linear_grad_args {
+  const void* dy;
+  const void* x;
+  const void* x_scale;
+  const void* w;
+  const void* kept;
+  const void* kept_scale;
+  void* dx;
+  void* dw;
+  void* dbias;
+  int64_t ld_dy, ld_x, ld_w, ld_kept, ld_dx, ld_dw;
+  int64_t M, N, K;
+  shampoo_dtype dt;
+  shampoo_dtype x_dt;
+  shampoo_dtype w_dt;
+  shampoo_dtype kept_dt;
+  shampoo_dtype dw_dt;
+  shampoo_dtype dbias_dt;
+  int32_t activation;
+  int32_t accumulate;
+  void* ws;
+  size_t ws_bytes;
+} shampoo_linear_grad_args;
+
+/* keep_gate, keep_up: both or neither; residual may be null. */
+typedef struct shampoo_gated_ffn_args {
+  const void* x;
+  const void* w_gate;
+  const void* w_up;
+  const void* w_down;
+  const void* residual;
+  void* y;
+  void* keep_gate;
+  void* keep_gate_scale;
+  void* keep_up;
+  void* keep_up_scale;
+  int64_t ld_x, ld_gate, ld_up, ld_down, ld_residual, ld_y, ld_keep;
+  int64_t T, d, f;
+  shampoo_dtype dt;
+  shampoo_dtype w_dt;
+  shampoo_dtype y_dt;
+  shampoo_dtype keep_dt;
+  int32_t activation;
+  void* ws;
+  size_t ws_bytes;
+} shampoo_gated_ffn_args;
+
+/* dx, dw_gate, dw_up, dw_down: null where not wanted. */
+typedef struct shampoo_gated_ffn_grad_args {
+  const void* dy;
+  const void* x;
+  const void* x_scale;
+  const void* w_gate;
+  const void* w_up;
+  const void* w_down;
+  const void* kept_gate;
+  const void* kept_gate_scale;
+  const void* kept_up;
+  const void* kept_up_scale;
+  void* dx;
+  void* dw_gate;
+  void* dw_up;
+  void* dw_down;
+  int64_t ld_dy, ld_x, ld_gate, ld_up, ld_down, ld_kept, ld_dx, ld_dw_gate, ld_dw_up, ld_dw_down;
+  int64_t T, d, f;
+  shampoo_dtype dt;
+  shampoo_dtype x_dt;
+  shampoo_dtype w_dt;
+  shampoo_dtype kept_dt;
+  shampoo_dtype dw_dt;
+  int32_t activation;
+  int32_t accumulate;
+  void* ws;
+  size_t ws_bytes;
+} shampoo_gated_ffn_grad_args;
+
+/* Workspace bytes (256-byte aligned) for these arguments, ws fields ignored. */
+shampoo_status shampoo_linear_workspace(const shampoo_linear_args* args, size_t* bytes);
+shampoo_status shampoo_linear(const shampoo_linear_args* args, hipStream_t stream);
+shampoo_status shampoo_linear_grad_workspace(const shampoo_linear_grad_args* args, size_t* bytes);
+shampoo_status shampoo_linear_grad(const shampoo_linear_grad_args* args, hipStream_t stream);
+shampoo_status shampoo_gated_ffn_workspace(const shampoo_gated_ffn_args* args, size_t* bytes);
+shampoo_status shampoo_gated_ffn(const shampoo_gated_ffn_args* args, hipStream_t stream);
+shampoo_status shampoo_gated_ffn_grad_workspace(const shampoo_gated_ffn_grad_args* args, size_t* bytes);
+shampoo_status shampoo_gated_ffn_grad(const shampoo_gated_ffn_grad_args* args, hipStream_t stream);
 
 #ifdef __cplusplus
 }

@@ -31,6 +31,7 @@ GRAFT_SGD, GRAFT_MOMENTUM, GRAFT_ADAM, GRAFT_NONE = 0, 1, 2, 3
 FLAG_NONFINITE, FLAG_ZERO_SCALE, FLAG_PI_FALLBACK, FLAG_RECOMPUTED_F64, FLAG_KEPT_PREVIOUS = 1, 2, 4, 8, 16
 FLAG_RESIDUAL = 32
 REDUCTIONS = {"none": 0, "sum": 1, "mean": 2}
+ACTIVATIONS = {None: 0, "none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 FORMATS_F8 = {"e4m3": E4M3, "e5m2": E5M2}
 FALLBACKS = {"none": 0, "keep": 1, "f64": 2}
 
@@ -105,6 +106,57 @@ class XentArgsC(ctypes.Structure):
                 ("ws", ctypes.c_void_p), ("ws_bytes", ctypes.c_size_t)]
 
 
+class LinearArgsC(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("w", ctypes.c_void_p), ("bias", ctypes.c_void_p),
+                ("residual", ctypes.c_void_p), ("y", ctypes.c_void_p), ("keep", ctypes.c_void_p),
+                ("keep_scale", ctypes.c_void_p),
+                ("ld_x", ctypes.c_int64), ("ld_w", ctypes.c_int64), ("ld_residual", ctypes.c_int64), ("ld_y", ctypes.c_int64),
+                ("ld_keep", ctypes.c_int64), ("M", ctypes.c_int64), ("N", ctypes.c_int64), ("K", ctypes.c_int64),
+                ("dt", ctypes.c_int32), ("w_dt", ctypes.c_int32), ("bias_dt", ctypes.c_int32), ("y_dt", ctypes.c_int32),
+                ("keep_dt", ctypes.c_int32), ("activation", ctypes.c_int32),
+                ("ws", ctypes.c_void_p), ("ws_bytes", ctypes.c_size_t)]
+
+
+class LinearGradArgsC(ctypes.Structure):
+    _fields_ = [("dy", ctypes.c_void_p), ("x", ctypes.c_void_p), ("x_scale", ctypes.c_void_p),
+                ("w", ctypes.c_void_p), ("kept", ctypes.c_void_p), ("kept_scale", ctypes.c_void_p),
+                ("dx", ctypes.c_void_p), ("dw", ctypes.c_void_p), ("dbias", ctypes.c_void_p),
+                ("ld_dy", ctypes.c_int64), ("ld_x", ctypes.c_int64), ("ld_w", ctypes.c_int64), ("ld_kept", ctypes.c_int64),
+                ("ld_dx", ctypes.c_int64), ("ld_dw", ctypes.c_int64), ("M", ctypes.c_int64), ("N", ctypes.c_int64),
+                ("K", ctypes.c_int64),
+                ("dt", ctypes.c_int32), ("x_dt", ctypes.c_int32), ("w_dt", ctypes.c_int32), ("kept_dt", ctypes.c_int32),
+                ("dw_dt", ctypes.c_int32), ("dbias_dt", ctypes.c_int32), ("activation", ctypes.c_int32), ("accumulate", ctypes.c_int32),
+                ("ws", ctypes.c_void_p), ("ws_bytes", ctypes.c_size_t)]
+
+
+class GatedArgsC(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("w_gate", ctypes.c_void_p), ("w_up", ctypes.c_void_p),
+                ("w_down", ctypes.c_void_p), ("residual", ctypes.c_void_p), ("y", ctypes.c_void_p),
+                ("keep_gate", ctypes.c_void_p), ("keep_gate_scale", ctypes.c_void_p), ("keep_up", ctypes.c_void_p),
+                ("keep_up_scale", ctypes.c_void_p),
+                ("ld_x", ctypes.c_int64), ("ld_gate", ctypes.c_int64), ("ld_up", ctypes.c_int64), ("ld_down", ctypes.c_int64),
+                ("ld_residual", ctypes.c_int64), ("ld_y", ctypes.c_int64), ("ld_keep", ctypes.c_int64), ("T", ctypes.c_int64),
+                ("d", ctypes.c_int64), ("f", ctypes.c_int64),
+                ("dt", ctypes.c_int32), ("w_dt", ctypes.c_int32), ("y_dt", ctypes.c_int32), ("keep_dt", ctypes.c_int32),
+                ("activation", ctypes.c_int32),
+                ("ws", ctypes.c_void_p), ("ws_bytes", ctypes.c_size_t)]
+
+
+class GatedGradArgsC(ctypes.Structure):
+    _fields_ = [("dy", ctypes.c_void_p), ("x", ctypes.c_void_p), ("x_scale", ctypes.c_void_p),
+                ("w_gate", ctypes.c_void_p), ("w_up", ctypes.c_void_p), ("w_down", ctypes.c_void_p),
+                ("kept_gate", ctypes.c_void_p), ("kept_gate_scale", ctypes.c_void_p), ("kept_up", ctypes.c_void_p),
+                ("kept_up_scale", ctypes.c_void_p), ("dx", ctypes.c_void_p), ("dw_gate", ctypes.c_void_p),
+                ("dw_up", ctypes.c_void_p), ("dw_down", ctypes.c_void_p),
+                ("ld_dy", ctypes.c_int64), ("ld_x", ctypes.c_int64), ("ld_gate", ctypes.c_int64), ("ld_up", ctypes.c_int64),
+                ("ld_down", ctypes.c_int64), ("ld_kept", ctypes.c_int64), ("ld_dx", ctypes.c_int64), ("ld_dw_gate", ctypes.c_int64),
+                ("ld_dw_up", ctypes.c_int64), ("ld_dw_down", ctypes.c_int64), ("T", ctypes.c_int64), ("d", ctypes.c_int64),
+                ("f", ctypes.c_int64),
+                ("dt", ctypes.c_int32), ("x_dt", ctypes.c_int32), ("w_dt", ctypes.c_int32), ("kept_dt", ctypes.c_int32),
+                ("dw_dt", ctypes.c_int32), ("activation", ctypes.c_int32), ("accumulate", ctypes.c_int32),
+                ("ws", ctypes.c_void_p), ("ws_bytes", ctypes.c_size_t)]
+
+
 EXPORTS = [
     "shampoo_version", "shampoo_last_error", "shampoo_plan_blocks", "shampoo_pack_blocks",
     "shampoo_unpack_blocks", "shampoo_update_stats", "shampoo_inverse_root_workspace",
@@ -113,6 +165,8 @@ EXPORTS = [
     "shampoo_step_workspace", "shampoo_step", "shampoo_check_flags", "shampoo_timing_enable",
     "shampoo_timing_read", "shampoo_mfma_peak", "shampoo_quantize_f8", "shampoo_matmul_f8_workspace",
     "shampoo_matmul_f8", "shampoo_linear_xent_workspace", "shampoo_linear_xent",
+    "shampoo_linear_workspace", "shampoo_linear", "shampoo_linear_grad_workspace", "shampoo_linear_grad",
+    "shampoo_gated_ffn_workspace", "shampoo_gated_ffn", "shampoo_gated_ffn_grad_workspace", "shampoo_gated_ffn_grad",
 ]
 
 
@@ -156,6 +210,10 @@ def _load():
         "shampoo_linear_xent_workspace": ([P(XentArgsC), P(sz)], ctypes.c_int),
         "shampoo_linear_xent": ([P(XentArgsC), vp], ctypes.c_int),
     }
+    for name, args in (("shampoo_linear", LinearArgsC), ("shampoo_linear_grad", LinearGradArgsC),
+                       ("shampoo_gated_ffn", GatedArgsC), ("shampoo_gated_ffn_grad", GatedGradArgsC)):
+        sig[name + "_workspace"] = ([P(args), P(sz)], ctypes.c_int)
+        sig[name] = ([P(args), vp], ctypes.c_int)
     for name in EXPORTS:
         f = getattr(lib, name)
         f.argtypes, f.restype = sig[name]
@@ -684,6 +742,330 @@ def shampoo_linear_xent(hidden, weight, targets, loss=None, lse=None, dhidden=No
     args.ws, args.ws_bytes = ws.data_ptr(), ws.numel() * ws.element_size()
     _launch(lib.shampoo_linear_xent, dev, stream, ctypes.byref(args))
     return loss
+
+
+# ---------------------------------------------------------------------------
+# feed-forward layers
+# ---------------------------------------------------------------------------
+KEEP_BLOCK = 32   # columns of a kept block of 8 bits
+
+
+def shampoo_kept_empty(rows, cols, keep, device, stream=None):
+    """Uninitialised room for what a forward pass keeps of [rows, cols]: keep
+    is a type (torch.float32, torch.bfloat16: a tensor) or "e4m3" (values and
+    scales)."""
+    torch = _torch()
+    device = torch.device(device)
+    if device.type == "cuda" and device.index is None:
+        device = torch.device("cuda", torch.cuda.current_device())
+    if keep != "e4m3":
+        if keep not in (torch.float32, torch.bfloat16):
+            raise ValueError("keep must be torch.float32, torch.bfloat16 or 'e4m3'")
+        return _empty((rows, cols), keep, device, stream)
+    wide = _up(cols, KEEP_BLOCK)
+    return (_empty((rows, wide), torch.float8_e4m3fn, device, stream),
+            _empty((rows, wide // KEEP_BLOCK), torch.float8_e8m0fnu, device, stream))
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+def _float_rows(t, name, rows, cols, dtypes):
+    """(pointer, elements between rows) of a [rows, cols] tensor in one of two types."""
+    if t is None:
+        return None, cols
+    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols or (t.dtype != dtypes[0] and t.dtype != dtypes[1]):
+        raise ValueError("%s must be a %s tensor of shape %s, got %s %s" % (
+            name, " or ".join(sorted({str(d) for d in dtypes})), (rows, cols), t.dtype, tuple(t.shape)))
+    down, across = t.stride()
+    if cols > 1 and across != 1 and rows:
+        raise ValueError("%s must have unit column stride" % name)
+    if rows <= 1:
+        down = cols
+    elif down < cols:
+        raise ValueError("%s must not overlap itself" % name)
+    return t.data_ptr(), down
+
+
+def _kept_rows(t, name, rows, cols, dtype):
+    """(values, scales, stride, type code) of what is kept of [rows, cols]."""
+    torch = _torch()
+    if t is None:
+        return None, None, cols, _dtype_code_of(dtype)
+    if isinstance(t, torch.Tensor):
+        p, ld = _float_rows(t, name, rows, cols, (dtype, dtype))
+        return p, None, ld, _dtype_code_of(dtype)
+    q, s = t
+    wide = _up(cols, KEEP_BLOCK)
+    for v, shape, kinds in ((q, (rows, wide), (torch.float8_e4m3fn,)),
+                            (s, (rows, wide // KEEP_BLOCK), (torch.float8_e8m0fnu, torch.uint8))):
+        if tuple(v.shape) != shape or v.dtype not in kinds or not v.is_contiguous():
+            raise ValueError("%s in 8 bits must be contiguous %s of shape %s, got %s %s" % (
+                name, kinds[0], shape, v.dtype, tuple(v.shape)))
+    return q.data_ptr(), s.data_ptr(), wide, E4M3
+
+
+def _given_rows(t, name, rows, cols, dtype):
+    """The same of an operand that may be in 8 bits as ``shampoo_quantize_f8`` gives it (block_rows 1)."""
+    torch = _torch()
+    if t is None or isinstance(t, torch.Tensor):
+        p, ld = _float_rows(t, name, rows, cols, (dtype, dtype))
+        return p, None, ld, _dtype_code_of(dtype)
+    q, s = t
+    wide = _up(cols, 128)
+    for v, shape, kinds in ((q, (rows, wide), (torch.float8_e4m3fn,)),
+                            (s, (rows, _up(wide // 128, 4)), (torch.float8_e8m0fnu, torch.uint8))):
+        if tuple(v.shape) != shape or v.dtype not in kinds or not v.is_contiguous():
+            raise ValueError("%s in 8 bits must be contiguous %s of shape %s, got %s %s" % (
+                name, kinds[0], shape, v.dtype, tuple(v.shape)))
+    return q.data_ptr(), s.data_ptr(), wide, E4M3
+
+
+def _dtype_code_of(dtype):
+    return F32 if dtype == _torch().float32 else BF16
+
+
+def _vector(t, name, n, dtypes):
+    if t is None:
+        return None
+    if t.dim() != 1 or t.shape[0] != n or t.dtype not in dtypes or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous %s tensor of shape (%d,), got %s %s" % (
+            name, " or ".join(sorted({str(d) for d in dtypes})), n, t.dtype, tuple(t.shape)))
+    return t.data_ptr()
+
+
+def _parts(t):
+    """The tensors of something kept (one, or values and scales)."""
+    return () if t is None else (t,) if isinstance(t, _torch().Tensor) else tuple(t)
+
+
+def _layer_types(x, act):
+    torch = _torch()
+    if x.dtype != torch.float32 and x.dtype != torch.bfloat16:
+        raise TypeError("unsupported dtype %s (float32, bfloat16)" % x.dtype)
+    code = ACTIVATIONS.get(act)
+    if code is None:
+        raise ValueError("activation must be one of %s" % [a for a in ACTIVATIONS if a is not None])
+    return x.dtype, code
+
+
+def _with_workspace(name, args, ws, dev, stream):
+    """Runs lib.<name> on ``args``, with a workspace of its own unless one is given."""
+    if ws is None:
+        need = ctypes.c_size_t(0)
+        _check(getattr(lib, name + "_workspace")(ctypes.byref(args), ctypes.byref(need)))
+        if need.value:
+            ws = _empty(need.value, _torch().uint8, dev, stream)
+    if ws is not None:
+        args.ws, args.ws_bytes = ws.data_ptr(), ws.numel() * ws.element_size()
+    _launch(getattr(lib, name), dev, stream, ctypes.byref(args))
+
+
+def _workspace_of(name, args):
+    need = ctypes.c_size_t(0)
+    _check(getattr(lib, name + "_workspace")(ctypes.byref(args), ctypes.byref(need)))
+    return need.value
+
+
+def _linear_args(x, w, y, bias, activation, residual, keep):
+    torch = _torch()
+    if x.dim() != 2 or w.dim() != 2:
+        raise ValueError("x and w must have 2 dimensions")
+    dt, act = _layer_types(x, activation)
+    M, K = x.shape
+    N = w.shape[0]
+    both = (dt, torch.float32)
+    xp, ldx = _float_rows(x, "x", M, K, (dt, dt))
+    wp, ldw = _float_rows(w, "w", N, K, both)
+    yp, ldy = _float_rows(y, "y", M, N, both)
+    ydt = dt if y is None else y.dtype
+    rp, ldr = _float_rows(residual, "residual", M, N, (ydt, ydt))
+    bp = _vector(bias, "bias", N, both)
+    kp, ks, ldk, kdt = _kept_rows(keep, "keep", M, N, dt)
+    code = _dtype_code_of(dt)
+    return LinearArgsC(xp, wp, bp, rp, yp, kp, ks, ldx, ldw, ldr, ldy, ldk, M, N, K, code, _dtype_code_of(w.dtype),
+                       code if bias is None else _dtype_code_of(bias.dtype), _dtype_code_of(ydt), kdt, act, None, 0)
+
+
+def shampoo_linear_workspace(x, w, y=None, bias=None, activation=None, residual=None, keep=None):
+    """Workspace bytes of ``shampoo_linear`` with these tensors."""
+    return _workspace_of("shampoo_linear", _linear_args(x, w, y, bias, activation, residual, keep))
+
+
+def shampoo_linear(x, w, y=None, bias=None, activation=None, residual=None, keep=None, ws=None, stream=None):
+    """y = act(x w^T + bias) + residual in one product's epilogue; returns y.
+
+    x [M, K] float32 or bfloat16, w [N, K] in x's type or float32 (rounded to
+    bfloat16 beside bfloat16 x: an optimizer's parameter), unit column
+    strides; bias [N], x's type or float32; activation None, "relu", "gelu",
+    "gelu_tanh" or "silu"; residual [M, N] in y's type (it may be y); y in x's
+    type (default) or float32.  keep receives x w^T + bias for
+    ``shampoo_linear_grad``: a tensor [M, N] of x's type, or values and scales
+    in 8 bits (``shampoo_kept_empty(M, N, "e4m3", device)``)."""
+    dev = _on_device(x, w, y, bias, residual, ws, *_parts(keep))
+    if y is None:
+        y = _empty((x.shape[0], w.shape[0]), x.dtype, dev, stream)
+    _with_workspace("shampoo_linear", _linear_args(x, w, y, bias, activation, residual, keep), ws, dev, stream)
+    return y
+
+
+def _linear_grad_args(dy, x, w, kept, activation, dx, dw, dbias, accumulate):
+    torch = _torch()
+    if dy.dim() != 2:
+        raise ValueError("dy must have 2 dimensions")
+    dt, act = _layer_types(dy, activation)
+    M, N = dy.shape
+    K = next((t.shape[1] for t in (w, dw, dx) if t is not None and t.dim() == 2), None)
+    if K is None:
+        if dbias is None:
+            raise ValueError("no gradient is asked for")
+        K = 1
+    if dx is not None and w is None:
+        raise ValueError("dx needs w")
+    if dw is not None and x is None:
+        raise ValueError("dw needs x")
+    if act and kept is None:
+        raise ValueError("the activation's gradient needs what the forward pass kept")
+    both = (dt, torch.float32)
+    dyp, lddy = _float_rows(dy, "dy", M, N, (dt, dt))
+    xp, xs, ldx, xdt = _given_rows(x if dw is not None else None, "x", M, K, dt)
+    wp, ldw = _float_rows(w if dx is not None else None, "w", N, K, both)
+    kp, ks, ldk, kdt = _kept_rows(kept if act else None, "kept", M, N, dt)
+    dxp, lddx = _float_rows(dx, "dx", M, K, (dt, dt))
+    dwp, lddw = _float_rows(dw, "dw", N, K, both)
+    dbp = _vector(dbias, "dbias", N, both)
+    code = _dtype_code_of(dt)
+    return LinearGradArgsC(dyp, xp, xs, wp, kp, ks, dxp, dwp, dbp, lddy, ldx, ldw, ldk, lddx, lddw, M, N, K, code, xdt,
+                           code if wp is None else _dtype_code_of(w.dtype), kdt,
+                           code if dw is None else _dtype_code_of(dw.dtype),
+                           code if dbias is None else _dtype_code_of(dbias.dtype), act, 1 if accumulate else 0, None, 0)
+
+
+def shampoo_linear_grad_workspace(dy, x, w, kept=None, activation=None, dx=None, dw=None, dbias=None):
+    """Workspace bytes of ``shampoo_linear_grad`` with these tensors."""
+    return _workspace_of("shampoo_linear_grad", _linear_grad_args(dy, x, w, kept, activation, dx, dw, dbias, False))
+
+
+def shampoo_linear_grad(dy, x, w, kept=None, activation=None, dx=None, dw=None, dbias=None, accumulate=False, ws=None,
+                        stream=None):
+    """Gradients of ``shampoo_linear`` from dy [M, N]: dz = dy act'(kept),
+    dx = dz w, dw = dz^T x, dbias = sum of dz's rows, each written to the tensor
+    given for it (dx in dy's type, dw and dbias in it or float32;
+    accumulate=True adds to dw and dbias).  The residual's gradient is dy.
+    x is as in the forward pass, or 8 bits of it (values and scales, e4m3, as
+    ``shampoo_quantize_f8`` returns them with block_rows=1); kept is what the
+    forward pass kept, as it was kept.  Returns (dx, dw, dbias)."""
+    dev = _on_device(dy, w, dx, dw, dbias, ws, *_parts(x), *_parts(kept))
+    args = _linear_grad_args(dy, x, w, kept, activation, dx, dw, dbias, accumulate)
+    _with_workspace("shampoo_linear_grad", args, ws, dev, stream)
+    return dx, dw, dbias
+
+
+def _gated_sizes(x, w_gate):
+    if x.dim() != 2 or w_gate.dim() != 2:
+        raise ValueError("x and the weights must have 2 dimensions")
+    return x.shape[0], x.shape[1], w_gate.shape[0]
+
+
+def _gated_weights(w_gate, w_up, w_down, d, f, dt):
+    torch = _torch()
+    kind = w_gate.dtype if w_gate is not None else w_down.dtype
+    if kind != dt and kind != torch.float32:
+        raise ValueError("weights must be %s or torch.float32, got %s" % (dt, kind))
+    one = (kind, kind)
+    return (_float_rows(w_gate, "w_gate", f, d, one), _float_rows(w_up, "w_up", f, d, one),
+            _float_rows(w_down, "w_down", d, f, one), _dtype_code_of(kind))
+
+
+def _gated_args(x, w_gate, w_up, w_down, y, activation, residual, keep):
+    torch = _torch()
+    T, d, f = _gated_sizes(x, w_gate)
+    dt, act = _layer_types(x, activation)
+    both = (dt, torch.float32)
+    xp, ldx = _float_rows(x, "x", T, d, (dt, dt))
+    (gp, ldg), (up, ldu), (dp, ldd), wdt = _gated_weights(w_gate, w_up, w_down, d, f, dt)
+    yp, ldy = _float_rows(y, "y", T, d, both)
+    ydt = dt if y is None else y.dtype
+    rp, ldr = _float_rows(residual, "residual", T, d, (ydt, ydt))
+    a, b = (None, None) if keep is None else keep
+    (kg, sg, ldk, kdt), (ku, su, ldk2, kdt2) = _kept_rows(a, "keep[0]", T, f, dt), _kept_rows(b, "keep[1]", T, f, dt)
+    if ldk != ldk2 or kdt != kdt2:
+        raise ValueError("both projections must be kept in one type, with one row stride")
+    return GatedArgsC(xp, gp, up, dp, rp, yp, kg, sg, ku, su, ldx, ldg, ldu, ldd, ldr, ldy, ldk, T, d, f,
+                      _dtype_code_of(dt), wdt, _dtype_code_of(ydt), kdt, act, None, 0)
+
+
+def shampoo_gated_ffn_workspace(x, w_gate, w_up, w_down, y=None, activation="silu", residual=None, keep=None):
+    """Workspace bytes of ``shampoo_gated_ffn`` with these tensors."""
+    return _workspace_of("shampoo_gated_ffn", _gated_args(x, w_gate, w_up, w_down, y, activation, residual, keep))
+
+
+def shampoo_gated_ffn(x, w_gate, w_up, w_down, y=None, activation="silu", residual=None, keep=None, ws=None, stream=None):
+    """y = (act(x w_gate^T) * (x w_up^T)) w_down^T + residual; returns y.
+
+    x [T, d], w_gate and w_up [f, d], w_down [d, f], residual and y [T, d], in
+    the types of ``shampoo_linear``.  keep: a pair that receives x w_gate^T and
+    x w_up^T for ``shampoo_gated_ffn_grad``, each as in ``shampoo_linear``
+    (tensors of x's type with one row stride, or values and scales in 8 bits)."""
+    kept = () if keep is None else _parts(keep[0]) + _parts(keep[1])
+    dev = _on_device(x, w_gate, w_up, w_down, y, residual, ws, *kept)
+    if y is None:
+        y = _empty(x.shape, x.dtype, dev, stream)
+    _with_workspace("shampoo_gated_ffn", _gated_args(x, w_gate, w_up, w_down, y, activation, residual, keep), ws, dev, stream)
+    return y
+
+
+def _gated_grad_args(dy, x, w_gate, w_up, w_down, kept, dx, dw_gate, dw_up, dw_down, activation, accumulate):
+    torch = _torch()
+    if dy.dim() != 2 or w_down.dim() != 2:
+        raise ValueError("dy and the weights must have 2 dimensions")
+    dt, act = _layer_types(dy, activation)
+    T, d = dy.shape
+    f = w_down.shape[1]
+    both = (dt, torch.float32)
+    if dx is not None and (w_gate is None or w_up is None):
+        raise ValueError("dx needs w_gate and w_up")
+    wanted = dw_gate is not None or dw_up is not None
+    if wanted and x is None:
+        raise ValueError("dw_gate and dw_up need x")
+    dyp, lddy = _float_rows(dy, "dy", T, d, (dt, dt))
+    xp, xs, ldx, xdt = _given_rows(x if wanted else None, "x", T, d, dt)
+    (gp, ldg), (up, ldu), (dp, ldd), wdt = _gated_weights(w_gate if dx is not None else None,
+                                                          w_up if dx is not None else None, w_down, d, f, dt)
+    (kg, sg, ldk, kdt), (ku, su, ldk2, kdt2) = _kept_rows(kept[0], "kept[0]", T, f, dt), _kept_rows(kept[1], "kept[1]", T, f, dt)
+    if ldk != ldk2 or kdt != kdt2:
+        raise ValueError("both projections must have been kept in one type, with one row stride")
+    dxp, lddx = _float_rows(dx, "dx", T, d, (dt, dt))
+    kinds = {t.dtype for t in (dw_gate, dw_up, dw_down) if t is not None}
+    if len(kinds) > 1:
+        raise ValueError("the weights' gradients must be of one type, got %s" % sorted(str(k) for k in kinds))
+    (wgp, ldwg), (wup, ldwu) = _float_rows(dw_gate, "dw_gate", f, d, both), _float_rows(dw_up, "dw_up", f, d, both)
+    wdp, ldwd = _float_rows(dw_down, "dw_down", d, f, both)
+    return GatedGradArgsC(dyp, xp, xs, gp, up, dp, kg, sg, ku, su, dxp, wgp, wup, wdp, lddy, ldx, ldg, ldu, ldd, ldk, lddx,
+                          ldwg, ldwu, ldwd, T, d, f, _dtype_code_of(dt), xdt, wdt, kdt,
+                          _dtype_code_of(kinds.pop() if kinds else dt), act, 1 if accumulate else 0, None, 0)
+
+
+def shampoo_gated_ffn_grad_workspace(dy, x, w_gate, w_up, w_down, kept, dx=None, dw_gate=None, dw_up=None, dw_down=None,
+                                     activation="silu"):
+    """Workspace bytes of ``shampoo_gated_ffn_grad`` with these tensors."""
+    return _workspace_of("shampoo_gated_ffn_grad", _gated_grad_args(dy, x, w_gate, w_up, w_down, kept, dx, dw_gate, dw_up,
+                                                                     dw_down, activation, False))
+
+
+def shampoo_gated_ffn_grad(dy, x, w_gate, w_up, w_down, kept, dx=None, dw_gate=None, dw_up=None, dw_down=None,
+                           activation="silu", accumulate=False, ws=None, stream=None):
+    """Gradients of ``shampoo_gated_ffn`` from dy [T, d] and what the forward
+    pass kept (the pair, as it was kept), each written to the tensor given for
+    it: dx in dy's type, the weights' in it or float32 (one type for the three;
+    accumulate=True adds to them).  x may be in 8 bits as in
+    ``shampoo_linear_grad``.  The residual's gradient is dy.  Returns
+    (dx, dw_gate, dw_up, dw_down)."""
+    dev = _on_device(dy, w_gate, w_up, w_down, dx, dw_gate, dw_up, dw_down, ws, *_parts(x), *_parts(kept[0]), *_parts(kept[1]))
+    args = _gated_grad_args(dy, x, w_gate, w_up, w_down, kept, dx, dw_gate, dw_up, dw_down, activation, accumulate)
+    _with_workspace("shampoo_gated_ffn_grad", args, ws, dev, stream)
+    return dx, dw_gate, dw_up, dw_down
 
 
 from .optimizer import Shampoo, ShampooStack  # noqa: E402  (needs the binding above)

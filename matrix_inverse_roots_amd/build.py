@@ -14,10 +14,12 @@ from concurrent.futures import ThreadPoolExecutor
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 LIB = os.path.join(PKG, "libshampoo.so")
-SOURCES = [os.path.join(PKG, "csrc", f) for f in ("shampoo.hip", "products.hip")]
+SOURCES = [os.path.join(PKG, "csrc", f) for f in ("shampoo.hip", "products.hip", "ffn.hip")]
 HEADERS = [os.path.join(PKG, "csrc", f) for f in ("gemm_common.hpp", "gemm.hpp", "gemm_hsym.hpp", "gemm_nn256.hpp",
                                                   "kernels.hpp", "host_common.hpp", "product_core.hpp",
-                                                  "product_plan.hpp", "product_passes.hpp",
+                                                  "product_types.hpp", "product_plan.hpp",
+                                                  "product_passes.hpp", "activation.hpp", "ffn_epilogue.hpp",
+                                                  "ffn_kernels.hpp",
                                                   "f8_kernels.hpp", "f8_rows.hpp", "xent_kernels.hpp")] + [
     os.path.join(ROOT, "include", "shampoo.h")]
 

@@ -1,0 +1,97 @@
+// Activations of the feed-forward layers and their derivatives, in float32.
+//
+//   relu       max(z, 0)
+//   gelu       z Phi(z), Phi the normal distribution's
+//   gelu_tanh  z sigma(p(z)), p(z) = 2 sqrt(2 / pi) (z + 0.044715 z^3):
+//              (1 + tanh(y)) / 2 = sigma(2 y)
+//   silu       z sigma(z)
+// sigma(p) = 1 / (1 + 2^(-p log2 e)): one exp2 and one reciprocal instruction,
+// off by some 2^-22 and |p| 2^-24 relative.  Phi(-|z|) = t P(t) e^(-z^2/2) / 2 with
+// t = 1 / (1 + 0.45 |z| / sqrt 2) and P of degree 9, fitted (least squares
+// reweighted towards the largest relative error) to erfc(x) e^(x^2) / t over
+// all x >= 0: 3.2e-8 relative in exact arithmetic, 3.6e-7 at most as it is
+// evaluated here.  Small probabilities keep their digits, which 1 + erf would
+// lose, and the exponential serves the derivative too.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace shampoo {
+
+struct ActNone {
+  __device__ __forceinline__ float value(float z) const { return z; }
+  __device__ __forceinline__ float both(float z, float& slope) const {
+    slope = 1.f;
+    return z;
+  }
+};
+
+struct ActRelu {
+  __device__ __forceinline__ float value(float z) const { return z < 0.f ? 0.f : z; }  // a NaN stays one
+  __device__ __forceinline__ float both(float z, float& slope) const {
+    slope = z <= 0.f ? 0.f : 1.f;
+    return value(z);
+  }
+};
+
+struct ActGelu {
+  // Phi(z), and e^(-z^2/2)
+  __device__ __forceinline__ float cdf(float z, float& bell) const {
+    const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.3181980515339464f, fabsf(z), 1.f));
+    bell = __builtin_amdgcn_exp2f(z * z * -0.7213475204444817f);
+    float p = -0.0413922855f;
+    p = __builtin_fmaf(p, t, 0.1906930092f);
+    p = __builtin_fmaf(p, t, -0.3005917998f);
+    p = __builtin_fmaf(p, t, 0.1424101846f);
+    p = __builtin_fmaf(p, t, -0.0223633167f);
+    p = __builtin_fmaf(p, t, 0.1199523115f);
+    p = __builtin_fmaf(p, t, 0.1752517454f);
+    p = __builtin_fmaf(p, t, 0.2282716835f);
+    p = __builtin_fmaf(p, t, 0.2538831608f);
+    p = __builtin_fmaf(p, t, 0.2538853208f);
+    const float q = 0.5f * (p * t) * bell;
+    return z < 0.f ? q : 1.f - q;
+  }
+  __device__ __forceinline__ float value(float z) const {
+    float bell;
+    return z * cdf(z, bell);
+  }
+  __device__ __forceinline__ float both(float z, float& slope) const {
+    float bell;
+    const float c = cdf(z, bell);
+    slope = __builtin_fmaf(z * 0.3989422804014327f, bell, c);
+    return z * c;
+  }
+};
+
+// z sigma(c1 z + c3 z^3)
+struct ActSigmoid {
+  float c1, c3;
+  __device__ __forceinline__ float sigma(float z) const {
+    constexpr float L2E = 1.4426950408889634f;
+    const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(-c3 * L2E, z * z, -c1 * L2E) * z);
+    return __builtin_amdgcn_rcpf(1.f + e);
+  }
+  __device__ __forceinline__ float value(float z) const { return z * sigma(z); }
+  __device__ __forceinline__ float both(float z, float& slope) const {
+    const float s = sigma(z);
+    // behind 10^4 sigma is 0 or 1, and z p'(z) would overflow
+    const float w = fminf(fmaxf(z, -1e4f), 1e4f);
+    slope = __builtin_fmaf(s * (1.f - s), w * __builtin_fmaf(3.f * c3, w * w, c1), s);
+    return z * s;
+  }
+};
+
+// f(the activation of SHAMPOO_ACT_* code `act`)
+template <typename F> __device__ __forceinline__ void with_activation(int act, F f) {
+  switch (act) {
+    case 1: f(ActRelu{}); break;
+    case 2: f(ActGelu{}); break;
+    case 3: f(ActSigmoid{1.5957691216057308f, 0.07135481627260025f}); break;
+    case 4: f(ActSigmoid{1.f, 0.f}); break;
+    default: f(ActNone{}); break;
+  }
+}
+
+}  // namespace shampoo

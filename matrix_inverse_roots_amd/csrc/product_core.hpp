@@ -58,54 +58,10 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
-#include "gemm_common.hpp"
+#include "ffn_epilogue.hpp"
+#include "product_types.hpp"
 
 namespace shampoo {
-
-typedef float floatx16 __attribute__((ext_vector_type(16)));
-typedef int intx8 __attribute__((ext_vector_type(8)));
-typedef short shortx4_t __attribute__((ext_vector_type(4)));
-typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
-typedef float floatx2 __attribute__((ext_vector_type(2)));
-
-enum class Elem { BF16, F32, F8, F8W };
-enum class Epi { STORE, SOFTMAX };
-
-struct ProductArgs {
-  const void* A;
-  const void* B;
-  const uint8_t* sa;  // F8: scales, [rows >> sa_shift][ldsa] bytes, 4-byte aligned rows
-  const uint8_t* sb;
-  void* C;            // STORE: float32, bfloat16 or half by c_dt; SOFTMAX: exponentials (may be null)
-  int64_t lda, ldb, ldc;              // elements
-  int64_t strideA, strideB, strideC;  // elements between the matrices of a batch
-  int64_t ldsa, ldsb, strideSa, strideSb;
-  int64_t split_stride;               // STORE: elements between the partial results of two k-ranges
-  int M, N, K;
-  int sa_shift, sb_shift;             // 0: a scale per row; 7: per 128 rows
-  int mt, nt;                         // tiles along M and N
-  int nst;                            // k-stages of 128 bytes
-  int splits, split_stages;           // ranges of k; stages of each but the last (F8: a multiple of 4)
-  int c_dt;                           // 0 float32, 1 half, 2 bfloat16
-  int vec;                            // rows of C allow 16-byte stores
-  float alpha, beta;                  // STORE: C = alpha acc + beta C
-  const float* alpha_dev;             // times this, or null
-  int64_t items;                      // batch * splits * mt * nt
-  // SOFTMAX
-  floatx2* stats;                     // [pieces][M]: (max, sum of exp(z - max)) of 128 columns
-  const int64_t* targets;             // [M]
-  float* target_logit;                // [M]: the logit at each row's target, where that is a column
-};
-
-template <Elem E> struct ElemTraits;
-template <> struct ElemTraits<Elem::BF16> { static constexpr int size = 2; };
-template <> struct ElemTraits<Elem::F32> { static constexpr int size = 4; };
-template <> struct ElemTraits<Elem::F8> { static constexpr int size = 1; };
-template <> struct ElemTraits<Elem::F8W> { static constexpr int size = 1; };
-
-// By value: __builtin_bit_cast of a vector's element reads element 0.
-__device__ __forceinline__ float bits_float(uint32_t b) { return __builtin_bit_cast(float, b); }
-__device__ __forceinline__ uint32_t float_bits(float f) { return __builtin_bit_cast(uint32_t, f); }
 
 // matrix-core instructions that a fragment pair (32 bytes a lane) takes
 template <Elem E> constexpr int MMA_STEPS = E == Elem::F8 ? 1 : E == Elem::BF16 ? 2 : E == Elem::F8W ? 4 : 8;
@@ -150,15 +106,6 @@ template <int K> __device__ __forceinline__ void wait_stage() {
   __builtin_amdgcn_s_waitcnt((K & 15) | (0x7 << 4) | ((K >> 4) << 14));
 }
 
-__device__ __forceinline__ uint32_t pack_bf16(float x, float y) {
-  typedef __bf16 b2 __attribute__((ext_vector_type(2)));
-  return __builtin_bit_cast(uint32_t, b2{(__bf16)x, (__bf16)y});
-}
-__device__ __forceinline__ uint32_t pack_f16(float x, float y) {
-  typedef _Float16 h2 __attribute__((ext_vector_type(2)));
-  return __builtin_bit_cast(uint32_t, h2{(_Float16)x, (_Float16)y});
-}
-
 // ds_read_b64_tr_b16.  The restrict-qualified parameter tells the compiler
 // that nothing writes what the read sees while it runs: without it, it would
 // wait for every load into LDS in flight before each such read (the waits
@@ -188,6 +135,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_kernel(ProductArgs g)
   constexpr int NIA = TM / 8 / W, NIB = TN / 8 / W;
   constexpr int SK = 128 / ES;  // k of one stage
   constexpr bool SCALED = E == Elem::F8 || E == Elem::F8W;
+  constexpr bool DUAL = EPI == Epi::GATED, TWO = EPI == Epi::STORE2;
+  constexpr int TNO = DUAL ? TN / 2 : TN;  // columns of a tile's results
   // LDS: NB buffers, then groups of scales (a group each for NB stages ahead at
   // most, and the current one), then as many groups of targets
   constexpr int NI = NIA + NIB, NG = scale_groups(NB), SCALES = NB * STAGE, SGROUP = 4 * (TM + TN);
@@ -198,6 +147,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_kernel(ProductArgs g)
   static_assert(!SCALED || (TM + TN) % (64 * W) == 0, "each wave loads the scales of as many rows");
   static_assert(TM % 64 == 0 && TM <= 64 * W, "a wave loads the targets of 64 rows");
   static_assert(!(AS && TM < 64) && !(BS && TN < 64), "k-strided swizzles need 64 columns");
+  static_assert(!DUAL || (FN == 4 && !BS && NIB * 8 <= 64 && 64 % (NIB * 8) == 0), "a wave loads from one of the two matrices");
+  static_assert(!TWO || BS, "two matrices follow each other along strided k");
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
   typedef __attribute__((address_space(3))) unsigned char lds_u8;
   lds_u8* const lds = (lds_u8*)smem;
@@ -262,7 +213,10 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_kernel(ProductArgs g)
   // of the operand's last row or k-row, past which a descriptor reads zeros.
   const int last = g.nst - 1, rest = g.K - last * SK;  // the last stage, and its k
   uint32_t offA[NIA], offB[NIB], tailA[NIA], tailB[NIB];
-  auto offsets = [&](uint32_t* off, uint32_t* tail, int n, bool strided, int T, int64_t ld) {
+  // DUAL: 64 rows of B1 and 64 of B2 in turn, so that a wave's first two
+  // fragments and its last two are the same columns of both
+  const bool second = DUAL && ((wave * NIB * 8) >> 6 & 1);
+  auto offsets = [&](uint32_t* off, uint32_t* tail, int n, bool strided, int T, int64_t ld, bool dual) {
 #pragma unroll
     for (int q = 0; q < n; ++q) {
       const int at = (wave * n + q) * 1024 + lane * 16;
@@ -272,13 +226,13 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_kernel(ProductArgs g)
         tail[q] = k < rest ? off[q] : RSRC_OUTSIDE;
       } else {
         const int row = at >> 7, byte = 16 * ((lane & 7) ^ ((row >> 1) & 7));
-        off[q] = (uint32_t)(row * ld * ES) + byte;
+        off[q] = (uint32_t)((dual ? (row >> 7) * 64 + (row & 63) : row) * ld * ES) + byte;
         tail[q] = byte < rest * ES ? off[q] : RSRC_OUTSIDE;
       }
     }
   };
-  offsets(offA, tailA, NIA, AS, TM, g.lda);
-  offsets(offB, tailB, NIB, BS, TN, g.ldb);
+  offsets(offA, tailA, NIA, AS, TM, g.lda, false);
+  offsets(offB, tailB, NIB, BS, TN, g.ldb, DUAL);
   const int Kb = (g.K * ES + 15) & ~15;  // k-contiguous: bytes of a row, in whole chunks
   const unsigned char *PA, *PB;
   int64_t endA, endB;
@@ -291,19 +245,28 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_kernel(ProductArgs g)
   };
   int lit = 0, lk = 0, lend = 0, ls = 0, lg = 0;  // item, stage, its end, buffer, scale group of the next load
   Item li;
+  // STORE2: B from the stage `lk` on
+  auto begin_two = [&]() {
+    const bool in2 = lk >= g.kswitch;
+    const int64_t kb = (int64_t)(lk - (in2 ? g.kswitch : 0)) * SK * g.ldb * ES;
+    const int rb = li.tn * TN;
+    PB = reinterpret_cast<const unsigned char*>(in2 ? g.B2 : g.B) + kb + (int64_t)rb * ES;
+    endB = (g.kpart - 1) * g.ldb * ES + (((g.N - rb) * ES + 15) & ~15) - kb;
+  };
   auto begin_loads = [&]() {
     li = item_at(lp);
     lk = li.k0;
     ahead = 0;
     lend = li.k0 + li.stages;
-    const int ra = li.tm * TM, rb = li.tn * TN;
+    const int ra = li.tm * TM, rb = li.tn * TNO;
     const int64_t ka = AS ? (int64_t)lk * SK * g.lda * ES : (int64_t)lk * 128, kb = BS ? (int64_t)lk * SK * g.ldb * ES : (int64_t)lk * 128;
     PA = reinterpret_cast<const unsigned char*>(g.A) + li.batch * g.strideA * ES + ka + (AS ? (int64_t)ra * ES : ra * g.lda * ES);
-    PB = reinterpret_cast<const unsigned char*>(g.B) + li.batch * g.strideB * ES + kb + (BS ? (int64_t)rb * ES : rb * g.ldb * ES);
+    PB = reinterpret_cast<const unsigned char*>(second ? g.B2 : g.B) + li.batch * g.strideB * ES + kb + (BS ? (int64_t)rb * ES : rb * g.ldb * ES);
     // strided: the last k-row's columns, in whole chunks (rows start on 16
     // bytes); columns past the tile's read what follows, and nothing past that
     endA = AS ? (g.K - 1) * g.lda * ES + (((g.M - ra) * ES + 15) & ~15) - ka : (g.M - 1 - ra) * g.lda * ES + Kb - ka;
     endB = BS ? (g.K - 1) * g.ldb * ES + (((g.N - rb) * ES + 15) & ~15) - kb : (g.N - 1 - rb) * g.ldb * ES + Kb - kb;
+    if constexpr (TWO) begin_two();
     if constexpr (EPI == Epi::SOFTMAX) {
       // the low halves of the rows' targets (a column fits; what else matches
       // one there, the row pass does not read), ahead of the item's first
@@ -369,6 +332,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_kernel(ProductArgs g)
         ahead = 0;
         lend = -1;
       }
+    } else if (TWO && lk == g.kswitch) {
+      begin_two();
     }
   };
 
@@ -582,7 +547,13 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_kernel(ProductArgs g)
     int el32 = l32, ehalf = half;
     asm volatile("" : "+v"(el32), "+v"(ehalf));  // addresses made here, not kept through the loop
     const int m0 = cur.tm * TM + wm * FM * 32, n0 = cur.tn * TN + wn * FN * 32;
-    if constexpr (EPI == Epi::STORE) {
+    if constexpr (EPI == Epi::LINEAR) {
+      linear_epilogue<FM, FN>(g, acc, m0, n0, el32, ehalf);
+    } else if constexpr (EPI == Epi::GATED) {
+      gated_epilogue<FM>(g, acc, m0, n0 / 2, el32, ehalf, cur.split);
+    } else if constexpr (EPI == Epi::GATED_GRAD) {
+      gated_grad_epilogue<FM, FN, ES>(g, acc, m0, n0, el32, ehalf);
+    } else if constexpr (EPI == Epi::STORE || EPI == Epi::STORE2) {
       const int64_t base = cur.batch * g.strideC + cur.split * g.split_stride;
       const float alpha = g.alpha * (g.alpha_dev ? *g.alpha_dev : 1.f);
       if (alpha != 1.f) {

@@ -107,7 +107,8 @@ hipError_t launch_tiles(ProductArgs g, int64_t batch, hipStream_t st) {
   }
   HIP_TRY_ERR(cu_count(&cus));
   g.mt = (g.M + TM - 1) / TM;
-  g.nt = (g.N + TN - 1) / TN;
+  constexpr int TNO = EPI == Epi::GATED ? TN / 2 : TN;
+  g.nt = (g.N + TNO - 1) / TNO;
   g.items = batch * g.splits * (int64_t)g.mt * g.nt;
   const int64_t grid = std::min<int64_t>(up(g.items, 8), std::max(8, cus * PER_CU / 8 * 8));
   hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(64 * WM * WN), LDS, st, g);
@@ -117,7 +118,7 @@ hipError_t launch_tiles(ProductArgs g, int64_t batch, hipStream_t st) {
 template <Elem E, bool AS, bool BS, Epi EPI, int FA = 0, int FB = 0>
 hipError_t launch_product(const ProductArgs& g, bool large, int64_t batch, hipStream_t st) {
   if (large) return launch_tiles<E, 2, 4, 4, 2, 2, 1, AS, BS, EPI, FA, FB>(g, batch, st);
-  const int64_t items = batch * g.splits * ((g.M + 127) / 128) * ((g.N + 127) / 128);
+  const int64_t items = batch * g.splits * ((g.M + 127) / 128) * (EPI == Epi::GATED ? (g.N + 63) / 64 : (g.N + 127) / 128);
   if (items <= CUS) return launch_tiles<E, 1, 4, 4, 1, 4, 1, AS, BS, EPI, FA, FB>(g, batch, st);
   return launch_tiles<E, 1, 4, 4, 1, 2, 2, AS, BS, EPI, FA, FB>(g, batch, st);
 }
