@@ -28,6 +28,25 @@ namespace shampoo {
 
 constexpr int KEEP_BLOCK = 32;  // columns of a kept block
 
+template <int ES> struct KeptType;
+template <> struct KeptType<2> { typedef uint16_t type; };
+template <> struct KeptType<4> { typedef float type; };
+
+// f(0), f(1), ... f(N - 1) with constants: the blocks' loop bodies are too large
+// for the compiler to unroll them, and a block indexed at run time would put the
+// tile's results into scratch memory.
+template <int I> struct Index { static constexpr int value = I; };
+template <int N, int I = 0, typename F> __device__ __forceinline__ void for_each(F f) {
+  if constexpr (I < N) {
+    f(Index<I>{});
+    for_each<N, I + 1>(f);
+  }
+}
+
+// Nothing in memory moves over it: the loads of several blocks at a time would
+// not fit the registers beside a tile's results.
+__device__ __forceinline__ void apart() { asm volatile("" ::: "memory"); }
+
 // A 32 x 32 block from column nb on, of a row: `row` is where the lane's row
 // starts, `ok` whether it is one, `cols` where the rows end.  vec: rows start
 // on 16 bytes.
@@ -77,9 +96,11 @@ __device__ __forceinline__ floatx16 load_block(const uint16_t* row, bool ok, int
   return r;
 }
 
+// FULL: the whole block lies within rows that start on 16 bytes.
+template <bool FULL = false>
 __device__ __forceinline__ void store_block(float* row, bool ok, int nb, int half, int cols, int vec, const floatx16& x) {
   if (!ok) return;
-  if (vec && nb + 32 <= cols) {
+  if (FULL || (vec && nb + 32 <= cols)) {
 #pragma unroll
     for (int q = 0; q < 4; ++q)
       *reinterpret_cast<floatx4*>(row + nb + 8 * q + 4 * half) = floatx4{x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]};
@@ -91,11 +112,12 @@ __device__ __forceinline__ void store_block(float* row, bool ok, int nb, int hal
     }
   }
 }
+template <bool FULL = false>
 __device__ __forceinline__ void store_block(uint16_t* row, bool ok, int nb, int half, int cols, int vec, const floatx16& x) {
   uint32_t two[8];
 #pragma unroll
   for (int v = 0; v < 8; ++v) two[v] = pack_bf16(x[2 * v], x[2 * v + 1]);
-  if (vec && nb + 32 <= cols) {
+  if (FULL || (vec && nb + 32 <= cols)) {
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
       const auto a = __builtin_amdgcn_permlane32_swap(two[4 * q], two[4 * q + 2], false, false);
@@ -160,83 +182,140 @@ __device__ __forceinline__ void keep_f8(uint8_t* q, uint8_t* s, int64_t ld, int 
     if (half == 0) s[m * (ld / KEEP_BLOCK) + nb / KEEP_BLOCK] = (uint8_t)byte;
   }
 }
-__device__ __forceinline__ floatx16 kept_f8(const uint8_t* q, const uint8_t* s, int64_t ld, int m, bool ok, int nb, int half, int cols) {
-  u32x4 w = u32x4{0, 0, 0, 0};
-  uint32_t byte = 127;
-  if (ok && nb < cols) {
-    w = *reinterpret_cast<const u32x4*>(q + m * ld + nb + 16 * half);
-    byte = s[m * (ld / KEEP_BLOCK) + nb / KEEP_BLOCK];
-  }
-  const float scale = scale_value(byte);
-  const auto a = __builtin_amdgcn_permlane32_swap(w[0], w[1], false, false);
-  const auto b = __builtin_amdgcn_permlane32_swap(w[2], w[3], false, false);
-  const uint32_t four[4] = {a[0], b[0], a[1], b[1]};
-  floatx16 r;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const floatx2 lo = __builtin_amdgcn_cvt_pk_f32_fp8(four[i], false), hi = __builtin_amdgcn_cvt_pk_f32_fp8(four[i], true);
-    r[4 * i] = lo[0] * scale;
-    r[4 * i + 1] = lo[1] * scale;
-    r[4 * i + 2] = hi[0] * scale;
-    r[4 * i + 3] = hi[1] * scale;
-  }
-  return r;
-}
-
 __device__ __forceinline__ void keep_block(const FfnArgs& e, int which, int m, bool ok, int nb, int half, int cols, const floatx16& x) {
   if (e.keep_dt == 4) keep_f8((uint8_t*)e.keep[which], e.keep_scale[which], e.ld_keep, m, ok, nb, half, cols, x);
   else store_rows(e.keep[which], e.keep_dt, e.ld_keep, m, ok, nb, half, cols, e.keep_vec, x);
 }
-__device__ __forceinline__ floatx16 kept_block(const FfnArgs& e, int which, int m, bool ok, int nb, int half, int cols) {
-  if (e.keep_dt == 4) return kept_f8((const uint8_t*)e.keep[which], e.keep_scale[which], e.ld_keep, m, ok, nb, half, cols);
-  return load_rows(e.keep[which], e.keep_dt, e.ld_keep, m, ok, nb, half, cols, e.keep_vec);
+// Half a block (values 8 q to 8 q + 7 of the lane, columns 16 q to 16 q + 15 of the
+// block): what an epilogue holds beside a tile's results and the next tile's
+// first fragments.
+struct Half {
+  float v[8];
+};
+__device__ __forceinline__ Half load_half(const float* row, bool ok, int n0, int half, int cols, int vec) {
+  Half r;
+  if (vec && n0 + 16 <= cols) {
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const floatx4 w = ok ? *reinterpret_cast<const floatx4*>(row + n0 + 8 * q + 4 * half) : floatx4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) r.v[4 * q + e] = w[e];
+    }
+  } else {
+#pragma unroll
+    for (int v = 0; v < 8; ++v) {
+      const int n = n0 + 8 * (v >> 2) + 4 * half + (v & 3);
+      r.v[v] = ok && n < cols ? row[n] : 0.f;
+    }
+  }
+  return r;
 }
+__device__ __forceinline__ Half load_half(const uint16_t* row, bool ok, int n0, int half, int cols, int vec) {
+  Half r;
+  if (vec && n0 + 16 <= cols) {
+    const u32x4 w = ok ? *reinterpret_cast<const u32x4*>(row + n0 + 8 * half) : u32x4{0, 0, 0, 0};
+    const auto a = __builtin_amdgcn_permlane32_swap(w[0], w[2], false, false);
+    const auto b = __builtin_amdgcn_permlane32_swap(w[1], w[3], false, false);
+    const uint32_t two[4] = {a[0], b[0], a[1], b[1]};
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      r.v[2 * v] = bits_float(two[v] << 16);
+      r.v[2 * v + 1] = bits_float(two[v] & 0xffff0000u);
+    }
+  } else {
+#pragma unroll
+    for (int v = 0; v < 8; ++v) {
+      const int n = n0 + 8 * (v >> 2) + 4 * half + (v & 3);
+      r.v[v] = ok && n < cols ? bits_float((uint32_t)row[n] << 16) : 0.f;
+    }
+  }
+  return r;
+}
+// wholly within rows that start on 16 bytes
+__device__ __forceinline__ void store_half(float* row, bool ok, int n0, int half, const Half& x) {
+  if (!ok) return;
+#pragma unroll
+  for (int q = 0; q < 2; ++q)
+    *reinterpret_cast<floatx4*>(row + n0 + 8 * q + 4 * half) = floatx4{x.v[4 * q], x.v[4 * q + 1], x.v[4 * q + 2], x.v[4 * q + 3]};
+}
+__device__ __forceinline__ void store_half(uint16_t* row, bool ok, int n0, int half, const Half& x) {
+  const auto a = __builtin_amdgcn_permlane32_swap(pack_bf16(x.v[0], x.v[1]), pack_bf16(x.v[4], x.v[5]), false, false);
+  const auto b = __builtin_amdgcn_permlane32_swap(pack_bf16(x.v[2], x.v[3]), pack_bf16(x.v[6], x.v[7]), false, false);
+  if (ok) *reinterpret_cast<u32x4*>(row + n0 + 8 * half) = u32x4{a[0], b[0], a[1], b[1]};
+}
+
+// A kept block in 8 bits, as it lies in memory, and its values 8 q to 8 q + 7.
+struct KeptF8 {
+  u32x4 w;
+  uint32_t byte;
+  __device__ __forceinline__ void load(const FfnArgs& e, int which, int m, bool ok, int nb, int half, int cols) {
+    w = u32x4{0, 0, 0, 0};
+    byte = 127;
+    if (ok && nb < cols) {
+      w = *reinterpret_cast<const u32x4*>((const uint8_t*)e.keep[which] + m * e.ld_keep + nb + 16 * half);
+      byte = e.keep_scale[which][m * (e.ld_keep / KEEP_BLOCK) + nb / KEEP_BLOCK];
+    }
+  }
+  __device__ __forceinline__ void swap() {
+    const auto a = __builtin_amdgcn_permlane32_swap(w[0], w[1], false, false);
+    const auto b = __builtin_amdgcn_permlane32_swap(w[2], w[3], false, false);
+    w = u32x4{a[0], b[0], a[1], b[1]};
+  }
+  __device__ __forceinline__ Half values(int q) const {
+    const float scale = scale_value(byte);
+    Half r;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t four = i == 0 ? (q == 0 ? w[0] : w[2]) : (q == 0 ? w[1] : w[3]);
+      const floatx2 lo = __builtin_amdgcn_cvt_pk_f32_fp8(four, false), hi = __builtin_amdgcn_cvt_pk_f32_fp8(four, true);
+      r.v[4 * i] = lo[0] * scale;
+      r.v[4 * i + 1] = lo[1] * scale;
+      r.v[4 * i + 2] = hi[0] * scale;
+      r.v[4 * i + 3] = hi[1] * scale;
+    }
+    return r;
+  }
+};
 
 template <int FM, int FN>
 __device__ __forceinline__ void linear_epilogue(const ProductArgs& g, floatx16 (&acc)[FM][FN], int m0, int n0, int l32, int half) {
   const FfnArgs& e = g.ffn;
-  if (e.bias) {
-#pragma unroll
-    for (int j = 0; j < FN; ++j)
+  for_each<FN>([&](auto J) __attribute__((always_inline)) {
+    const int nb = n0 + 32 * J.value;
+    if (nb >= g.N) return;
+    apart();
+    floatx16 b;
+    if (e.bias) {
 #pragma unroll
       for (int v = 0; v < 16; ++v) {
-        const int n = min(n0 + 32 * j + 8 * (v >> 2) + 4 * half + (v & 3), g.N - 1);
-        const float b = e.bias_bf16 ? bits_float((uint32_t)reinterpret_cast<const uint16_t*>(e.bias)[n] << 16) : reinterpret_cast<const float*>(e.bias)[n];
-#pragma unroll
-        for (int i = 0; i < FM; ++i) acc[i][j][v] += b;
+        const int n = min(nb + 8 * (v >> 2) + 4 * half + (v & 3), g.N - 1);
+        b[v] = e.bias_bf16 ? bits_float((uint32_t)reinterpret_cast<const uint16_t*>(e.bias)[n] << 16) : reinterpret_cast<const float*>(e.bias)[n];
       }
-  }
-  if (e.keep[0]) {
-#pragma unroll
-    for (int i = 0; i < FM; ++i)
-#pragma unroll
-      for (int j = 0; j < FN; ++j) keep_block(e, 0, m0 + 32 * i + l32, m0 + 32 * i + l32 < g.M, n0 + 32 * j, half, g.N, acc[i][j]);
-  }
-  if (e.act) {
-    with_activation(e.act, [&](auto act) {
-#pragma unroll
-      for (int i = 0; i < FM; ++i)
-#pragma unroll
-        for (int j = 0; j < FN; ++j)
-#pragma unroll
-          for (int v = 0; v < 16; ++v) acc[i][j][v] = act.value(acc[i][j][v]);
-    });
-  }
-#pragma unroll
-  for (int i = 0; i < FM; ++i) {
-    const int m = m0 + 32 * i + l32;
-#pragma unroll
-    for (int j = 0; j < FN; ++j) {
-      const int nb = n0 + 32 * j;
-      if (nb >= g.N) continue;
-      if (e.residual) {
-        const floatx16 r = load_rows(e.residual, g.c_dt, e.ld_residual, m, m < g.M, nb, half, g.N, e.residual_vec);
-#pragma unroll
-        for (int v = 0; v < 16; ++v) acc[i][j][v] += r[v];
-      }
-      store_rows(g.C, g.c_dt, g.ldc, m, m < g.M, nb, half, g.N, g.vec, acc[i][j]);
     }
-  }
+    for_each<FM>([&](auto I) __attribute__((always_inline)) {
+      const int m = m0 + 32 * I.value + l32;
+      const bool ok = m < g.M;
+      apart();
+      floatx16 z = acc[I.value][J.value];
+      if (e.bias) {
+#pragma unroll
+        for (int v = 0; v < 16; ++v) z[v] += b[v];
+      }
+      if (e.keep[0]) keep_block(e, 0, m, ok, nb, half, g.N, z);
+      if (e.act) {
+        with_activation(e.act, [&](auto act) __attribute__((always_inline)) {
+#pragma unroll
+          for (int v = 0; v < 16; ++v) z[v] = act.value(z[v]);
+        });
+      }
+      if (e.residual) {
+        const floatx16 r = load_rows(e.residual, g.c_dt, e.ld_residual, m, ok, nb, half, g.N, e.residual_vec);
+#pragma unroll
+        for (int v = 0; v < 16; ++v) z[v] += r[v];
+      }
+      store_rows(g.C, g.c_dt, g.ldc, m, ok, nb, half, g.N, g.vec, z);
+    });
+  });
 }
 
 // C receives h: rows of ldc, zeros behind the columns
@@ -255,33 +334,31 @@ __device__ __forceinline__ void gated_epilogue(const ProductArgs& g, floatx16 (&
     }
     return;
   }
-  if (e.keep[0]) {
-#pragma unroll
-    for (int i = 0; i < FM; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        keep_block(e, j >> 1, m0 + 32 * i + l32, m0 + 32 * i + l32 < g.M, n0 + 32 * (j & 1), half, g.N, acc[i][j]);
-  }
-  with_activation(e.act, [&](auto act) {
-#pragma unroll
-    for (int i = 0; i < FM; ++i)
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int v = 0; v < 16; ++v) acc[i][j][v] = act.value(acc[i][j][v]) * acc[i][j + 2][v];
-  });
 #pragma unroll
   for (int i = 0; i < FM; ++i) {
     const int m = m0 + 32 * i + l32;
+    const bool ok = m < g.M;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const int nb = n0 + 32 * j;
+      if (nb >= g.ldc) break;
+      floatx16 h = acc[i][j];
+      const floatx16 up = acc[i][j + 2];
+      if (e.keep[0]) {
+        keep_block(e, 0, m, ok, nb, half, g.N, h);
+        keep_block(e, 1, m, ok, nb, half, g.N, up);
+      }
+      with_activation(e.act, [&](auto act) __attribute__((always_inline)) {
+#pragma unroll
+        for (int v = 0; v < 16; ++v) h[v] = act.value(h[v]) * up[v];
+      });
       if (nb + 32 > g.N) {
 #pragma unroll
         for (int v = 0; v < 16; ++v)
-          if (nb + 8 * (v >> 2) + 4 * half + (v & 3) >= g.N) acc[i][j][v] = 0.f;
+          if (nb + 8 * (v >> 2) + 4 * half + (v & 3) >= g.N) h[v] = 0.f;
       }
-      store_rows(g.C, g.c_dt, g.ldc, m, m < g.M, nb, half, (int)g.ldc, g.vec, acc[i][j]);
+      if (g.c_dt == 0) store_block<true>(reinterpret_cast<float*>(g.C) + m * g.ldc, ok, nb, half, 0, 1, h);
+      else store_block<true>(reinterpret_cast<uint16_t*>(g.C) + m * g.ldc, ok, nb, half, 0, 1, h);
     }
   }
 }
@@ -289,39 +366,56 @@ __device__ __forceinline__ void gated_epilogue(const ProductArgs& g, floatx16 (&
 // ES: bytes of an element of dg, du (rows of ldc) and h (rows of ldc / 2), zeros behind the columns
 template <int FM, int FN, int ES>
 __device__ __forceinline__ void gated_grad_epilogue(const ProductArgs& g, floatx16 (&acc)[FM][FN], int m0, int n0, int l32, int half) {
+  using T = typename KeptType<ES>::type;
   const FfnArgs& e = g.ffn;
-  constexpr int DT = ES == 4 ? 0 : 2;
   const int wide = (int)(g.ldc / 2);
-#pragma unroll
-  for (int i = 0; i < FM; ++i) {
-    const int m = m0 + 32 * i + l32;
+  for_each<FM * FN>([&](auto K) __attribute__((always_inline)) {
+    constexpr int I = K.value / FN, J = K.value % FN;
+    const int m = m0 + 32 * I + l32, nb = n0 + 32 * J;
     const bool ok = m < g.M;
+    if (nb >= wide) return;
+    const bool f8 = e.keep_dt == 4;
+    apart();
+    KeptF8 gate8, up8;
+    if (f8) {
+      gate8.load(e, 0, m, ok, nb, half, g.N);
+      up8.load(e, 1, m, ok, nb, half, g.N);
+      gate8.swap();
+      up8.swap();
+    }
+    for_each<2>([&](auto Q) __attribute__((always_inline)) {
+      constexpr int q = Q.value;
+      const int n = nb + 16 * q;
+      apart();
+      Half gate, up, h;
+      if (f8) {
+        gate = gate8.values(q);
+        up = up8.values(q);
+      } else {
+        gate = load_half(reinterpret_cast<const T*>(e.keep[0]) + m * e.ld_keep, ok, n, half, g.N, e.keep_vec);
+        up = load_half(reinterpret_cast<const T*>(e.keep[1]) + m * e.ld_keep, ok, n, half, g.N, e.keep_vec);
+      }
+      // gate becomes dg, up du
+      with_activation(e.act, [&](auto act) __attribute__((always_inline)) {
 #pragma unroll
-    for (int j = 0; j < FN; ++j) {
-      const int nb = n0 + 32 * j;
-      if (nb >= wide) continue;
-      floatx16 gate = kept_block(e, 0, m, ok, nb, half, g.N), up = kept_block(e, 1, m, ok, nb, half, g.N);
-      floatx16 dg, h;
-      with_activation(e.act, [&](auto act) {
-#pragma unroll
-        for (int v = 0; v < 16; ++v) {
+        for (int v = 0; v < 8; ++v) {
           float slope;
-          const float a = act.both(gate[v], slope), dh = acc[i][j][v];
-          h[v] = a * up[v];
-          dg[v] = dh * up[v] * slope;
-          acc[i][j][v] = dh * a;
+          const float a = act.both(gate.v[v], slope), dh = acc[I][J][8 * q + v];
+          h.v[v] = a * up.v[v];
+          gate.v[v] = dh * up.v[v] * slope;
+          up.v[v] = dh * a;
         }
       });
-      if (nb + 32 > g.N) {
+      if (n + 16 > g.N) {
 #pragma unroll
-        for (int v = 0; v < 16; ++v)
-          if (nb + 8 * (v >> 2) + 4 * half + (v & 3) >= g.N) h[v] = dg[v] = acc[i][j][v] = 0.f;
+        for (int v = 0; v < 8; ++v)
+          if (n + 8 * (v >> 2) + 4 * half + (v & 3) >= g.N) h.v[v] = gate.v[v] = up.v[v] = 0.f;
       }
-      store_rows(g.C, DT, g.ldc, m, ok, nb, half, wide, 1, dg);
-      store_rows(e.du, DT, g.ldc, m, ok, nb, half, wide, 1, acc[i][j]);
-      store_rows(e.h, DT, wide, m, ok, nb, half, wide, 1, h);
-    }
-  }
+      store_half(reinterpret_cast<T*>(g.C) + m * g.ldc, ok, n, half, gate);
+      store_half(reinterpret_cast<T*>(e.du) + m * g.ldc, ok, n, half, up);
+      store_half(reinterpret_cast<T*>(e.h) + m * (int64_t)wide, ok, n, half, h);
+    });
+  });
 }
 
 }  // namespace shampoo
