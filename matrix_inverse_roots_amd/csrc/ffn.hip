@@ -114,6 +114,52 @@ hipError_t place(const Operand& o, const void*& p, const void* scale, int64_t ro
   return hipGetLastError();
 }
 
+// Tile and ranges of k of a layer's product: the least of the tiles' costs.
+//
+// Costs in the time of one 256 x 256 tile (bfloat16) where the chip is full and
+// power holds its clock: 256 x 256 1, 256 x 128 0.54, two 128 x 128 on a unit 0.60
+// (8192 x 10240 x 4096: 533, 585 and 644 us; 4096^3: 115, 122 and 138), one alone
+// 0.33.  Where it is not, the clock rises and a tile is faster: 0.63, 0.40, 0.45,
+// so that a last round which few units take costs less than a full one (4096 x
+// 10240 x 8192, 2.5 rounds of large tiles, 5 of medium: 575 and 585 us; 8192 x
+// 1024 x 4096, half a round and one: 88 and 65).  The epilogue of a large tile
+// leaves the matrix cores waiting for longer: `epilogue` counts it in columns of
+// k (150 for bias, activation, residual or kept values, 300 for the gated block's
+// gradients; 8192 x 4096 x 1024 with gelu and kept values: 103 us large, 95
+// medium, 100 small; with k 4096 and 10240 columns 598, 665, 775).
+// float32 (matrix instructions, not loads, bound it): a 128 x 128 tile 0.26, a 64
+// x 64 one 0.073 (777 x 2731 x 1000, 154 tiles or 559: 76 and 60 us; 2048 x
+// 2048 x 1024, 256 or 1024: 72 and 79).
+Shape plan_layer(int64_t batch, int64_t M, int64_t N, int64_t K, int es, bool may_split, int epilogue, bool dual = false) {
+  Shape s = plan_shape(batch, M, N, K, es, may_split);
+  s.tile = s.large ? TILE_LARGE : TILE_128;
+  auto tiles = [&](int64_t m, int64_t n) { return batch * ((M + m - 1) / m) * ((N + n - 1) / n); };
+  if (es == 4) {
+    // ranges of k: some 6 us more, for the launch that sums them
+    const double now = s.large ? (double)((tiles(256, 256) + CUS - 1) / CUS)
+                               : (double)((tiles(128, 128) * s.splits + CUS - 1) / CUS) * 0.26 / s.splits + (s.splits > 1 ? 30.0 / K : 0.0);
+    if (!dual && (double)((tiles(64, 64) + CUS - 1) / CUS) * 0.073 < now) {
+      s.large = false;
+      s.tile = TILE_64;
+      s.splits = 1;
+      s.split_stages = s.nst;
+    }
+    return s;
+  }
+  if (s.splits > 1) return s;
+  auto cost = [&](int64_t n, int64_t slots, double full, double alone) {
+    return std::max((double)n / slots * full, (double)((n + slots - 1) / slots) * alone);
+  };
+  const double e = 1.0 + (double)epilogue / K;
+  const int64_t small = tiles(128, 128);
+  const double large = cost(tiles(256, 256), CUS, 1.0, 0.63) * e;
+  const double medium = cost(tiles(256, 128), CUS, 0.54, 0.40);
+  const double least = small <= CUS ? 0.33 : cost(small, 2 * CUS, 0.60, 0.45);
+  s.large = large <= medium && large <= least;
+  s.tile = s.large ? TILE_LARGE : medium <= least ? TILE_MEDIUM : TILE_128;
+  return s;
+}
+
 int kept_code(int dt) { return dt == SHAMPOO_E4M3 ? 4 : out_code(dt); }
 // A call of few rows takes no matrix cores, unless it keeps blocks of 8 bits,
 // which reach over its workgroups.
@@ -143,8 +189,8 @@ template <Elem E> hipError_t run_layer(const Layer& l, hipStream_t st) {
   g.ffn = l.ffn;
   const Out o{l.y, l.ldy, 0, out_code(l.y_dt), rows_vec(l.y, l.ldy, 0, l.y_dt), 0.f};
   point_output(g, l.shape, o, l.part, 1);
-  if (l.shape.splits == 1) return launch_product<E, false, false, Epi::LINEAR>(g, l.shape.large, 1, st);
-  HIP_TRY_ERR((launch_product<E, false, false, Epi::STORE>(g, l.shape.large, 1, st)));
+  if (l.shape.splits == 1) return launch_layer<E, false, false, Epi::LINEAR>(g, l.shape, 1, st);
+  HIP_TRY_ERR((launch_layer<E, false, false, Epi::STORE>(g, l.shape, 1, st)));
   FinishArgs f{l.part, g.split_stride, l.shape.splits, (int)l.M, (int)l.N, 0, l.y, l.ldy, out_code(l.y_dt), l.ffn};
   hipLaunchKernelGGL(ffn_finish_kernel<false>, dim3((unsigned)((up(l.N, 32) + 1023) / 1024), (unsigned)std::min<int64_t>(l.M, 65535)), dim3(256), 0,
                      st, f);
@@ -191,7 +237,7 @@ shampoo_status linear_layout(const shampoo_linear_args* a, LinearLayout* L) {
   if (!L->few) {
     L->x = operand(c, a->x, a->M, a->K, a->ld_x, a->dt, a->dt);
     L->w = operand(c, a->w, a->N, a->K, a->ld_w, a->w_dt, a->dt);
-    L->shape = plan_shape(1, a->M, a->N, a->K, (int)size_of(a->dt), true);
+    L->shape = plan_layer(1, a->M, a->N, a->K, (int)size_of(a->dt), true, a->bias || a->residual || a->keep || a->activation ? 150 : 0);
     L->part = c.take(partial_bytes(L->shape, 1, a->M, a->N));
   }
   L->total = c.at;
@@ -236,8 +282,8 @@ shampoo_status linear_grad_layout(const shampoo_linear_grad_args* a, LinearGradL
   L->ld_dz = L->store ? up(a->N, 8) : a->ld_dy;
   L->x = operand(c, a->x, a->M, a->K, a->ld_x, a->x_dt, a->dt, a->dw);
   L->w = operand(c, a->w, a->N, a->K, a->ld_w, a->w_dt, a->dt, a->dx);
-  L->dx = plan_shape(1, a->M, a->K, a->N, es, true);
-  L->dw = plan_shape(1, a->N, a->K, a->M, es, true);
+  L->dx = plan_layer(1, a->M, a->K, a->N, es, true, 0);
+  L->dw = plan_layer(1, a->N, a->K, a->M, es, true, 0);
   L->dz = c.take(L->store ? (size_t)a->M * L->ld_dz * es : 0);
   L->sums = c.take(a->dbias ? (size_t)((a->M + GRAD_ROWS - 1) / GRAD_ROWS) * a->N * 4 : 0);
   size_t part = 0;
@@ -254,7 +300,7 @@ template <Elem E, bool AS, bool BS, Epi EPI = Epi::STORE>
 hipError_t run_product(ProductArgs& g, const Shape& s, const Out& o, float* part, int64_t batch, hipStream_t st) {
   set_shape(g, s);
   point_output(g, s, o, part, batch);
-  HIP_TRY_ERR((launch_product<E, AS, BS, EPI>(g, s.large, batch, st)));
+  HIP_TRY_ERR((launch_layer<E, AS, BS, EPI>(g, s, batch, st)));
   return finish_split(g, s, o, part, batch, st);
 }
 // zeros, or the unchanged accumulated gradient, of an empty batch
@@ -356,8 +402,8 @@ shampoo_status gated_layout(const shampoo_gated_ffn_args* a, GatedLayout* L) {
   gated_operands(c, L->gate, L->up_, a->w_gate, a->w_up, a->f, a->d, a->ld_gate, a->ld_up, a->w_dt, a->dt);
   L->down = operand(c, a->w_down, a->d, a->f, a->ld_down, a->w_dt, a->dt);
   L->ldh = up(a->f, 64);
-  L->in = plan_shape(1, a->T, 2 * a->f, a->d, es, true);
-  L->out = plan_shape(1, a->T, a->d, a->f, es, true);
+  L->in = plan_layer(1, a->T, 2 * a->f, a->d, es, true, 0, true);
+  L->out = plan_layer(1, a->T, a->d, a->f, es, true, a->residual ? 150 : 0);
   L->h = c.take((size_t)a->T * L->ldh * es);
   L->part = c.take(std::max(partial_bytes(L->in, 1, a->T, 2 * a->f), partial_bytes(L->out, 1, a->T, a->d)));
   L->total = c.at;
@@ -396,7 +442,7 @@ template <Elem E> hipError_t run_gated(const shampoo_gated_ffn_args* a, const Ga
   g.vec = 1;
   g.ffn = gated_kept(a->keep_gate, a->keep_gate_scale, a->keep_up, a->keep_up_scale, a->ld_keep, a->keep_dt, a->f, a->activation);
   g.ffn.part = part;
-  HIP_TRY_ERR((launch_product<E, false, false, Epi::GATED>(g, L.in.large, 1, st)));
+  HIP_TRY_ERR((launch_layer<E, false, false, Epi::GATED>(g, L.in, 1, st)));
   if (L.in.splits > 1) {
     const FinishArgs f{part, 2 * a->T * a->f, L.in.splits, (int)a->T, (int)a->f, (int)L.ldh, g.C, L.ldh, g.c_dt, g.ffn};
     hipLaunchKernelGGL(ffn_finish_kernel<true>, dim3((unsigned)((L.ldh + 1023) / 1024), (unsigned)std::min<int64_t>(a->T, 65535)), dim3(256), 0, st, f);
@@ -464,10 +510,10 @@ shampoo_status gated_grad_layout(const shampoo_gated_ffn_grad_args* a, GatedGrad
   L->down = operand(c, a->w_down, a->d, a->f, a->ld_down, a->w_dt, a->dt);
   L->fp = up(a->f, 64);
   L->pair = a->dw_gate && a->dw_up && a->ld_dw_gate == a->ld_dw_up;
-  L->dh = plan_shape(1, a->T, L->fp, a->d, es, false);
-  L->dx = plan_shape(1, a->T, a->d, 2 * L->fp, es, true);
-  L->dwd = plan_shape(1, a->d, a->f, a->T, es, true);
-  L->dwp = plan_shape(L->pair ? 2 : 1, a->f, a->d, a->T, es, true);
+  L->dh = plan_layer(1, a->T, L->fp, a->d, es, false, 300);
+  L->dx = plan_layer(1, a->T, a->d, 2 * L->fp, es, true, 0);
+  L->dwd = plan_layer(1, a->d, a->f, a->T, es, true, 0);
+  L->dwp = plan_layer(L->pair ? 2 : 1, a->f, a->d, a->T, es, true, 0);
   L->D = c.take((size_t)a->T * 2 * L->fp * es);
   L->h = c.take((size_t)a->T * L->fp * es);
   size_t part = 0;
@@ -504,7 +550,7 @@ template <Elem E> hipError_t run_gated_grad(const shampoo_gated_ffn_grad_args* a
                        const_cast<void*>(a->kept_up_scale), a->ld_kept, a->kept_dt, a->f, a->activation);
     g.ffn.du = du;
     g.ffn.h = h;
-    HIP_TRY_ERR((launch_product<E, false, true, Epi::GATED_GRAD>(g, L.dh.large, 1, st)));
+    HIP_TRY_ERR((launch_layer<E, false, true, Epi::GATED_GRAD>(g, L.dh, 1, st)));
   }
   if (a->dx) {
     HIP_TRY_ERR(place(L.gate, wg, nullptr, a->f, a->d, a->ld_gate, a->w_dt, a->dt, ws, st));
@@ -638,6 +684,7 @@ shampoo_status shampoo_linear(const shampoo_linear_args* a, hipStream_t stream) 
   FfnArgs e{};
   e.bias = a->bias;
   e.bias_bf16 = a->bias_dt == SHAMPOO_BF16;
+  e.bias_vec = aligned(a->bias, 16);
   e.residual = a->residual;
   e.ld_residual = a->ld_residual;
   e.residual_vec = rows16(a->residual, a->ld_residual, a->y_dt);

@@ -277,24 +277,78 @@ struct KeptF8 {
   }
 };
 
+// Loads that a block's epilogue will need, issued a block ahead: bfloat16 rows
+// that start on 16 bytes, wholly inside.
+struct Ahead {
+  u32x4 w[2];
+  __device__ __forceinline__ void load(const uint16_t* row, bool ok, int nb, int half) {
+#pragma unroll
+    for (int q = 0; q < 2; ++q) w[q] = ok ? *reinterpret_cast<const u32x4*>(row + nb + 16 * q + 8 * half) : u32x4{0, 0, 0, 0};
+  }
+  __device__ __forceinline__ Half values(int q) const {
+    const auto a = __builtin_amdgcn_permlane32_swap(w[q][0], w[q][2], false, false);
+    const auto b = __builtin_amdgcn_permlane32_swap(w[q][1], w[q][3], false, false);
+    const uint32_t two[4] = {a[0], b[0], a[1], b[1]};
+    Half r;
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      r.v[2 * v] = bits_float(two[v] << 16);
+      r.v[2 * v + 1] = bits_float(two[v] & 0xffff0000u);
+    }
+    return r;
+  }
+};
+
+__device__ __forceinline__ floatx16 bias_block(const FfnArgs& e, int nb, int half, int cols) {
+  floatx16 b;
+  if (nb + 32 <= cols && e.bias_vec) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int n = nb + 8 * q + 4 * half;
+      if (e.bias_bf16) {
+        const u32x2 w = *reinterpret_cast<const u32x2*>(reinterpret_cast<const uint16_t*>(e.bias) + n);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) b[4 * q + c] = bits_float(c & 1 ? w[c >> 1] & 0xffff0000u : w[c >> 1] << 16);
+      } else {
+        const floatx4 w = *reinterpret_cast<const floatx4*>(reinterpret_cast<const float*>(e.bias) + n);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) b[4 * q + c] = w[c];
+      }
+    }
+  } else {
+#pragma unroll
+    for (int v = 0; v < 16; ++v) {
+      const int n = min(nb + 8 * (v >> 2) + 4 * half + (v & 3), cols - 1);
+      b[v] = e.bias_bf16 ? bits_float((uint32_t)reinterpret_cast<const uint16_t*>(e.bias)[n] << 16) : reinterpret_cast<const float*>(e.bias)[n];
+    }
+  }
+  return b;
+}
+
 template <int FM, int FN>
 __device__ __forceinline__ void linear_epilogue(const ProductArgs& g, floatx16 (&acc)[FM][FN], int m0, int n0, int l32, int half) {
   const FfnArgs& e = g.ffn;
+  const bool early = e.residual && e.residual_vec && g.c_dt == 2 && n0 + 32 * FN <= g.N;
+  const auto residual_row = [&](int i) __attribute__((always_inline)) {
+    return reinterpret_cast<const uint16_t*>(e.residual) + (m0 + 32 * i + l32) * e.ld_residual;
+  };
+  Ahead next;
+  if (early) next.load(residual_row(0), m0 + l32 < g.M, n0, half);
   for_each<FN>([&](auto J) __attribute__((always_inline)) {
     const int nb = n0 + 32 * J.value;
     if (nb >= g.N) return;
     apart();
     floatx16 b;
-    if (e.bias) {
-#pragma unroll
-      for (int v = 0; v < 16; ++v) {
-        const int n = min(nb + 8 * (v >> 2) + 4 * half + (v & 3), g.N - 1);
-        b[v] = e.bias_bf16 ? bits_float((uint32_t)reinterpret_cast<const uint16_t*>(e.bias)[n] << 16) : reinterpret_cast<const float*>(e.bias)[n];
-      }
-    }
+    if (e.bias) b = bias_block(e, nb, half, g.N);
     for_each<FM>([&](auto I) __attribute__((always_inline)) {
       const int m = m0 + 32 * I.value + l32;
       const bool ok = m < g.M;
+      apart();
+      const Ahead now = next;
+      if (early && !(I.value == FM - 1 && J.value == FN - 1)) {
+        constexpr int i = I.value == FM - 1 ? 0 : I.value + 1, j = I.value == FM - 1 ? J.value + 1 : J.value;
+        next.load(residual_row(i), m0 + 32 * i + l32 < g.M, n0 + 32 * j, half);
+      }
       apart();
       floatx16 z = acc[I.value][J.value];
       if (e.bias) {
@@ -308,7 +362,14 @@ __device__ __forceinline__ void linear_epilogue(const ProductArgs& g, floatx16 (
           for (int v = 0; v < 16; ++v) z[v] = act.value(z[v]);
         });
       }
-      if (e.residual) {
+      if (early) {
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const Half r = now.values(q);
+#pragma unroll
+          for (int v = 0; v < 8; ++v) z[8 * q + v] += r.v[v];
+        }
+      } else if (e.residual) {
         const floatx16 r = load_rows(e.residual, g.c_dt, e.ld_residual, m, ok, nb, half, g.N, e.residual_vec);
 #pragma unroll
         for (int v = 0; v < 16; ++v) z[v] += r[v];
@@ -318,49 +379,45 @@ __device__ __forceinline__ void linear_epilogue(const ProductArgs& g, floatx16 (
   });
 }
 
-// C receives h: rows of ldc, zeros behind the columns
-template <int FM>
-__device__ __forceinline__ void gated_epilogue(const ProductArgs& g, floatx16 (&acc)[FM][4], int m0, int n0, int l32, int half, int range) {
+// C receives h: rows of ldc, zeros behind the columns.  Blocks j and j + FN / 2
+// are the same columns of the gate and of the up projection.
+template <int FM, int FN>
+__device__ __forceinline__ void gated_epilogue(const ProductArgs& g, floatx16 (&acc)[FM][FN], int m0, int n0, int l32, int half, int range) {
+  constexpr int HF = FN / 2;
   const FfnArgs& e = g.ffn;
   if (g.splits > 1) {
     float* part = e.part + (int64_t)range * g.M * 2 * g.N;
-#pragma unroll
-    for (int i = 0; i < FM; ++i) {
-      const int m = m0 + 32 * i + l32;
-      float* row = part + m * (int64_t)(2 * g.N);
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        store_block(row + (j >> 1) * g.N, m < g.M, n0 + 32 * (j & 1), half, g.N, g.N % 4 == 0, acc[i][j]);
-    }
+    for_each<FM * FN>([&](auto K) __attribute__((always_inline)) {
+      constexpr int I = K.value / FN, J = K.value % FN;
+      const int m = m0 + 32 * I + l32;
+      store_block(part + m * (int64_t)(2 * g.N) + J / HF * g.N, m < g.M, n0 + 32 * (J % HF), half, g.N, g.N % 4 == 0, acc[I][J]);
+    });
     return;
   }
-#pragma unroll
-  for (int i = 0; i < FM; ++i) {
-    const int m = m0 + 32 * i + l32;
+  for_each<FM * HF>([&](auto K) __attribute__((always_inline)) {
+    constexpr int I = K.value / HF, J = K.value % HF;
+    const int m = m0 + 32 * I + l32, nb = n0 + 32 * J;
     const bool ok = m < g.M;
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int nb = n0 + 32 * j;
-      if (nb >= g.ldc) break;
-      floatx16 h = acc[i][j];
-      const floatx16 up = acc[i][j + 2];
-      if (e.keep[0]) {
-        keep_block(e, 0, m, ok, nb, half, g.N, h);
-        keep_block(e, 1, m, ok, nb, half, g.N, up);
-      }
-      with_activation(e.act, [&](auto act) __attribute__((always_inline)) {
-#pragma unroll
-        for (int v = 0; v < 16; ++v) h[v] = act.value(h[v]) * up[v];
-      });
-      if (nb + 32 > g.N) {
-#pragma unroll
-        for (int v = 0; v < 16; ++v)
-          if (nb + 8 * (v >> 2) + 4 * half + (v & 3) >= g.N) h[v] = 0.f;
-      }
-      if (g.c_dt == 0) store_block<true>(reinterpret_cast<float*>(g.C) + m * g.ldc, ok, nb, half, 0, 1, h);
-      else store_block<true>(reinterpret_cast<uint16_t*>(g.C) + m * g.ldc, ok, nb, half, 0, 1, h);
+    if (nb >= g.ldc) return;
+    apart();
+    floatx16 h = acc[I][J];
+    const floatx16 up = acc[I][J + HF];
+    if (e.keep[0]) {
+      keep_block(e, 0, m, ok, nb, half, g.N, h);
+      keep_block(e, 1, m, ok, nb, half, g.N, up);
     }
-  }
+    with_activation(e.act, [&](auto act) __attribute__((always_inline)) {
+#pragma unroll
+      for (int v = 0; v < 16; ++v) h[v] = act.value(h[v]) * up[v];
+    });
+    if (nb + 32 > g.N) {
+#pragma unroll
+      for (int v = 0; v < 16; ++v)
+        if (nb + 8 * (v >> 2) + 4 * half + (v & 3) >= g.N) h[v] = 0.f;
+    }
+    if (g.c_dt == 0) store_block<true>(reinterpret_cast<float*>(g.C) + m * g.ldc, ok, nb, half, 0, 1, h);
+    else store_block<true>(reinterpret_cast<uint16_t*>(g.C) + m * g.ldc, ok, nb, half, 0, 1, h);
+  });
 }
 
 // ES: bytes of an element of dg, du (rows of ldc) and h (rows of ldc / 2), zeros behind the columns
@@ -369,17 +426,30 @@ __device__ __forceinline__ void gated_grad_epilogue(const ProductArgs& g, floatx
   using T = typename KeptType<ES>::type;
   const FfnArgs& e = g.ffn;
   const int wide = (int)(g.ldc / 2);
+  const bool f8 = e.keep_dt == 4;
+  // what was kept of the next block is loaded before this one is computed
+  const bool early = ES == 2 && !f8 && e.keep_vec && n0 + 32 * FN <= g.N;
+  KeptF8 next8[2];
+  Ahead next[2];
+  const auto load = [&](int i, int j) __attribute__((always_inline)) {
+    const int m = m0 + 32 * i + l32, nb = n0 + 32 * j;
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      if (f8) next8[p].load(e, p, m, m < g.M, nb, half, g.N);
+      else if (early) next[p].load(reinterpret_cast<const uint16_t*>(e.keep[p]) + m * e.ld_keep, m < g.M, nb, half);
+    }
+  };
+  load(0, 0);
   for_each<FM * FN>([&](auto K) __attribute__((always_inline)) {
     constexpr int I = K.value / FN, J = K.value % FN;
     const int m = m0 + 32 * I + l32, nb = n0 + 32 * J;
     const bool ok = m < g.M;
-    if (nb >= wide) return;
-    const bool f8 = e.keep_dt == 4;
     apart();
-    KeptF8 gate8, up8;
+    KeptF8 gate8 = next8[0], up8 = next8[1];
+    const Ahead gate16 = next[0], up16 = next[1];
+    if constexpr (K.value + 1 < FM * FN) load((K.value + 1) / FN, (K.value + 1) % FN);
+    if (nb >= wide) return;
     if (f8) {
-      gate8.load(e, 0, m, ok, nb, half, g.N);
-      up8.load(e, 1, m, ok, nb, half, g.N);
       gate8.swap();
       up8.swap();
     }
@@ -391,6 +461,9 @@ __device__ __forceinline__ void gated_grad_epilogue(const ProductArgs& g, floatx
       if (f8) {
         gate = gate8.values(q);
         up = up8.values(q);
+      } else if (early) {
+        gate = gate16.values(q);
+        up = up16.values(q);
       } else {
         gate = load_half(reinterpret_cast<const T*>(e.keep[0]) + m * e.ld_keep, ok, n, half, g.N, e.keep_vec);
         up = load_half(reinterpret_cast<const T*>(e.keep[1]) + m * e.ld_keep, ok, n, half, g.N, e.keep_vec);

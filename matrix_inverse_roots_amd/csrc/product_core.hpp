@@ -137,17 +137,21 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_kernel(ProductArgs g)
   constexpr bool SCALED = E == Elem::F8 || E == Elem::F8W;
   constexpr bool DUAL = EPI == Epi::GATED, TWO = EPI == Epi::STORE2;
   constexpr int TNO = DUAL ? TN / 2 : TN;  // columns of a tile's results
+  constexpr int TURN = 16 * FN;            // DUAL: rows of B1 and B2 take turns
+  // registers of the next tile's first fragments are given to these epilogues,
+  // which read them again behind
+  constexpr bool AGAIN = EPI == Epi::LINEAR || EPI == Epi::GATED || EPI == Epi::GATED_GRAD;
   // LDS: NB buffers, then groups of scales (a group each for NB stages ahead at
   // most, and the current one), then as many groups of targets
   constexpr int NI = NIA + NIB, NG = scale_groups(NB), SCALES = NB * STAGE, SGROUP = 4 * (TM + TN);
   constexpr int TARGETS = SCALES + (SCALED ? NG * SGROUP : 0);
-  static_assert(NB == 2 || NB == 4, "buffers are counted with masks");
+  static_assert(NB >= 2 && NB <= 4, "groups of scales are counted with masks");
   static_assert(NIA * W * 8 == TM && NIB * W * 8 == TN, "loads divide among the waves");
   static_assert(!SCALED || (!AS && !BS), "8-bit operands are k-contiguous");
   static_assert(!SCALED || (TM + TN) % (64 * W) == 0, "each wave loads the scales of as many rows");
   static_assert(TM % 64 == 0 && TM <= 64 * W, "a wave loads the targets of 64 rows");
   static_assert(!(AS && TM < 64) && !(BS && TN < 64), "k-strided swizzles need 64 columns");
-  static_assert(!DUAL || (FN == 4 && !BS && NIB * 8 <= 64 && 64 % (NIB * 8) == 0), "a wave loads from one of the two matrices");
+  static_assert(!DUAL || (FN % 2 == 0 && !BS && TURN % (NIB * 8) == 0), "a wave loads from one of the two matrices");
   static_assert(!TWO || BS, "two matrices follow each other along strided k");
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
   typedef __attribute__((address_space(3))) unsigned char lds_u8;
@@ -213,9 +217,9 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_kernel(ProductArgs g)
   // of the operand's last row or k-row, past which a descriptor reads zeros.
   const int last = g.nst - 1, rest = g.K - last * SK;  // the last stage, and its k
   uint32_t offA[NIA], offB[NIB], tailA[NIA], tailB[NIB];
-  // DUAL: 64 rows of B1 and 64 of B2 in turn, so that a wave's first two
-  // fragments and its last two are the same columns of both
-  const bool second = DUAL && ((wave * NIB * 8) >> 6 & 1);
+  // DUAL: half a wave's rows of B1, then as many of B2, so that the first half
+  // of a wave's fragments and the second are the same columns of both
+  const bool second = DUAL && (wave * NIB * 8 / TURN & 1);
   auto offsets = [&](uint32_t* off, uint32_t* tail, int n, bool strided, int T, int64_t ld, bool dual) {
 #pragma unroll
     for (int q = 0; q < n; ++q) {
@@ -226,7 +230,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_kernel(ProductArgs g)
         tail[q] = k < rest ? off[q] : RSRC_OUTSIDE;
       } else {
         const int row = at >> 7, byte = 16 * ((lane & 7) ^ ((row >> 1) & 7));
-        off[q] = (uint32_t)((dual ? (row >> 7) * 64 + (row & 63) : row) * ld * ES) + byte;
+        off[q] = (uint32_t)((dual ? row / (2 * TURN) * TURN + row % TURN : row) * ld * ES) + byte;
         tail[q] = byte < rest * ES ? off[q] : RSRC_OUTSIDE;
       }
     }
@@ -318,7 +322,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_kernel(ProductArgs g)
     }
   };
   auto advance = [&]() {
-    ls = NB == 2 ? ls ^ 1 : (ls + 1) & (NB - 1);
+    ls = NB == 2 ? ls ^ 1 : NB == 4 ? (ls + 1) & 3 : ls == NB - 1 ? 0 : ls + 1;
     if (lend < 0) return;  // nothing left: the descriptors stay empty
     if (AS) PA += SK * g.lda * ES, endA -= SK * g.lda * ES;
     if (BS) PB += SK * g.ldb * ES, endB -= SK * g.ldb * ES;
@@ -526,7 +530,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_kernel(ProductArgs g)
       issue_scales();
       const bool last = s + 1 == cur.stages;
       if (last || (s & 3) == 3) rg = (rg + 1) & (NG - 1);
-      const int next = NB == 2 ? rb ^ 1 : (rb + 1) & (NB - 1);
+      const int next = NB == 2 ? rb ^ 1 : NB == 4 ? (rb + 1) & 3 : rb == NB - 1 ? 0 : rb + 1;
       issue();
       read_frags(next, 0);
       read_scales(rg, last ? 0 : s + 1, sc[1]);
@@ -550,7 +554,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_kernel(ProductArgs g)
     if constexpr (EPI == Epi::LINEAR) {
       linear_epilogue<FM, FN>(g, acc, m0, n0, el32, ehalf);
     } else if constexpr (EPI == Epi::GATED) {
-      gated_epilogue<FM>(g, acc, m0, n0 / 2, el32, ehalf, cur.split);
+      gated_epilogue<FM, FN>(g, acc, m0, n0 / 2, el32, ehalf, cur.split);
     } else if constexpr (EPI == Epi::GATED_GRAD) {
       gated_grad_epilogue<FM, FN, ES>(g, acc, m0, n0, el32, ehalf);
     } else if constexpr (EPI == Epi::STORE || EPI == Epi::STORE2) {
@@ -706,6 +710,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_kernel(ProductArgs g)
         }
       }
     }
+    if constexpr (AGAIN) read_frags(rb, 0);
     move_on(cp);
   }
   if constexpr (E == Elem::F8W) {

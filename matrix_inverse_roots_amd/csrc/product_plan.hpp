@@ -58,6 +58,7 @@ template <size_t COUNT> shampoo_status check_apart(const Span (&spans)[COUNT], s
 struct Shape {
   bool large;
   int splits, split_stages, nst;
+  int tile = 0;  // Tile, where plan_layer chose
 };
 
 constexpr int CUS = 256;  // planning only; the grid follows the device
@@ -121,6 +122,18 @@ hipError_t launch_product(const ProductArgs& g, bool large, int64_t batch, hipSt
   const int64_t items = batch * g.splits * ((g.M + 127) / 128) * (EPI == Epi::GATED ? (g.N + 63) / 64 : (g.N + 127) / 128);
   if (items <= CUS) return launch_tiles<E, 1, 4, 4, 1, 4, 1, AS, BS, EPI, FA, FB>(g, batch, st);
   return launch_tiles<E, 1, 4, 4, 1, 2, 2, AS, BS, EPI, FA, FB>(g, batch, st);
+}
+
+// Tiles of the feed-forward layers' products.
+enum Tile { TILE_64 = 1, TILE_128, TILE_MEDIUM, TILE_LARGE };
+
+template <Elem E, bool AS, bool BS, Epi EPI>
+hipError_t launch_layer(const ProductArgs& g, const Shape& s, int64_t batch, hipStream_t st) {
+  if constexpr (E == Elem::F32 && EPI != Epi::GATED) {
+    if (s.tile == TILE_64) return launch_tiles<E, 1, 1, 2, 2, 4, 2, AS, BS, EPI, 0, 0>(g, batch, st);
+  }
+  if (s.tile == TILE_MEDIUM) return launch_tiles<E, 2, 2, 4, 2, 3, 1, AS, BS, EPI, 0, 0>(g, batch, st);
+  return launch_product<E, AS, BS, EPI>(g, s.tile == TILE_LARGE, batch, st);
 }
 
 inline void set_shape(ProductArgs& g, const Shape& s) {
