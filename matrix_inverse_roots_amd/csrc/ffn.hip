@@ -100,15 +100,13 @@ hipError_t place(const Operand& o, const void*& p, const void* scale, int64_t ro
       hipLaunchKernelGGL(widen_rows_kernel<uint16_t>, dim3(wgs), dim3(256), 0, st, (const uint8_t*)p, (const uint8_t*)scale, up(cols, 128),
                          up(up(cols, 128) / 128, 4), rows, (int)cols, (uint16_t*)to, o.ld);
   } else {
-    const int wgs = (int)std::max<int64_t>(1, std::min<int64_t>((rows + 3) / 4, 8192));
-    const int vec = ld % 4 == 0 && aligned(p, 4 * size_of(from));
+    const int wgs = (int)std::min<int64_t>((rows * (o.ld / 8) + 255) / 256, 16384);
     if (from == SHAMPOO_F32 && dt == SHAMPOO_BF16)
-      hipLaunchKernelGGL((pad_rows_kernel<float, uint16_t>), dim3(wgs), dim3(256), 0, st, (const float*)p, ld, rows, (int)cols, (uint16_t*)to, (int)o.ld, vec);
+      hipLaunchKernelGGL((copy_rows_kernel<float, uint16_t>), dim3(wgs), dim3(256), 0, st, (const float*)p, ld, rows, (int)cols, (uint16_t*)to, o.ld);
     else if (dt == SHAMPOO_F32)
-      hipLaunchKernelGGL((pad_rows_kernel<float, float>), dim3(wgs), dim3(256), 0, st, (const float*)p, ld, rows, (int)cols, (float*)to, (int)o.ld, vec);
+      hipLaunchKernelGGL((copy_rows_kernel<float, float>), dim3(wgs), dim3(256), 0, st, (const float*)p, ld, rows, (int)cols, (float*)to, o.ld);
     else
-      hipLaunchKernelGGL((pad_rows_kernel<uint16_t, uint16_t>), dim3(wgs), dim3(256), 0, st, (const uint16_t*)p, ld, rows, (int)cols, (uint16_t*)to,
-                         (int)o.ld, vec);
+      hipLaunchKernelGGL((copy_rows_kernel<uint16_t, uint16_t>), dim3(wgs), dim3(256), 0, st, (const uint16_t*)p, ld, rows, (int)cols, (uint16_t*)to, o.ld);
   }
   p = to;
   return hipGetLastError();
@@ -189,6 +187,11 @@ template <Elem E> hipError_t run_layer(const Layer& l, hipStream_t st) {
   g.ffn = l.ffn;
   const Out o{l.y, l.ldy, 0, out_code(l.y_dt), rows_vec(l.y, l.ldy, 0, l.y_dt), 0.f};
   point_output(g, l.shape, o, l.part, 1);
+  if (l.shape.splits > 1) {  // rows that start on 16 bytes
+    g.ldc = up(l.N, 4);
+    g.split_stride = l.M * g.ldc;
+    g.vec = 1;
+  }
   if (l.shape.splits == 1) return launch_layer<E, false, false, Epi::LINEAR>(g, l.shape, 1, st);
   HIP_TRY_ERR((launch_layer<E, false, false, Epi::STORE>(g, l.shape, 1, st)));
   FinishArgs f{l.part, g.split_stride, l.shape.splits, (int)l.M, (int)l.N, 0, l.y, l.ldy, out_code(l.y_dt), l.ffn};
@@ -238,7 +241,7 @@ shampoo_status linear_layout(const shampoo_linear_args* a, LinearLayout* L) {
     L->x = operand(c, a->x, a->M, a->K, a->ld_x, a->dt, a->dt);
     L->w = operand(c, a->w, a->N, a->K, a->ld_w, a->w_dt, a->dt);
     L->shape = plan_layer(1, a->M, a->N, a->K, (int)size_of(a->dt), true, a->bias || a->residual || a->keep || a->activation ? 150 : 0);
-    L->part = c.take(partial_bytes(L->shape, 1, a->M, a->N));
+    L->part = c.take(partial_bytes(L->shape, 1, a->M, up(a->N, 4)));
   }
   L->total = c.at;
   return SHAMPOO_OK;
@@ -326,7 +329,7 @@ template <Elem E, typename T> hipError_t run_linear_grad(const shampoo_linear_gr
     hipLaunchKernelGGL(act_grad_kernel<T>, dim3((unsigned)(chunks * g.blocks)), dim3(256), 0, st, g);
     HIP_TRY_ERR(hipGetLastError());
     if (a->dbias) {
-      hipLaunchKernelGGL(bias_grad_kernel, dim3((unsigned)((a->N + 63) / 64)), dim3(256), 0, st, g.sums, (int)chunks, (int)a->N, a->dbias,
+      hipLaunchKernelGGL(bias_grad_kernel, dim3((unsigned)((a->N + 63) / 64)), dim3(1024), 0, st, g.sums, (int)chunks, (int)a->N, a->dbias,
                          out_code(a->dbias_dt), a->accumulate);
       HIP_TRY_ERR(hipGetLastError());
     }
@@ -405,7 +408,7 @@ shampoo_status gated_layout(const shampoo_gated_ffn_args* a, GatedLayout* L) {
   L->in = plan_layer(1, a->T, 2 * a->f, a->d, es, true, 0, true);
   L->out = plan_layer(1, a->T, a->d, a->f, es, true, a->residual ? 150 : 0);
   L->h = c.take((size_t)a->T * L->ldh * es);
-  L->part = c.take(std::max(partial_bytes(L->in, 1, a->T, 2 * a->f), partial_bytes(L->out, 1, a->T, a->d)));
+  L->part = c.take(std::max(partial_bytes(L->in, 1, a->T, 2 * up(a->f, 4)), partial_bytes(L->out, 1, a->T, up(a->d, 4))));
   L->total = c.at;
   return SHAMPOO_OK;
 }
@@ -444,7 +447,7 @@ template <Elem E> hipError_t run_gated(const shampoo_gated_ffn_args* a, const Ga
   g.ffn.part = part;
   HIP_TRY_ERR((launch_layer<E, false, false, Epi::GATED>(g, L.in, 1, st)));
   if (L.in.splits > 1) {
-    const FinishArgs f{part, 2 * a->T * a->f, L.in.splits, (int)a->T, (int)a->f, (int)L.ldh, g.C, L.ldh, g.c_dt, g.ffn};
+    const FinishArgs f{part, 2 * a->T * up(a->f, 4), L.in.splits, (int)a->T, (int)a->f, (int)L.ldh, g.C, L.ldh, g.c_dt, g.ffn};
     hipLaunchKernelGGL(ffn_finish_kernel<true>, dim3((unsigned)((L.ldh + 1023) / 1024), (unsigned)std::min<int64_t>(a->T, 65535)), dim3(256), 0, st, f);
     HIP_TRY_ERR(hipGetLastError());
   }

@@ -386,11 +386,12 @@ __device__ __forceinline__ void gated_epilogue(const ProductArgs& g, floatx16 (&
   constexpr int HF = FN / 2;
   const FfnArgs& e = g.ffn;
   if (g.splits > 1) {
-    float* part = e.part + (int64_t)range * g.M * 2 * g.N;
+    const int P = (g.N + 3) & ~3;
+    float* part = e.part + (int64_t)range * g.M * 2 * P;
     for_each<FM * FN>([&](auto K) __attribute__((always_inline)) {
       constexpr int I = K.value / FN, J = K.value % FN;
       const int m = m0 + 32 * I + l32;
-      store_block(part + m * (int64_t)(2 * g.N) + J / HF * g.N, m < g.M, n0 + 32 * (J % HF), half, g.N, g.N % 4 == 0, acc[I][J]);
+      store_block(part + m * (int64_t)(2 * P) + J / HF * P, m < g.M, n0 + 32 * (J % HF), half, g.N, 1, acc[I][J]);
     });
     return;
   }

@@ -107,14 +107,24 @@ __global__ __launch_bounds__(256) void ffn_rows_kernel(RowsArgs g) {
         for (int e = 0; e < 8; ++e) acc[m][r] = __builtin_fmaf(a[e], b[r][e], acc[m][r]);
     }
   }
+  // sums over the wave: halves of it, then quarters, take a value each, so that
+  // a register serves four values when 16 lanes are left to join
 #pragma unroll
   for (int m = 0; m < MB; ++m)
 #pragma unroll
-    for (int r = 0; r < NW; ++r) {
-      float s = acc[m][r];
+    for (int r = 0; r < NW; r += 4) {
+      float two[2];
 #pragma unroll
-      for (int d = 1; d < 64; d *= 2) s += __shfl_xor(s, d);
-      if (lane == 0) red[wave][m * NW + r] = s;
+      for (int i = 0; i < 2; ++i) {
+        const auto w = __builtin_amdgcn_permlane32_swap(float_bits(acc[m][r + 2 * i]), float_bits(acc[m][r + 2 * i + 1]), false, false);
+        two[i] = bits_float(w[0]) + bits_float(w[1]);
+      }
+      const auto w = __builtin_amdgcn_permlane16_swap(float_bits(two[0]), float_bits(two[1]), false, false);
+      float t = bits_float(w[0]) + bits_float(w[1]);
+#pragma unroll
+      for (int d = 1; d < 16; d *= 2) t += __shfl_xor(t, d);
+      // quarters: value 0 of r, 2, 1, 3
+      if ((lane & 15) == 0) red[wave][m * NW + r + ((lane >> 4 & 1) << 1 | lane >> 5)] = t;
     }
   __syncthreads();
   if (ks != 0) return;
@@ -139,7 +149,7 @@ __global__ __launch_bounds__(256) void ffn_rows_kernel(RowsArgs g) {
 // partial results of a product split along k
 // ---------------------------------------------------------------------------
 struct FinishArgs {
-  const float* part;      // [range][M][N], GATED: [range][M][2 N]
+  const float* part;      // [range][M][P], GATED: [range][M][2 P], P: N rounded up to 4
   int64_t range_stride;
   int splits, M, N, wide; // wide: GATED: h's padded width
   void* y;
@@ -154,26 +164,22 @@ template <bool GATED>
 static __global__ __launch_bounds__(256) void ffn_finish_kernel(FinishArgs g) {
   const FfnArgs& e = g.ffn;
   const int n = (blockIdx.x * 256 + threadIdx.x) * 4;
-  const int64_t row = GATED ? 2 * (int64_t)g.N : g.N;
+  const int P = (g.N + 3) & ~3;
+  const int64_t row = GATED ? 2 * (int64_t)P : P;
   for (int m = blockIdx.y; m < g.M; m += gridDim.y) {
     float z[GATED ? 2 : 1][4];
 #pragma unroll
     for (int p = 0; p < (GATED ? 2 : 1); ++p) {
 #pragma unroll
       for (int c = 0; c < 4; ++c) z[p][c] = 0.f;
-      const float* from = g.part + m * row + p * g.N + n;
-      if (n + 4 <= g.N && g.N % 4 == 0) {
+      const float* from = g.part + m * row + p * P + n;
+      if (n < g.N) {
 #pragma unroll 4
         for (int s = 0; s < g.splits; ++s) {
           const floatx4 v = *reinterpret_cast<const floatx4*>(from + s * g.range_stride);
 #pragma unroll
-          for (int c = 0; c < 4; ++c) z[p][c] += v[c];
+          for (int c = 0; c < 4; ++c) z[p][c] += n + c < g.N ? v[c] : 0.f;  // columns from N on hold anything
         }
-      } else {
-        for (int s = 0; s < g.splits; ++s)
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-            if (n + c < g.N) z[p][c] += from[s * g.range_stride + c];
       }
     }
     if (e.bias) {
@@ -314,22 +320,59 @@ __global__ __launch_bounds__(256) void act_grad_kernel(ActGradArgs g) {
 }
 
 // dbias from the chunks' sums: a column per thread of a wave, chunks dealt to
-// the 4 waves (+ dbias where accumulated).
-static __global__ __launch_bounds__(256) void bias_grad_kernel(const float* __restrict__ sums, int chunks, int N, void* __restrict__ out,
-                                                               int dt, int accumulate) {
-  __shared__ float red[4][64];
+// the 16 waves (+ dbias where accumulated).  Bound by latency.
+static __global__ __launch_bounds__(1024) void bias_grad_kernel(const float* __restrict__ sums, int chunks, int N, void* __restrict__ out,
+                                                                int dt, int accumulate) {
+  __shared__ float red[16][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n = blockIdx.x * 64 + lane;
   float s = 0.f;
   if (n < N) {
 #pragma unroll 4
-    for (int c = wave; c < chunks; c += 4) s += sums[(int64_t)c * N + n];
+    for (int c = wave; c < chunks; c += 16) s += sums[(int64_t)c * N + n];
   }
   red[wave][lane] = s;
   __syncthreads();
   if (wave != 0 || n >= N) return;
-  s = (red[0][lane] + red[1][lane]) + (red[2][lane] + red[3][lane]);
+  s = 0.f;
+#pragma unroll
+  for (int w = 0; w < 16; ++w) s += red[w][lane];
   if (accumulate) s += load_one(out, dt, n);
   store_one(out, dt, n, s);
+}
+
+// ---------------------------------------------------------------------------
+// operands whose rows do not start on 16 bytes
+// ---------------------------------------------------------------------------
+// Rows of `cols` elements, ld apart, as rows of ldo (a multiple of 8) with zeros
+// behind; float32 to bfloat16 on the way where TI and TO say so.  A thread
+// takes 8 elements, in 16-byte loads at any element's address: 1000 rows of
+// 2731 bfloat16 (11 MB) MEASURED_COPY.
+template <typename TI, typename TO>
+__global__ __launch_bounds__(256) void copy_rows_kernel(const TI* __restrict__ x, int64_t ld, int64_t rows, int cols, TO* __restrict__ o, int64_t ldo) {
+  struct Eight { TI v[8]; };
+  const int per = (int)(ldo / 8);
+  const int64_t total = rows * per;
+  for (int64_t i = blockIdx.x * (int64_t)256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+    const int64_t r = i / per;
+    const int c = (int)(i - r * per) * 8;
+    const TI* from = x + r * ld + c;
+    Eight w;
+    if (c + 8 <= cols) {
+      __builtin_memcpy(&w, from, sizeof(w));
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) w.v[e] = c + e < cols ? from[e] : TI(0);
+    }
+    TO* to = o + r * ldo + c;
+    if constexpr (sizeof(TO) == 4) {
+#pragma unroll
+      for (int e = 0; e < 8; e += 4) *reinterpret_cast<floatx4*>(to + e) = floatx4{w.v[e], w.v[e + 1], w.v[e + 2], w.v[e + 3]};
+    } else if constexpr (sizeof(TI) == 4) {
+      *reinterpret_cast<u32x4*>(to) = u32x4{pack_bf16(w.v[0], w.v[1]), pack_bf16(w.v[2], w.v[3]), pack_bf16(w.v[4], w.v[5]), pack_bf16(w.v[6], w.v[7])};
+    } else {
+      *reinterpret_cast<u32x4*>(to) = __builtin_bit_cast(u32x4, w);
+    }
+  }
 }
 
 // ---------------------------------------------------------------------------

@@ -130,7 +130,7 @@ enum Tile { TILE_64 = 1, TILE_128, TILE_MEDIUM, TILE_LARGE };
 template <Elem E, bool AS, bool BS, Epi EPI>
 hipError_t launch_layer(const ProductArgs& g, const Shape& s, int64_t batch, hipStream_t st) {
   if constexpr (E == Elem::F32 && EPI != Epi::GATED) {
-    if (s.tile == TILE_64) return launch_tiles<E, 1, 1, 2, 2, 4, 2, AS, BS, EPI, 0, 0>(g, batch, st);
+    if (s.tile == TILE_64) return launch_tiles<E, 1, 1, 2, 2, 3, 3, AS, BS, EPI, 0, 0>(g, batch, st);
   }
   if (s.tile == TILE_MEDIUM) return launch_tiles<E, 2, 2, 4, 2, 3, 1, AS, BS, EPI, 0, 0>(g, batch, st);
   return launch_product<E, AS, BS, EPI>(g, s.tile == TILE_LARGE, batch, st);

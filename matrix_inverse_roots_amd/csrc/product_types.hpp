@@ -31,7 +31,7 @@ struct FfnArgs {
   void* keep[2];
   uint8_t* keep_scale[2];
   int64_t ld_keep;        // elements; 8 bits: N rounded up to 32
-  float* part;            // GATED with ranges of k: partial results [range][M][2 N]
+  float* part;            // GATED with ranges of k: partial results [range][M][2 P], P: N rounded up to 4
   void* du;               // GATED_GRAD: rows of ldc (C receives dg)
   void* h;                // GATED_GRAD: rows of ldc / 2
   int bias_bf16, bias_vec, act, keep_dt, keep_vec, residual_vec;  // keep_dt: 0 float32, 2 bfloat16, 4 e4m3
