@@ -65,20 +65,20 @@ struct ActGelu {
   }
 };
 
-// z sigma(c1 z + c3 z^3)
-struct ActSigmoid {
-  float c1, c3;
+// z sigma(p(z)): p(z) = z, or gelu_tanh's cubic (whose z^2 may overflow: p keeps its sign)
+template <bool CUBIC> struct ActSigmoid {
+  static constexpr float C1 = CUBIC ? 1.5957691216057308f : 1.f, C3 = 0.07135481627260025f;
   __device__ __forceinline__ float sigma(float z) const {
     constexpr float L2E = 1.4426950408889634f;
-    const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(-c3 * L2E, z * z, -c1 * L2E) * z);
-    return __builtin_amdgcn_rcpf(1.f + e);
+    const float slope = CUBIC ? __builtin_fmaf(-C3 * L2E, z * z, -C1 * L2E) : -L2E;
+    return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(slope * z));
   }
   __device__ __forceinline__ float value(float z) const { return z * sigma(z); }
   __device__ __forceinline__ float both(float z, float& slope) const {
     const float s = sigma(z);
     // behind 10^4 sigma is 0 or 1, and z p'(z) would overflow
     const float w = fminf(fmaxf(z, -1e4f), 1e4f);
-    slope = __builtin_fmaf(s * (1.f - s), w * __builtin_fmaf(3.f * c3, w * w, c1), s);
+    slope = __builtin_fmaf(s * (1.f - s), CUBIC ? w * __builtin_fmaf(3.f * C3, w * w, C1) : w, s);
     return z * s;
   }
 };
@@ -88,8 +88,8 @@ template <typename F> __device__ __forceinline__ void with_activation(int act, F
   switch (act) {
     case 1: f(ActRelu{}); break;
     case 2: f(ActGelu{}); break;
-    case 3: f(ActSigmoid{1.5957691216057308f, 0.07135481627260025f}); break;
-    case 4: f(ActSigmoid{1.f, 0.f}); break;
+    case 3: f(ActSigmoid<true>{}); break;
+    case 4: f(ActSigmoid<false>{}); break;
     default: f(ActNone{}); break;
   }
 }

@@ -129,6 +129,7 @@ hipError_t place(const Operand& o, const void*& p, const void* scale, int64_t ro
 // x 64 one 0.073 (777 x 2731 x 1000, 154 tiles or 559: 76 and 60 us; 2048 x
 // 2048 x 1024, 256 or 1024: 72 and 79).
 Shape plan_layer(int64_t batch, int64_t M, int64_t N, int64_t K, int es, bool may_split, int epilogue, bool dual = false) {
+  if (M == 0 || K == 0) return Shape{};  // an empty batch, which launches none
   Shape s = plan_shape(batch, M, N, K, es, may_split);
   s.tile = s.large ? TILE_LARGE : TILE_128;
   auto tiles = [&](int64_t m, int64_t n) { return batch * ((M + m - 1) / m) * ((N + n - 1) / n); };

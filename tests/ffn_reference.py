@@ -46,6 +46,11 @@ def act_off(z, kind):
     return rel * a.abs() + 1e-36, rel * spread + 1e-36
 
 
+def two(e):
+    """2^e (float64) for whole e, from its bits: a device's pow may be off in the last one."""
+    return ((e.long() + 1023) << 52).view(torch.float64)
+
+
 def blocks(x, block):
     """x [rows, cols] in float32 -> (e4m3 values as float32, scale bytes) per ``block`` columns of a row, exactly."""
     rows, cols = x.shape
@@ -57,12 +62,12 @@ def blocks(x, block):
     e = torch.zeros_like(size)
     on = size > 0
     e[on] = torch.ceil(torch.log2(size[on] / 448.0))
-    e = torch.where(on & (size <= 448.0 * 2.0 ** (e - 1)), e - 1, e)
-    e = torch.where(on & (size > 448.0 * 2.0 ** e), e + 1, e).clamp(-127, 127)
-    v = p / (2.0 ** e)[:, :, None]
+    e = torch.where(on & (size <= 448.0 * two(e - 1)), e - 1, e)
+    e = torch.where(on & (size > 448.0 * two(e)), e + 1, e).clamp(-127, 127)
+    v = p / two(e)[:, :, None]
     a = v.abs()
     low = torch.floor(torch.log2(torch.where(a > 0, a, torch.ones_like(a)))).clamp(min=-6)
-    step = 2.0 ** (low - 3)
+    step = two(low - 3)
     q = torch.where(torch.isfinite(v), torch.round(v / step) * step, torch.full_like(v, float("nan")))
     return q.reshape(rows, wide).float(), (e + 127).to(torch.uint8)
 
@@ -71,7 +76,7 @@ def stand(q, s, cols, block):
     """What 8-bit values and scales stand for, float64 [rows, cols]."""
     rows, wide = q.shape
     e = s.view(torch.uint8).double()[:, :wide // block] - 127
-    return (q.double().view(rows, -1, block) * (2.0 ** e)[:, :, None]).view(rows, wide)[:, :cols]
+    return (q.double().view(rows, -1, block) * two(e)[:, :, None]).view(rows, wide)[:, :cols]
 
 
 def widen(kept, cols, block=32):
