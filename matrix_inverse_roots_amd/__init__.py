@@ -767,19 +767,26 @@ def shampoo_kept_empty(rows, cols, keep, device, stream=None):
             _empty((rows, wide // KEEP_BLOCK), torch.float8_e8m0fnu, device, stream))
 
 
-def _at(t):
-    return None if t is None else t.data_ptr()
+_LAYER_CODES = {}
+
+
+def _layer_codes():
+    """Types of the layers' tensors."""
+    if not _LAYER_CODES:
+        torch = _torch()
+        _LAYER_CODES.update({torch.float32: F32, torch.bfloat16: BF16})
+    return _LAYER_CODES
 
 
 def _float_rows(t, name, rows, cols, dtypes):
-    """(pointer, elements between rows) of a [rows, cols] tensor in one of two types."""
+    """(pointer, elements between rows) of a [rows, cols] tensor in one of these types."""
     if t is None:
         return None, cols
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols or (t.dtype != dtypes[0] and t.dtype != dtypes[1]):
+    if t.shape != (rows, cols) or t.dtype not in dtypes:
         raise ValueError("%s must be a %s tensor of shape %s, got %s %s" % (
             name, " or ".join(sorted({str(d) for d in dtypes})), (rows, cols), t.dtype, tuple(t.shape)))
     down, across = t.stride()
-    if cols > 1 and across != 1 and rows:
+    if across != 1 and cols > 1 and rows:
         raise ValueError("%s must have unit column stride" % name)
     if rows <= 1:
         down = cols
@@ -790,12 +797,12 @@ def _float_rows(t, name, rows, cols, dtypes):
 
 def _kept_rows(t, name, rows, cols, dtype):
     """(values, scales, stride, type code) of what is kept of [rows, cols]."""
-    torch = _torch()
     if t is None:
-        return None, None, cols, _dtype_code_of(dtype)
+        return None, None, cols, _layer_codes()[dtype]
+    torch = _torch()
     if isinstance(t, torch.Tensor):
-        p, ld = _float_rows(t, name, rows, cols, (dtype, dtype))
-        return p, None, ld, _dtype_code_of(dtype)
+        p, ld = _float_rows(t, name, rows, cols, (dtype,))
+        return p, None, ld, _layer_codes()[dtype]
     q, s = t
     wide = _up(cols, KEEP_BLOCK)
     for v, shape, kinds in ((q, (rows, wide), (torch.float8_e4m3fn,)),
@@ -810,8 +817,8 @@ def _given_rows(t, name, rows, cols, dtype):
     """The same of an operand that may be in 8 bits as ``shampoo_quantize_f8`` gives it (block_rows 1)."""
     torch = _torch()
     if t is None or isinstance(t, torch.Tensor):
-        p, ld = _float_rows(t, name, rows, cols, (dtype, dtype))
-        return p, None, ld, _dtype_code_of(dtype)
+        p, ld = _float_rows(t, name, rows, cols, (dtype,))
+        return p, None, ld, _layer_codes()[dtype]
     q, s = t
     wide = _up(cols, 128)
     for v, shape, kinds in ((q, (rows, wide), (torch.float8_e4m3fn,)),
@@ -822,14 +829,10 @@ def _given_rows(t, name, rows, cols, dtype):
     return q.data_ptr(), s.data_ptr(), wide, E4M3
 
 
-def _dtype_code_of(dtype):
-    return F32 if dtype == _torch().float32 else BF16
-
-
 def _vector(t, name, n, dtypes):
     if t is None:
         return None
-    if t.dim() != 1 or t.shape[0] != n or t.dtype not in dtypes or not t.is_contiguous():
+    if t.shape != (n,) or t.dtype not in dtypes or not t.is_contiguous():
         raise ValueError("%s must be a contiguous %s tensor of shape (%d,), got %s %s" % (
             name, " or ".join(sorted({str(d) for d in dtypes})), n, t.dtype, tuple(t.shape)))
     return t.data_ptr()
@@ -841,13 +844,15 @@ def _parts(t):
 
 
 def _layer_types(x, act):
-    torch = _torch()
-    if x.dtype != torch.float32 and x.dtype != torch.bfloat16:
-        raise TypeError("unsupported dtype %s (float32, bfloat16)" % x.dtype)
-    code = ACTIVATIONS.get(act)
-    if code is None:
+    """(x's type, its code, the types that may stand beside it, the activation's code)."""
+    codes = _layer_codes()
+    dt = x.dtype
+    if dt not in codes:
+        raise TypeError("unsupported dtype %s (float32, bfloat16)" % dt)
+    kind = ACTIVATIONS.get(act)
+    if kind is None:
         raise ValueError("activation must be one of %s" % [a for a in ACTIVATIONS if a is not None])
-    return x.dtype, code
+    return dt, codes[dt], (dt,) if codes[dt] == F32 else (dt, _torch().float32), kind
 
 
 def _with_workspace(name, args, ws, dev, stream):
@@ -869,23 +874,21 @@ def _workspace_of(name, args):
 
 
 def _linear_args(x, w, y, bias, activation, residual, keep):
-    torch = _torch()
     if x.dim() != 2 or w.dim() != 2:
         raise ValueError("x and w must have 2 dimensions")
-    dt, act = _layer_types(x, activation)
+    dt, code, both, act = _layer_types(x, activation)
+    codes, own = _LAYER_CODES, (dt,)
     M, K = x.shape
     N = w.shape[0]
-    both = (dt, torch.float32)
-    xp, ldx = _float_rows(x, "x", M, K, (dt, dt))
+    xp, ldx = _float_rows(x, "x", M, K, own)
     wp, ldw = _float_rows(w, "w", N, K, both)
     yp, ldy = _float_rows(y, "y", M, N, both)
     ydt = dt if y is None else y.dtype
-    rp, ldr = _float_rows(residual, "residual", M, N, (ydt, ydt))
-    bp = _vector(bias, "bias", N, both)
-    kp, ks, ldk, kdt = _kept_rows(keep, "keep", M, N, dt)
-    code = _dtype_code_of(dt)
-    return LinearArgsC(xp, wp, bp, rp, yp, kp, ks, ldx, ldw, ldr, ldy, ldk, M, N, K, code, _dtype_code_of(w.dtype),
-                       code if bias is None else _dtype_code_of(bias.dtype), _dtype_code_of(ydt), kdt, act, None, 0)
+    rp, ldr = (None, N) if residual is None else _float_rows(residual, "residual", M, N, (ydt,))
+    bp, bdt = (None, code) if bias is None else (_vector(bias, "bias", N, both), codes[bias.dtype])
+    kp, ks, ldk, kdt = (None, None, N, code) if keep is None else _kept_rows(keep, "keep", M, N, dt)
+    return LinearArgsC(xp, wp, bp, rp, yp, kp, ks, ldx, ldw, ldr, ldy, ldk, M, N, K, code, codes[w.dtype], bdt, codes[ydt],
+                       kdt, act, None, 0)
 
 
 def shampoo_linear_workspace(x, w, y=None, bias=None, activation=None, residual=None, keep=None):
@@ -911,10 +914,10 @@ def shampoo_linear(x, w, y=None, bias=None, activation=None, residual=None, keep
 
 
 def _linear_grad_args(dy, x, w, kept, activation, dx, dw, dbias, accumulate):
-    torch = _torch()
     if dy.dim() != 2:
         raise ValueError("dy must have 2 dimensions")
-    dt, act = _layer_types(dy, activation)
+    dt, code, both, act = _layer_types(dy, activation)
+    codes, own = _LAYER_CODES, (dt,)
     M, N = dy.shape
     K = next((t.shape[1] for t in (w, dw, dx) if t is not None and t.dim() == 2), None)
     if K is None:
@@ -927,19 +930,17 @@ def _linear_grad_args(dy, x, w, kept, activation, dx, dw, dbias, accumulate):
         raise ValueError("dw needs x")
     if act and kept is None:
         raise ValueError("the activation's gradient needs what the forward pass kept")
-    both = (dt, torch.float32)
-    dyp, lddy = _float_rows(dy, "dy", M, N, (dt, dt))
+    dyp, lddy = _float_rows(dy, "dy", M, N, own)
     xp, xs, ldx, xdt = _given_rows(x if dw is not None else None, "x", M, K, dt)
     wp, ldw = _float_rows(w if dx is not None else None, "w", N, K, both)
     kp, ks, ldk, kdt = _kept_rows(kept if act else None, "kept", M, N, dt)
-    dxp, lddx = _float_rows(dx, "dx", M, K, (dt, dt))
+    dxp, lddx = _float_rows(dx, "dx", M, K, own)
     dwp, lddw = _float_rows(dw, "dw", N, K, both)
     dbp = _vector(dbias, "dbias", N, both)
-    code = _dtype_code_of(dt)
     return LinearGradArgsC(dyp, xp, xs, wp, kp, ks, dxp, dwp, dbp, lddy, ldx, ldw, ldk, lddx, lddw, M, N, K, code, xdt,
-                           code if wp is None else _dtype_code_of(w.dtype), kdt,
-                           code if dw is None else _dtype_code_of(dw.dtype),
-                           code if dbias is None else _dtype_code_of(dbias.dtype), act, 1 if accumulate else 0, None, 0)
+                           code if wp is None else codes[w.dtype], kdt,
+                           code if dw is None else codes[dw.dtype],
+                           code if dbias is None else codes[dbias.dtype], act, 1 if accumulate else 0, None, 0)
 
 
 def shampoo_linear_grad_workspace(dy, x, w, kept=None, activation=None, dx=None, dw=None, dbias=None):
@@ -968,32 +969,31 @@ def _gated_sizes(x, w_gate):
     return x.shape[0], x.shape[1], w_gate.shape[0]
 
 
-def _gated_weights(w_gate, w_up, w_down, d, f, dt):
-    torch = _torch()
-    kind = w_gate.dtype if w_gate is not None else w_down.dtype
-    if kind != dt and kind != torch.float32:
-        raise ValueError("weights must be %s or torch.float32, got %s" % (dt, kind))
-    one = (kind, kind)
+def _gated_weights(w_gate, w_up, w_down, d, f, both):
+    kind = w_down.dtype
+    if kind not in both:
+        raise ValueError("weights must be %s, got %s" % (" or ".join(str(k) for k in both), kind))
+    one = (kind,)
     return (_float_rows(w_gate, "w_gate", f, d, one), _float_rows(w_up, "w_up", f, d, one),
-            _float_rows(w_down, "w_down", d, f, one), _dtype_code_of(kind))
+            _float_rows(w_down, "w_down", d, f, one), _LAYER_CODES[kind])
 
 
 def _gated_args(x, w_gate, w_up, w_down, y, activation, residual, keep):
-    torch = _torch()
     T, d, f = _gated_sizes(x, w_gate)
-    dt, act = _layer_types(x, activation)
-    both = (dt, torch.float32)
-    xp, ldx = _float_rows(x, "x", T, d, (dt, dt))
-    (gp, ldg), (up, ldu), (dp, ldd), wdt = _gated_weights(w_gate, w_up, w_down, d, f, dt)
+    dt, code, both, act = _layer_types(x, activation)
+    xp, ldx = _float_rows(x, "x", T, d, (dt,))
+    (gp, ldg), (up, ldu), (dp, ldd), wdt = _gated_weights(w_gate, w_up, w_down, d, f, both)
     yp, ldy = _float_rows(y, "y", T, d, both)
     ydt = dt if y is None else y.dtype
-    rp, ldr = _float_rows(residual, "residual", T, d, (ydt, ydt))
-    a, b = (None, None) if keep is None else keep
-    (kg, sg, ldk, kdt), (ku, su, ldk2, kdt2) = _kept_rows(a, "keep[0]", T, f, dt), _kept_rows(b, "keep[1]", T, f, dt)
-    if ldk != ldk2 or kdt != kdt2:
-        raise ValueError("both projections must be kept in one type, with one row stride")
-    return GatedArgsC(xp, gp, up, dp, rp, yp, kg, sg, ku, su, ldx, ldg, ldu, ldd, ldr, ldy, ldk, T, d, f,
-                      _dtype_code_of(dt), wdt, _dtype_code_of(ydt), kdt, act, None, 0)
+    rp, ldr = (None, d) if residual is None else _float_rows(residual, "residual", T, d, (ydt,))
+    kg = sg = ku = su = None
+    ldk, kdt = f, code
+    if keep is not None:
+        (kg, sg, ldk, kdt), (ku, su, ldk2, kdt2) = (_kept_rows(t, "keep[%d]" % i, T, f, dt) for i, t in enumerate(keep))
+        if ldk != ldk2 or kdt != kdt2:
+            raise ValueError("both projections must be kept in one type, with one row stride")
+    return GatedArgsC(xp, gp, up, dp, rp, yp, kg, sg, ku, su, ldx, ldg, ldu, ldd, ldr, ldy, ldk, T, d, f, code, wdt,
+                      _LAYER_CODES[ydt], kdt, act, None, 0)
 
 
 def shampoo_gated_ffn_workspace(x, w_gate, w_up, w_down, y=None, activation="silu", residual=None, keep=None):
@@ -1017,34 +1017,32 @@ def shampoo_gated_ffn(x, w_gate, w_up, w_down, y=None, activation="silu", residu
 
 
 def _gated_grad_args(dy, x, w_gate, w_up, w_down, kept, dx, dw_gate, dw_up, dw_down, activation, accumulate):
-    torch = _torch()
     if dy.dim() != 2 or w_down.dim() != 2:
         raise ValueError("dy and the weights must have 2 dimensions")
-    dt, act = _layer_types(dy, activation)
+    dt, code, both, act = _layer_types(dy, activation)
     T, d = dy.shape
     f = w_down.shape[1]
-    both = (dt, torch.float32)
     if dx is not None and (w_gate is None or w_up is None):
         raise ValueError("dx needs w_gate and w_up")
     wanted = dw_gate is not None or dw_up is not None
     if wanted and x is None:
         raise ValueError("dw_gate and dw_up need x")
-    dyp, lddy = _float_rows(dy, "dy", T, d, (dt, dt))
+    dyp, lddy = _float_rows(dy, "dy", T, d, (dt,))
     xp, xs, ldx, xdt = _given_rows(x if wanted else None, "x", T, d, dt)
     (gp, ldg), (up, ldu), (dp, ldd), wdt = _gated_weights(w_gate if dx is not None else None,
-                                                          w_up if dx is not None else None, w_down, d, f, dt)
+                                                          w_up if dx is not None else None, w_down, d, f, both)
     (kg, sg, ldk, kdt), (ku, su, ldk2, kdt2) = _kept_rows(kept[0], "kept[0]", T, f, dt), _kept_rows(kept[1], "kept[1]", T, f, dt)
     if ldk != ldk2 or kdt != kdt2:
         raise ValueError("both projections must have been kept in one type, with one row stride")
-    dxp, lddx = _float_rows(dx, "dx", T, d, (dt, dt))
+    dxp, lddx = _float_rows(dx, "dx", T, d, (dt,))
     kinds = {t.dtype for t in (dw_gate, dw_up, dw_down) if t is not None}
     if len(kinds) > 1:
         raise ValueError("the weights' gradients must be of one type, got %s" % sorted(str(k) for k in kinds))
     (wgp, ldwg), (wup, ldwu) = _float_rows(dw_gate, "dw_gate", f, d, both), _float_rows(dw_up, "dw_up", f, d, both)
     wdp, ldwd = _float_rows(dw_down, "dw_down", d, f, both)
     return GatedGradArgsC(dyp, xp, xs, gp, up, dp, kg, sg, ku, su, dxp, wgp, wup, wdp, lddy, ldx, ldg, ldu, ldd, ldk, lddx,
-                          ldwg, ldwu, ldwd, T, d, f, _dtype_code_of(dt), xdt, wdt, kdt,
-                          _dtype_code_of(kinds.pop() if kinds else dt), act, 1 if accumulate else 0, None, 0)
+                          ldwg, ldwu, ldwd, T, d, f, code, xdt, wdt, kdt,
+                          _LAYER_CODES[kinds.pop() if kinds else dt], act, 1 if accumulate else 0, None, 0)
 
 
 def shampoo_gated_ffn_grad_workspace(dy, x, w_gate, w_up, w_down, kept, dx=None, dw_gate=None, dw_up=None, dw_down=None,
