@@ -423,6 +423,7 @@ FfnArgs gated_kept(void* gate, void* gate_scale, void* up_, void* up_scale, int6
   e.ld_keep = dt == SHAMPOO_E4M3 ? up(f, KEEP_BLOCK) : ld;
   e.keep_dt = kept_code(dt);
   e.keep_vec = rows16(gate, ld, dt) && rows16(up_, ld, dt);
+  e.scale_vec = up(f, KEEP_BLOCK) % (4 * KEEP_BLOCK) == 0 && aligned(gate_scale, 4) && aligned(up_scale, 4);
   e.act = act;
   return e;
 }
@@ -697,6 +698,7 @@ shampoo_status shampoo_linear(const shampoo_linear_args* a, hipStream_t stream) 
   e.ld_keep = a->keep_dt == SHAMPOO_E4M3 ? up(a->N, KEEP_BLOCK) : a->ld_keep;
   e.keep_dt = kept_code(a->keep_dt);
   e.keep_vec = rows16(a->keep, a->ld_keep, a->keep_dt);
+  e.scale_vec = up(a->N, KEEP_BLOCK) % (4 * KEEP_BLOCK) == 0 && aligned(a->keep_scale, 4);
   e.act = a->activation;
   HIP_TRY(a->dt == SHAMPOO_F32 ? run_linear<Elem::F32>(a, L, e, stream) : run_linear<Elem::BF16>(a, L, e, stream));
   return SHAMPOO_OK;

@@ -162,9 +162,9 @@ __device__ __forceinline__ uint32_t block_max(const floatx16& x) {
 }
 
 // A block to 8 bits: 16 bytes a lane, the first half of the wave the first 16
-// columns.  Rows of `ld` bytes (cols rounded up to 32), their scales behind
-// one another; columns past `cols` become zeros.
-__device__ __forceinline__ void keep_f8(uint8_t* q, uint8_t* s, int64_t ld, int m, bool ok, int nb, int half, int cols, floatx16 x) {
+// columns; rows of `ld` bytes (cols rounded up to 32); columns past `cols`
+// become zeros.  Returns the scale's byte, which store_scales takes.
+__device__ __forceinline__ uint32_t keep_f8(uint8_t* q, int64_t ld, int m, bool ok, int nb, int half, int cols, floatx16 x) {
   if (nb + 32 > cols) {
 #pragma unroll
     for (int v = 0; v < 16; ++v)
@@ -177,15 +177,45 @@ __device__ __forceinline__ void keep_f8(uint8_t* q, uint8_t* s, int64_t ld, int 
   for (int i = 0; i < 4; ++i) w[i] = to_f8x4<0>(x[4 * i] * inv, x[4 * i + 1] * inv, x[4 * i + 2] * inv, x[4 * i + 3] * inv);
   const auto a = __builtin_amdgcn_permlane32_swap(w[0], w[2], false, false);
   const auto b = __builtin_amdgcn_permlane32_swap(w[1], w[3], false, false);
-  if (ok && nb < cols) {
-    *reinterpret_cast<u32x4*>(q + m * ld + nb + 16 * half) = u32x4{a[0], a[1], b[0], b[1]};
-    if (half == 0) s[m * (ld / KEEP_BLOCK) + nb / KEEP_BLOCK] = (uint8_t)byte;
+  if (ok && nb < cols) *reinterpret_cast<u32x4*>(q + m * ld + nb + 16 * half) = u32x4{a[0], a[1], b[0], b[1]};
+  return (uint32_t)byte;
+}
+__device__ __forceinline__ uint32_t keep_block(const FfnArgs& e, int which, int m, bool ok, int nb, int half, int cols, const floatx16& x) {
+  if (e.keep_dt == 4) return keep_f8((uint8_t*)e.keep[which], e.ld_keep, m, ok, nb, half, cols, x);
+  store_rows(e.keep[which], e.keep_dt, e.ld_keep, m, ok, nb, half, cols, e.keep_vec, x);
+  return 0;
+}
+
+// The scales of COUNT neighbouring blocks of a row, a byte each of `word`, in one
+// store (a byte for each block at a time was half of all the epilogue's line
+// accesses).
+template <int COUNT> __device__ __forceinline__ void store_scales(const FfnArgs& e, int which, int m, bool ok, int n0, int cols, uint32_t word) {
+  if (!ok) return;
+  uint8_t* s = e.keep_scale[which] + m * (e.ld_keep / KEEP_BLOCK) + n0 / KEEP_BLOCK;
+  if (COUNT > 1 && e.scale_vec && n0 + COUNT * KEEP_BLOCK <= cols) {
+    if constexpr (COUNT == 4) *reinterpret_cast<uint32_t*>(s) = word;
+    else if constexpr (COUNT == 2) *reinterpret_cast<uint16_t*>(s) = (uint16_t)word;
+  } else {
+#pragma unroll
+    for (int c = 0; c < COUNT; ++c)
+      if (n0 + c * KEEP_BLOCK < cols) s[c] = (uint8_t)(word >> (8 * c));
   }
 }
-__device__ __forceinline__ void keep_block(const FfnArgs& e, int which, int m, bool ok, int nb, int half, int cols, const floatx16& x) {
-  if (e.keep_dt == 4) keep_f8((uint8_t*)e.keep[which], e.keep_scale[which], e.ld_keep, m, ok, nb, half, cols, x);
-  else store_rows(e.keep[which], e.keep_dt, e.ld_keep, m, ok, nb, half, cols, e.keep_vec, x);
+template <int COUNT> __device__ __forceinline__ uint32_t load_scales(const FfnArgs& e, int which, int m, bool ok, int n0, int cols) {
+  uint32_t word = 0x7f7f7f7fu;
+  if (!ok) return word;
+  const uint8_t* s = e.keep_scale[which] + m * (e.ld_keep / KEEP_BLOCK) + n0 / KEEP_BLOCK;
+  if (COUNT > 1 && e.scale_vec && n0 + COUNT * KEEP_BLOCK <= cols) {
+    if constexpr (COUNT == 4) word = *reinterpret_cast<const uint32_t*>(s);
+    else if constexpr (COUNT == 2) word = *reinterpret_cast<const uint16_t*>(s);
+  } else {
+    word = 0;
+#pragma unroll
+    for (int c = 0; c < COUNT; ++c) word |= (n0 + c * KEEP_BLOCK < cols ? (uint32_t)s[c] : 127u) << (8 * c);
+  }
+  return word;
 }
+
 // Half a block (values 8 q to 8 q + 7 of the lane, columns 16 q to 16 q + 15 of the
 // block): what an epilogue holds beside a tile's results and the next tile's
 // first fragments.
@@ -248,13 +278,10 @@ __device__ __forceinline__ void store_half(uint16_t* row, bool ok, int n0, int h
 struct KeptF8 {
   u32x4 w;
   uint32_t byte;
-  __device__ __forceinline__ void load(const FfnArgs& e, int which, int m, bool ok, int nb, int half, int cols) {
+  __device__ __forceinline__ void load(const FfnArgs& e, int which, int m, bool ok, int nb, int half, int cols, uint32_t scale) {
     w = u32x4{0, 0, 0, 0};
-    byte = 127;
-    if (ok && nb < cols) {
-      w = *reinterpret_cast<const u32x4*>((const uint8_t*)e.keep[which] + m * e.ld_keep + nb + 16 * half);
-      byte = e.keep_scale[which][m * (e.ld_keep / KEEP_BLOCK) + nb / KEEP_BLOCK];
-    }
+    byte = scale;
+    if (ok && nb < cols) w = *reinterpret_cast<const u32x4*>((const uint8_t*)e.keep[which] + m * e.ld_keep + nb + 16 * half);
   }
   __device__ __forceinline__ void swap() {
     const auto a = __builtin_amdgcn_permlane32_swap(w[0], w[1], false, false);
@@ -334,6 +361,7 @@ __device__ __forceinline__ void linear_epilogue(const ProductArgs& g, floatx16 (
   };
   Ahead next;
   if (early) next.load(residual_row(0), m0 + l32 < g.M, n0, half);
+  uint32_t scales[FM] = {};
   for_each<FN>([&](auto J) __attribute__((always_inline)) {
     const int nb = n0 + 32 * J.value;
     if (nb >= g.N) return;
@@ -355,7 +383,7 @@ __device__ __forceinline__ void linear_epilogue(const ProductArgs& g, floatx16 (
 #pragma unroll
         for (int v = 0; v < 16; ++v) z[v] += b[v];
       }
-      if (e.keep[0]) keep_block(e, 0, m, ok, nb, half, g.N, z);
+      if (e.keep[0]) scales[I.value] |= keep_block(e, 0, m, ok, nb, half, g.N, z) << (8 * J.value);
       if (e.act) {
         with_activation(e.act, [&](auto act) __attribute__((always_inline)) {
 #pragma unroll
@@ -377,6 +405,10 @@ __device__ __forceinline__ void linear_epilogue(const ProductArgs& g, floatx16 (
       store_rows(g.C, g.c_dt, g.ldc, m, ok, nb, half, g.N, g.vec, z);
     });
   });
+  if (e.keep[0] && e.keep_dt == 4) {
+#pragma unroll
+    for (int i = 0; i < FM; ++i) store_scales<FN>(e, 0, m0 + 32 * i + l32, m0 + 32 * i + l32 < g.M && half == 0, n0, g.N, scales[i]);
+  }
 }
 
 // C receives h: rows of ldc, zeros behind the columns.  Blocks j and j + FN / 2
@@ -395,6 +427,7 @@ __device__ __forceinline__ void gated_epilogue(const ProductArgs& g, floatx16 (&
     });
     return;
   }
+  uint32_t scales[FM][2] = {};
   for_each<FM * HF>([&](auto K) __attribute__((always_inline)) {
     constexpr int I = K.value / HF, J = K.value % HF;
     const int m = m0 + 32 * I + l32, nb = n0 + 32 * J;
@@ -404,8 +437,8 @@ __device__ __forceinline__ void gated_epilogue(const ProductArgs& g, floatx16 (&
     floatx16 h = acc[I][J];
     const floatx16 up = acc[I][J + HF];
     if (e.keep[0]) {
-      keep_block(e, 0, m, ok, nb, half, g.N, h);
-      keep_block(e, 1, m, ok, nb, half, g.N, up);
+      scales[I][0] |= keep_block(e, 0, m, ok, nb, half, g.N, h) << (8 * J);
+      scales[I][1] |= keep_block(e, 1, m, ok, nb, half, g.N, up) << (8 * J);
     }
     with_activation(e.act, [&](auto act) __attribute__((always_inline)) {
 #pragma unroll
@@ -419,6 +452,11 @@ __device__ __forceinline__ void gated_epilogue(const ProductArgs& g, floatx16 (&
     if (g.c_dt == 0) store_block<true>(reinterpret_cast<float*>(g.C) + m * g.ldc, ok, nb, half, 0, 1, h);
     else store_block<true>(reinterpret_cast<uint16_t*>(g.C) + m * g.ldc, ok, nb, half, 0, 1, h);
   });
+  if (e.keep[0] && e.keep_dt == 4) {
+#pragma unroll
+    for (int i = 0; i < FM; ++i)  // the gate's from one half of the wave, the up projection's from the other
+      store_scales<HF>(e, half, m0 + 32 * i + l32, m0 + 32 * i + l32 < g.M, n0, g.N, half ? scales[i][1] : scales[i][0]);
+  }
 }
 
 // ES: bytes of an element of dg, du (rows of ldc) and h (rows of ldc / 2), zeros behind the columns
@@ -430,13 +468,20 @@ __device__ __forceinline__ void gated_grad_epilogue(const ProductArgs& g, floatx
   const bool f8 = e.keep_dt == 4;
   // what was kept of the next block is loaded before this one is computed
   const bool early = ES == 2 && !f8 && e.keep_vec && n0 + 32 * FN <= g.N;
+  uint32_t scales[FM][2];
+  if (f8) {
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+      for (int p = 0; p < 2; ++p) scales[i][p] = load_scales<FN>(e, p, m0 + 32 * i + l32, m0 + 32 * i + l32 < g.M, n0, g.N);
+  }
   KeptF8 next8[2];
   Ahead next[2];
   const auto load = [&](int i, int j) __attribute__((always_inline)) {
     const int m = m0 + 32 * i + l32, nb = n0 + 32 * j;
 #pragma unroll
     for (int p = 0; p < 2; ++p) {
-      if (f8) next8[p].load(e, p, m, m < g.M, nb, half, g.N);
+      if (f8) next8[p].load(e, p, m, m < g.M, nb, half, g.N, scales[i][p] >> (8 * j) & 255);
       else if (early) next[p].load(reinterpret_cast<const uint16_t*>(e.keep[p]) + m * e.ld_keep, m < g.M, nb, half);
     }
   };

@@ -34,7 +34,7 @@ struct FfnArgs {
   float* part;            // GATED with ranges of k: partial results [range][M][2 P], P: N rounded up to 4
   void* du;               // GATED_GRAD: rows of ldc (C receives dg)
   void* h;                // GATED_GRAD: rows of ldc / 2
-  int bias_bf16, bias_vec, act, keep_dt, keep_vec, residual_vec;  // keep_dt: 0 float32, 2 bfloat16, 4 e4m3
+  int bias_bf16, bias_vec, act, keep_dt, keep_vec, scale_vec, residual_vec;  // keep_dt: 0 float32, 2 bfloat16, 4 e4m3; scale_vec: rows of scales start on 4 bytes
 };
 
 struct ProductArgs {
