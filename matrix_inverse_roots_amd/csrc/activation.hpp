@@ -6,9 +6,9 @@
 //              (1 + tanh(y)) / 2 = sigma(2 y)
 //   silu       z sigma(z)
 // sigma(p) = 1 / (1 + 2^(-p log2 e)): one exp2 and one reciprocal instruction,
-// off by some 2^-22 and |p| 2^-24 relative.  Phi(-|z|) = t P(t) e^(-z^2/2) / 2 with
+// off by some 2^-22 and |p| 2^-24 relative.  Phi(-|z|) = t P(t) e^(-z^2/2) with
 // t = 1 / (1 + 0.45 |z| / sqrt 2) and P of degree 9, fitted (least squares
-// reweighted towards the largest relative error) to erfc(x) e^(x^2) / t over
+// reweighted towards the largest relative error) to erfc(x) e^(x^2) / (2 t) over
 // all x >= 0: 3.2e-8 relative in exact arithmetic, 3.6e-7 at most as it is
 // evaluated here.  Small probabilities keep their digits, which 1 + erf would
 // lose, and the exponential serves the derivative too.
@@ -40,17 +40,17 @@ struct ActGelu {
   __device__ __forceinline__ float cdf(float z, float& bell) const {
     const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.3181980515339464f, fabsf(z), 1.f));
     bell = __builtin_amdgcn_exp2f(z * z * -0.7213475204444817f);
-    float p = -0.0413922855f;
-    p = __builtin_fmaf(p, t, 0.1906930092f);
-    p = __builtin_fmaf(p, t, -0.3005917998f);
-    p = __builtin_fmaf(p, t, 0.1424101846f);
-    p = __builtin_fmaf(p, t, -0.0223633167f);
-    p = __builtin_fmaf(p, t, 0.1199523115f);
-    p = __builtin_fmaf(p, t, 0.1752517454f);
-    p = __builtin_fmaf(p, t, 0.2282716835f);
-    p = __builtin_fmaf(p, t, 0.2538831608f);
-    p = __builtin_fmaf(p, t, 0.2538853208f);
-    const float q = 0.5f * (p * t) * bell;
+    float p = -0.02069614275f;
+    p = __builtin_fmaf(p, t, 0.0953465046f);
+    p = __builtin_fmaf(p, t, -0.1502958999f);
+    p = __builtin_fmaf(p, t, 0.0712050923f);
+    p = __builtin_fmaf(p, t, -0.01118165835f);
+    p = __builtin_fmaf(p, t, 0.05997615575f);
+    p = __builtin_fmaf(p, t, 0.0876258727f);
+    p = __builtin_fmaf(p, t, 0.11413584175f);
+    p = __builtin_fmaf(p, t, 0.1269415804f);
+    p = __builtin_fmaf(p, t, 0.1269426604f);
+    const float q = p * t * bell;
     return z < 0.f ? q : 1.f - q;
   }
   __device__ __forceinline__ float value(float z) const {

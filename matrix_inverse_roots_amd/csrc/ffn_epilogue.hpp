@@ -147,11 +147,13 @@ __device__ __forceinline__ void store_rows(void* p, int dt, int64_t ld, int m, b
 __device__ __forceinline__ float scale_value(uint32_t byte) { return bits_float(byte ? byte << 23 : 0x00400000u); }
 
 // Largest finite magnitude's bits among 16 values of this lane and of its
-// partner in the other half of the wave.
+// partner in the other half of the wave.  The maximum passes over NaN by
+// itself; a wave that meets an infinity filters.
 __device__ __forceinline__ uint32_t block_max(const floatx16& x) {
-  uint32_t a = 0;
+  float f = 0.f;
 #pragma unroll
-  for (int v = 0; v < 16; ++v) a = max(a, float_bits(x[v]) & 0x7fffffffu);
+  for (int v = 0; v < 16; ++v) f = fmaxf(f, fabsf(x[v]));
+  uint32_t a = float_bits(f);
   if (__any(a >= 0x7f800000u)) {
     a = 0;
 #pragma unroll
