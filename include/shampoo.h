@@ -588,7 +588,8 @@ shampoo_status shampoo_linear_xent(const shampoo_xent_args* args, hipStream_t st
  * stored.  Weights are in dt, or F32 beside BF16 (rounded to bfloat16 for the
  * products).  Between two products h, dz, dg and du are rounded to dt (h of at
  * most 4 rows stays float32).  Formulas are followed where values are not
- * finite: silu and gelu of minus infinity are NaN.
+ * finite: silu and gelu of minus infinity are NaN, and a row of x with a NaN
+ * reaches the weights' gradients even where its row of dy is zero.
  *
  * Kept.  What a forward call keeps for the backward one, z or g and u, is
  * written by the products' epilogues and is one of
@@ -607,7 +608,7 @@ shampoo_status shampoo_linear_xent(const shampoo_xent_args* args, hipStream_t st
  *
  * Rows may be any stride apart; rows that do not start on 16 bytes, and row
  * lengths that are no multiple of 16 bytes, cost a copy in the workspace.  M, T
- * at most 2^29, other sizes at most 2^18, row strides at most 2^20.  An empty batch
+ * below 2^29, other sizes at most 2^18, row strides at most 2^20.  An empty batch
  * leaves weight gradients zero (or unchanged where accumulated).  What a call
  * writes may overlap nothing else of it (E_INVALID), but y may be residual
  * itself.  Results do not depend on the stream, the workspace's contents or the

@@ -13,6 +13,17 @@
 // the least power of two that keeps the block's largest finite magnitude
 // within 448 (e = 0 for zeros), and a value has one rounding.
 //
+// What bounds them: one workgroup holds a unit's LDS, so a tile's epilogue and
+// products take turns, and every instruction and byte here shows.  8191 x 4096
+// x 1024 with gelu and z in 8 bits: 108 us, of which 26% of the cycles are the
+// matrix cores', 35% this arithmetic (some 35 instructions an element), the rest
+// waits; without activation and kept values the product takes 81.  8192 x 10240 x
+// 4096 with the gated block's gradients from 8 bits: 810-830 us against 533 for
+// the product alone, for 168 MB read, 503 MB written and the arithmetic.
+// Blocks are done one after another (apart()), what was kept of the next one
+// loaded ahead: all at once they spilled up to 300 registers, which cost the
+// gated block's gradients 8%.
+//
 // Layout of a block (see product_core.hpp): lane l holds row l % 32 and, in
 // value v, column 8 (v / 4) + 4 (l / 32) + v % 4.
 #pragma once
