@@ -1008,6 +1008,8 @@ def shampoo_gated_ffn(x, w_gate, w_up, w_down, y=None, activation="silu", residu
     the types of ``shampoo_linear``.  keep: a pair that receives x w_gate^T and
     x w_up^T for ``shampoo_gated_ffn_grad``, each as in ``shampoo_linear``
     (tensors of x's type with one row stride, or values and scales in 8 bits)."""
+    if keep is not None and len(keep) != 2:
+        raise ValueError("keep must be a pair")
     kept = () if keep is None else _parts(keep[0]) + _parts(keep[1])
     dev = _on_device(x, w_gate, w_up, w_down, y, residual, ws, *kept)
     if y is None:
@@ -1060,6 +1062,8 @@ def shampoo_gated_ffn_grad(dy, x, w_gate, w_up, w_down, kept, dx=None, dw_gate=N
     accumulate=True adds to them).  x may be in 8 bits as in
     ``shampoo_linear_grad``.  The residual's gradient is dy.  Returns
     (dx, dw_gate, dw_up, dw_down)."""
+    if kept is None or len(kept) != 2:
+        raise ValueError("kept must be the pair that the forward pass kept")
     dev = _on_device(dy, w_gate, w_up, w_down, dx, dw_gate, dw_up, dw_down, ws, *_parts(x), *_parts(kept[0]), *_parts(kept[1]))
     args = _gated_grad_args(dy, x, w_gate, w_up, w_down, kept, dx, dw_gate, dw_up, dw_down, activation, accumulate)
     _with_workspace("shampoo_gated_ffn_grad", args, ws, dev, stream)

@@ -124,15 +124,19 @@ hipError_t launch_product(const ProductArgs& g, bool large, int64_t batch, hipSt
   return launch_tiles<E, 1, 4, 4, 1, 2, 2, AS, BS, EPI, FA, FB>(g, batch, st);
 }
 
-// Tiles of the feed-forward layers' products.
+// Tiles of the feed-forward layers' products: 64 x 64 (float32 only), 128 x 128,
+// 256 x 128 (bfloat16 only; three buffers, since its stages are half as long as a large
+// tile's and loads take as long), 256 x 256.
 enum Tile { TILE_64 = 1, TILE_128, TILE_MEDIUM, TILE_LARGE };
 
 template <Elem E, bool AS, bool BS, Epi EPI>
 hipError_t launch_layer(const ProductArgs& g, const Shape& s, int64_t batch, hipStream_t st) {
-  if constexpr (E == Elem::F32 && EPI != Epi::GATED) {
+  if constexpr (E == Elem::F32 && EPI != Epi::GATED) {  // GATED needs two fragments of columns
     if (s.tile == TILE_64) return launch_tiles<E, 1, 1, 2, 2, 3, 3, AS, BS, EPI, 0, 0>(g, batch, st);
   }
-  if (s.tile == TILE_MEDIUM) return launch_tiles<E, 2, 2, 4, 2, 3, 1, AS, BS, EPI, 0, 0>(g, batch, st);
+  if constexpr (E == Elem::BF16) {
+    if (s.tile == TILE_MEDIUM) return launch_tiles<E, 2, 2, 4, 2, 3, 1, AS, BS, EPI, 0, 0>(g, batch, st);
+  }
   return launch_product<E, AS, BS, EPI>(g, s.tile == TILE_LARGE, batch, st);
 }
 

@@ -7,7 +7,7 @@ import pytest
 
 import ffn_reference as ref
 from helpers import log
-from test_gpu_ffn import check_kept, gen_of, nans, normal
+from test_gpu_ffn import check_kept, gen_of, nans, normal, room
 
 pytestmark = pytest.mark.gpu
 
@@ -130,6 +130,68 @@ def test_accumulated_gradients(mir, T, d, f, gdt):
         v, err = want[name]
         v = v + g[name].double()
         ref.check(got, v, err + 2 * ref.U * (v.abs() + g[name].double().abs()) + ref.HALF[gdt] * (v.abs() + err), name)
+
+
+# (rows, inner, columns): every tile in whole and ragged sizes.  bfloat16: 256 x 128
+# from 257 tiles of 128 x 128 on, 256 x 256 where they fill the chip and the inner size is long or
+# the epilogue a plain store; 128 x 128 two to a unit for few rows of very many columns.
+# float32: 64 x 64, 128 x 128, 256 x 256.
+TILES = [(2100, 40, 2100), (4090, 72, 4000), (4000, 4200, 4090), (100, 64, 70000), (2048, 136, 2048), (600, 1000, 900)]
+
+
+@pytest.mark.parametrize("dt", ["float32", "bfloat16"])
+@pytest.mark.parametrize("M,K,N", TILES)
+def test_every_tile(mir, M, K, N, dt):
+    """Forward and backward of a layer at the sizes of each tile: all in the
+    epilogue, then nothing in it."""
+    import torch
+    dt = getattr(torch, dt)
+    half = ref.HALF[dt]
+    gen = gen_of(M, K, N, 20)
+    x, w, r = normal(gen, M, K, 1.0, dt, 0.3), normal(gen, N, K, K ** -0.5, dt), normal(gen, M, N, 1.0, dt)
+    bias = torch.randn(N, generator=gen, device="cuda")
+    kept = mir.shampoo_kept_empty(M, N, "e4m3", "cuda")
+    y = mir.shampoo_linear(x, w, bias=bias, activation="gelu", residual=r, keep=kept)
+    z, dz, want, err = ref.linear(x, w, bias, "gelu", r)
+    ref.check(y, want, err + half * (want.abs() + err), "y")
+    check_kept(kept, z, dz, dt, "kept")
+    del z, dz, want, err
+    y = mir.shampoo_linear(x, w)
+    _, _, want, err = ref.linear(x, w, None, "none", None)
+    ref.check(y, want, err + half * (want.abs() + err), "plain y")
+    del y, want, err
+    out = dict(dx=nans(M, K, dtype=dt), dw=nans(N, K, dtype=torch.float32), dbias=nans(N, dtype=torch.float32))
+    mir.shampoo_linear_grad(r, x, w, kept=kept, activation="gelu", **out)
+    want = ref.linear_grad(r, x, w, ref.widen(kept, N), "gelu", half if dt != torch.float32 else 0)
+    for name, got in out.items():
+        v, e = want[name]
+        ref.check(got, v, e + ref.HALF[got.dtype] * (v.abs() + e), name)
+
+
+@pytest.mark.parametrize("dt", ["float32", "bfloat16"])
+@pytest.mark.parametrize("keep", ["dtype", "e4m3"])
+@pytest.mark.parametrize("T,d,f", [(2100, 40, 2100), (4090, 72, 4000), (4000, 4200, 2100), (100, 64, 35000), (1030, 2056, 1100)])
+def test_every_tile_of_the_gated_block(mir, T, d, f, keep, dt):
+    import torch
+    dt = getattr(torch, dt)
+    half = ref.HALF[dt]
+    gen = gen_of(T, d, f, 21)
+    x, dy = normal(gen, T, d, 1.0, dt, 0.3), normal(gen, T, d, 1.0, dt)
+    wg, wu, wd = normal(gen, f, d, d ** -0.5, dt), normal(gen, f, d, d ** -0.5, dt), normal(gen, d, f, f ** -0.5, dt)
+    pair = [room(mir, T, f, keep, dt) for _ in range(2)]
+    y = mir.shampoo_gated_ffn(x, wg, wu, wd, residual=dy, keep=pair)
+    (g, eg), (u, eu), (want, err) = ref.gated(x, wg, wu, wd, "silu", dy, half)
+    ref.check(y, want, err + half * (want.abs() + err), "y")
+    check_kept(pair[0], g, eg, dt, "gate")
+    check_kept(pair[1], u, eu, dt, "up")
+    del g, eg, u, eu, want, err
+    both = nans(2, f, d, dtype=dt)      # the up projection's gradient below the gate's in memory
+    out = dict(dx=nans(T, d, dtype=dt), dw_gate=both[1], dw_up=both[0], dw_down=nans(d, f, dtype=dt))
+    mir.shampoo_gated_ffn_grad(dy, x, wg, wu, wd, pair, **out)
+    want = ref.gated_grad(dy, x, wg, wu, wd, ref.widen(pair[0], f), ref.widen(pair[1], f), "silu", half)
+    for name, got in out.items():
+        v, e = want[name]
+        ref.check(got, v, e + half * (v.abs() + e), name)
 
 
 def test_each_gradient_alone_is_the_same(mir):
