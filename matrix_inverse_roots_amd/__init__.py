@@ -855,9 +855,10 @@ def _layer_types(x, act):
     return dt, codes[dt], (dt,) if codes[dt] == F32 else (dt, _torch().float32), kind
 
 
-def _with_workspace(name, args, ws, dev, stream):
-    """Runs lib.<name> on ``args``, with a workspace of its own unless one is given."""
-    if ws is None:
+def _with_workspace(name, args, ws, dev, stream, none=False):
+    """Runs lib.<name> on ``args``, with a workspace of its own unless one is
+    given (``none``: it is known to need none)."""
+    if ws is None and not none:
         need = ctypes.c_size_t(0)
         _check(getattr(lib, name + "_workspace")(ctypes.byref(args), ctypes.byref(need)))
         if need.value:
@@ -907,9 +908,12 @@ def shampoo_linear(x, w, y=None, bias=None, activation=None, residual=None, keep
     ``shampoo_linear_grad``: a tensor [M, N] of x's type, or values and scales
     in 8 bits (``shampoo_kept_empty(M, N, "e4m3", device)``)."""
     dev = _on_device(x, w, y, bias, residual, ws, *_parts(keep))
-    if y is None:
+    if y is None and x.dim() == 2 and w.dim() == 2:
         y = _empty((x.shape[0], w.shape[0]), x.dtype, dev, stream)
-    _with_workspace("shampoo_linear", _linear_args(x, w, y, bias, activation, residual, keep), ws, dev, stream)
+    args = _linear_args(x, w, y, bias, activation, residual, keep)
+    # up to four rows take no workspace, unless they keep 8 bits
+    none = x.shape[0] <= 4 and (keep is None or len(_parts(keep)) == 1)
+    _with_workspace("shampoo_linear", args, ws, dev, stream, none)
     return y
 
 
