@@ -134,14 +134,21 @@ Shape plan_layer(int64_t batch, int64_t M, int64_t N, int64_t K, int es, bool ma
   s.tile = s.large ? TILE_LARGE : TILE_128;
   auto tiles = [&](int64_t m, int64_t n) { return batch * ((M + m - 1) / m) * ((N + n - 1) / n); };
   if (es == 4) {
-    // ranges of k: some 6 us more, for the launch that sums them
-    const double now = s.large ? (double)((tiles(256, 256) + CUS - 1) / CUS)
-                               : (double)((tiles(128, 128) * s.splits + CUS - 1) / CUS) * 0.26 / s.splits + (s.splits > 1 ? 30.0 / K : 0.0);
-    if (!dual && (double)((tiles(64, 64) + CUS - 1) / CUS) * 0.073 < now) {
+    // a range of k costs some 6 us, for the launch that sums them, and its reading
+    auto ranges = [&](int64_t n, double tile, int r) {
+      return (double)((n * r + CUS - 1) / CUS) * tile / r + (r > 1 ? (30.0 + 1.2 * r) / K : 0.0);
+    };
+    double now = s.large ? (double)((tiles(256, 256) + CUS - 1) / CUS) : ranges(tiles(128, 128), 0.26, s.splits);
+    for (int r = 1; !dual && r <= (may_split ? 16 : 1) && (r == 1 || r <= s.nst / 4); ++r) {
+      const int stages = (s.nst + r - 1) / r;
+      if ((s.nst + stages - 1) / stages != r) continue;
+      const double c = ranges(tiles(64, 64), 0.073, r);
+      if (c >= now) continue;
+      now = c;
       s.large = false;
       s.tile = TILE_64;
-      s.splits = 1;
-      s.split_stages = s.nst;
+      s.splits = r;
+      s.split_stages = stages;
     }
     return s;
   }
@@ -179,6 +186,20 @@ struct Layer {
   float* part;
 };
 
+// Partial results in rows that start on 16 bytes.
+size_t padded_bytes(const Shape& s, int64_t batch, int64_t M, int64_t N) { return partial_bytes(s, batch, M, up(N, 4)); }
+void pad_partials(ProductArgs& g, const Shape& s, int64_t batch) {
+  if (s.splits == 1) return;
+  g.ldc = up(g.N, 4);
+  g.strideC = g.M * g.ldc;
+  g.split_stride = batch * g.strideC;
+  g.vec = 1;
+}
+hipError_t finish_layer(const FinishArgs& f, hipStream_t st) {
+  hipLaunchKernelGGL(ffn_finish_kernel<false>, dim3((unsigned)((up(f.N, 32) + 1023) / 1024), (unsigned)std::min(f.M, 65535)), dim3(256), 0, st, f);
+  return hipGetLastError();
+}
+
 template <Elem E> hipError_t run_layer(const Layer& l, hipStream_t st) {
   ProductArgs g{};
   g.A = l.x; g.B = l.w;
@@ -186,19 +207,12 @@ template <Elem E> hipError_t run_layer(const Layer& l, hipStream_t st) {
   g.M = (int)l.M; g.N = (int)l.N; g.K = (int)l.K;
   set_shape(g, l.shape);
   g.ffn = l.ffn;
-  const Out o{l.y, l.ldy, 0, out_code(l.y_dt), rows_vec(l.y, l.ldy, 0, l.y_dt), 0.f};
+  const Out o{l.y, l.ldy, 0, out_code(l.y_dt), 1, 0.f};
   point_output(g, l.shape, o, l.part, 1);
-  if (l.shape.splits > 1) {  // rows that start on 16 bytes
-    g.ldc = up(l.N, 4);
-    g.split_stride = l.M * g.ldc;
-    g.vec = 1;
-  }
   if (l.shape.splits == 1) return launch_layer<E, false, false, Epi::LINEAR>(g, l.shape, 1, st);
+  pad_partials(g, l.shape, 1);
   HIP_TRY_ERR((launch_layer<E, false, false, Epi::STORE>(g, l.shape, 1, st)));
-  FinishArgs f{l.part, g.split_stride, l.shape.splits, (int)l.M, (int)l.N, 0, l.y, l.ldy, out_code(l.y_dt), l.ffn};
-  hipLaunchKernelGGL(ffn_finish_kernel<false>, dim3((unsigned)((up(l.N, 32) + 1023) / 1024), (unsigned)std::min<int64_t>(l.M, 65535)), dim3(256), 0,
-                     st, f);
-  return hipGetLastError();
+  return finish_layer({l.part, g.split_stride, l.shape.splits, (int)l.M, (int)l.N, 0, l.y, l.ldy, out_code(l.y_dt), l.ffn}, st);
 }
 
 // Waves that share a row's k in ffn_rows_kernel: one for each 512 elements.
@@ -242,7 +256,7 @@ shampoo_status linear_layout(const shampoo_linear_args* a, LinearLayout* L) {
     L->x = operand(c, a->x, a->M, a->K, a->ld_x, a->dt, a->dt);
     L->w = operand(c, a->w, a->N, a->K, a->ld_w, a->w_dt, a->dt);
     L->shape = plan_layer(1, a->M, a->N, a->K, (int)size_of(a->dt), true, a->bias || a->residual || a->keep || a->activation ? 150 : 0);
-    L->part = c.take(partial_bytes(L->shape, 1, a->M, up(a->N, 4)));
+    L->part = c.take(padded_bytes(L->shape, 1, a->M, a->N));
   }
   L->total = c.at;
   return SHAMPOO_OK;
@@ -291,21 +305,31 @@ shampoo_status linear_grad_layout(const shampoo_linear_grad_args* a, LinearGradL
   L->dz = c.take(L->store ? (size_t)a->M * L->ld_dz * es : 0);
   L->sums = c.take(a->dbias ? (size_t)((a->M + GRAD_ROWS - 1) / GRAD_ROWS) * a->N * 4 : 0);
   size_t part = 0;
-  if (a->dx) part = std::max(part, partial_bytes(L->dx, 1, a->M, a->K));
-  if (a->dw) part = std::max(part, partial_bytes(L->dw, 1, a->N, a->K));
+  if (a->dx) part = std::max(part, padded_bytes(L->dx, 1, a->M, a->K));
+  if (a->dw) part = std::max(part, padded_bytes(L->dw, 1, a->N, a->K));
   L->part = c.take(part);
   L->total = c.at;
   return SHAMPOO_OK;
 }
 
-// C (+)= A B of operands that start on 16 bytes; one launch, and one that sums
-// ranges of k.
+// C (+)= A B of operands that start on 16 bytes; one launch, and, over ranges
+// of k, one for each matrix that sums them (where C is added to, it is its own
+// residual).
 template <Elem E, bool AS, bool BS, Epi EPI = Epi::STORE>
 hipError_t run_product(ProductArgs& g, const Shape& s, const Out& o, float* part, int64_t batch, hipStream_t st) {
   set_shape(g, s);
   point_output(g, s, o, part, batch);
+  pad_partials(g, s, batch);
   HIP_TRY_ERR((launch_layer<E, AS, BS, EPI>(g, s, batch, st)));
-  return finish_split(g, s, o, part, batch, st);
+  if (s.splits == 1) return hipSuccess;
+  for (int64_t b = 0; b < batch; ++b) {
+    void* C = (unsigned char*)o.C + b * o.strideC * (o.c_dt == 0 ? 4 : 2);
+    FinishArgs f{part + b * g.strideC, g.split_stride, s.splits, g.M, g.N, 0, C, o.ldc, o.c_dt, {}};
+    f.ffn.residual = o.beta != 0.f ? C : nullptr;
+    f.ffn.ld_residual = o.ldc;
+    HIP_TRY_ERR(finish_layer(f, st));
+  }
+  return hipSuccess;
 }
 // zeros, or the unchanged accumulated gradient, of an empty batch
 hipError_t no_gradient(void* p, int64_t ld, int dt, int accumulate, int64_t rows, int64_t cols, hipStream_t st) {
@@ -343,7 +367,7 @@ template <Elem E, typename T> hipError_t run_linear_grad(const shampoo_linear_gr
     g.A = dz; g.B = w;
     g.lda = L.ld_dz; g.ldb = L.w.ld;
     g.M = (int)a->M; g.N = (int)a->K; g.K = (int)a->N;
-    const Out o{a->dx, a->ld_dx, 0, out_code(a->dt), rows_vec(a->dx, a->ld_dx, 0, a->dt), 0.f};
+    const Out o{a->dx, a->ld_dx, 0, out_code(a->dt), 1, 0.f};
     HIP_TRY_ERR((run_product<E, false, true>(g, L.dx, o, part, 1, st)));
   }
   if (a->dw) {
@@ -352,7 +376,7 @@ template <Elem E, typename T> hipError_t run_linear_grad(const shampoo_linear_gr
     g.A = dz; g.B = x;
     g.lda = L.ld_dz; g.ldb = L.x.ld;
     g.M = (int)a->N; g.N = (int)a->K; g.K = (int)a->M;
-    const Out o{a->dw, a->ld_dw, 0, out_code(a->dw_dt), rows_vec(a->dw, a->ld_dw, 0, a->dw_dt), a->accumulate ? 1.f : 0.f};
+    const Out o{a->dw, a->ld_dw, 0, out_code(a->dw_dt), 1, a->accumulate ? 1.f : 0.f};
     HIP_TRY_ERR((run_product<E, true, true>(g, L.dw, o, part, 1, st)));
   }
   return hipSuccess;
@@ -409,7 +433,7 @@ shampoo_status gated_layout(const shampoo_gated_ffn_args* a, GatedLayout* L) {
   L->in = plan_layer(1, a->T, 2 * a->f, a->d, es, true, 0, true);
   L->out = plan_layer(1, a->T, a->d, a->f, es, true, a->residual ? 150 : 0);
   L->h = c.take((size_t)a->T * L->ldh * es);
-  L->part = c.take(std::max(partial_bytes(L->in, 1, a->T, 2 * up(a->f, 4)), partial_bytes(L->out, 1, a->T, up(a->d, 4))));
+  L->part = c.take(std::max(partial_bytes(L->in, 1, a->T, 2 * up(a->f, 4)), padded_bytes(L->out, 1, a->T, a->d)));
   L->total = c.at;
   return SHAMPOO_OK;
 }
@@ -422,7 +446,6 @@ FfnArgs gated_kept(void* gate, void* gate_scale, void* up_, void* up_scale, int6
   e.keep_scale[1] = (uint8_t*)up_scale;
   e.ld_keep = dt == SHAMPOO_E4M3 ? up(f, KEEP_BLOCK) : ld;
   e.keep_dt = kept_code(dt);
-  e.keep_vec = rows16(gate, ld, dt) && rows16(up_, ld, dt);
   e.scale_vec = up(f, KEEP_BLOCK) % (4 * KEEP_BLOCK) == 0 && aligned(gate_scale, 4) && aligned(up_scale, 4);
   e.act = act;
   return e;
@@ -456,7 +479,6 @@ template <Elem E> hipError_t run_gated(const shampoo_gated_ffn_args* a, const Ga
   FfnArgs e{};
   e.residual = a->residual;
   e.ld_residual = a->ld_residual;
-  e.residual_vec = rows16(a->residual, a->ld_residual, a->y_dt);
   return run_layer<E>({g.C, wd, L.ldh, L.down.ld, a->T, a->d, a->f, a->y, a->ld_y, a->y_dt, e, L.out, part}, st);
 }
 
@@ -522,9 +544,9 @@ shampoo_status gated_grad_layout(const shampoo_gated_ffn_grad_args* a, GatedGrad
   L->D = c.take((size_t)a->T * 2 * L->fp * es);
   L->h = c.take((size_t)a->T * L->fp * es);
   size_t part = 0;
-  if (a->dx) part = std::max(part, partial_bytes(L->dx, 1, a->T, a->d));
-  if (a->dw_down) part = std::max(part, partial_bytes(L->dwd, 1, a->d, a->f));
-  if (a->dw_gate || a->dw_up) part = std::max(part, partial_bytes(L->dwp, L->pair ? 2 : 1, a->f, a->d));
+  if (a->dx) part = std::max(part, padded_bytes(L->dx, 1, a->T, a->d));
+  if (a->dw_down) part = std::max(part, padded_bytes(L->dwd, 1, a->d, a->f));
+  if (a->dw_gate || a->dw_up) part = std::max(part, padded_bytes(L->dwp, L->pair ? 2 : 1, a->f, a->d));
   L->part = c.take(part);
   L->total = c.at;
   return SHAMPOO_OK;
@@ -566,7 +588,7 @@ template <Elem E> hipError_t run_gated_grad(const shampoo_gated_ffn_grad_args* a
     g.M = (int)a->T; g.N = (int)a->d; g.K = (int)(2 * L.fp);
     g.kswitch = (int)(L.fp * es / 128);
     g.kpart = (int)a->f;
-    const Out o{a->dx, a->ld_dx, 0, out_code(a->dt), rows_vec(a->dx, a->ld_dx, 0, a->dt), 0.f};
+    const Out o{a->dx, a->ld_dx, 0, out_code(a->dt), 1, 0.f};
     HIP_TRY_ERR((run_product<E, false, true, Epi::STORE2>(g, L.dx, o, part, 1, st)));
   }
   const float beta = a->accumulate ? 1.f : 0.f;
@@ -583,7 +605,7 @@ template <Elem E> hipError_t run_gated_grad(const shampoo_gated_ffn_grad_args* a
       g.strideA = L.fp;
       g.M = (int)a->f; g.N = (int)a->d; g.K = (int)a->T;
       const int64_t apart = L.pair ? ((const char*)a->dw_up - (const char*)a->dw_gate) / (int64_t)size_of(a->dw_dt) : 0;
-      const Out o{C, ldc, apart, c_dt, rows_vec(C, ldc, apart, a->dw_dt), beta};
+      const Out o{C, ldc, apart, c_dt, 1, beta};
       HIP_TRY_ERR((run_product<E, true, true>(g, L.dwp, o, part, L.pair ? 2 : 1, st)));
     }
   }
@@ -592,7 +614,7 @@ template <Elem E> hipError_t run_gated_grad(const shampoo_gated_ffn_grad_args* a
     g.A = dy; g.B = h;
     g.lda = L.dy.ld; g.ldb = L.fp;
     g.M = (int)a->d; g.N = (int)a->f; g.K = (int)a->T;
-    const Out o{a->dw_down, a->ld_dw_down, 0, c_dt, rows_vec(a->dw_down, a->ld_dw_down, 0, a->dw_dt), beta};
+    const Out o{a->dw_down, a->ld_dw_down, 0, c_dt, 1, beta};
     HIP_TRY_ERR((run_product<E, true, true>(g, L.dwd, o, part, 1, st)));
   }
   return hipSuccess;
@@ -689,15 +711,12 @@ shampoo_status shampoo_linear(const shampoo_linear_args* a, hipStream_t stream) 
   FfnArgs e{};
   e.bias = a->bias;
   e.bias_bf16 = a->bias_dt == SHAMPOO_BF16;
-  e.bias_vec = aligned(a->bias, 16);
   e.residual = a->residual;
   e.ld_residual = a->ld_residual;
-  e.residual_vec = rows16(a->residual, a->ld_residual, a->y_dt);
   e.keep[0] = a->keep;
   e.keep_scale[0] = (uint8_t*)a->keep_scale;
   e.ld_keep = a->keep_dt == SHAMPOO_E4M3 ? up(a->N, KEEP_BLOCK) : a->ld_keep;
   e.keep_dt = kept_code(a->keep_dt);
-  e.keep_vec = rows16(a->keep, a->ld_keep, a->keep_dt);
   e.scale_vec = up(a->N, KEEP_BLOCK) % (4 * KEEP_BLOCK) == 0 && aligned(a->keep_scale, 4);
   e.act = a->activation;
   HIP_TRY(a->dt == SHAMPOO_F32 ? run_linear<Elem::F32>(a, L, e, stream) : run_linear<Elem::BF16>(a, L, e, stream));

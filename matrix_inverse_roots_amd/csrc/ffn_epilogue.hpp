@@ -59,14 +59,14 @@ template <int N, int I = 0, typename F> __device__ __forceinline__ void for_each
 __device__ __forceinline__ void apart() { asm volatile("" ::: "memory"); }
 
 // A 32 x 32 block from column nb on, of a row: `row` is where the lane's row
-// starts, `ok` whether it is one, `cols` where the rows end.  vec: rows start
-// on 16 bytes.
-__device__ __forceinline__ floatx16 load_block(const float* row, bool ok, int nb, int half, int cols, int vec) {
+// starts, `ok` whether it is one, `cols` where the rows end.  Accesses are 16
+// bytes wherever rows start; only a block over the rows' end goes by elements.
+__device__ __forceinline__ floatx16 load_block(const float* row, bool ok, int nb, int half, int cols) {
   floatx16 r;
-  if (vec && nb + 32 <= cols) {
+  if (nb + 32 <= cols) {
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      const floatx4 v = ok ? *reinterpret_cast<const floatx4*>(row + nb + 8 * q + 4 * half) : floatx4{0.f, 0.f, 0.f, 0.f};
+      const floatx4 v = ok ? *reinterpret_cast<const floatx4_any*>(row + nb + 8 * q + 4 * half) : floatx4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int e = 0; e < 4; ++e) r[4 * q + e] = v[e];
     }
@@ -79,17 +79,17 @@ __device__ __forceinline__ floatx16 load_block(const float* row, bool ok, int nb
   }
   return r;
 }
-__device__ __forceinline__ floatx16 load_block(const uint16_t* row, bool ok, int nb, int half, int cols, int vec) {
+__device__ __forceinline__ floatx16 load_block(const uint16_t* row, bool ok, int nb, int half, int cols) {
   floatx16 r;
   auto put = [&](int v, uint32_t two) {
     r[v] = bits_float(two << 16);
     r[v + 1] = bits_float(two & 0xffff0000u);
   };
-  if (vec && nb + 32 <= cols) {
+  if (nb + 32 <= cols) {
     // 8 columns a lane; the halves of the wave swap 4 of them
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
-      const u32x4 w = ok ? *reinterpret_cast<const u32x4*>(row + nb + 16 * q + 8 * half) : u32x4{0, 0, 0, 0};
+      const u32x4 w = ok ? *reinterpret_cast<const u32x4_any*>(row + nb + 16 * q + 8 * half) : u32x4{0, 0, 0, 0};
       const auto a = __builtin_amdgcn_permlane32_swap(w[0], w[2], false, false);
       const auto b = __builtin_amdgcn_permlane32_swap(w[1], w[3], false, false);
       put(8 * q, a[0]);
@@ -107,14 +107,14 @@ __device__ __forceinline__ floatx16 load_block(const uint16_t* row, bool ok, int
   return r;
 }
 
-// FULL: the whole block lies within rows that start on 16 bytes.
+// FULL: the whole block lies within the rows.
 template <bool FULL = false>
-__device__ __forceinline__ void store_block(float* row, bool ok, int nb, int half, int cols, int vec, const floatx16& x) {
+__device__ __forceinline__ void store_block(float* row, bool ok, int nb, int half, int cols, const floatx16& x) {
   if (!ok) return;
-  if (FULL || (vec && nb + 32 <= cols)) {
+  if (FULL || nb + 32 <= cols) {
 #pragma unroll
     for (int q = 0; q < 4; ++q)
-      *reinterpret_cast<floatx4*>(row + nb + 8 * q + 4 * half) = floatx4{x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]};
+      *reinterpret_cast<floatx4_any*>(row + nb + 8 * q + 4 * half) = floatx4{x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]};
   } else {
 #pragma unroll
     for (int v = 0; v < 16; ++v) {
@@ -124,16 +124,16 @@ __device__ __forceinline__ void store_block(float* row, bool ok, int nb, int hal
   }
 }
 template <bool FULL = false>
-__device__ __forceinline__ void store_block(uint16_t* row, bool ok, int nb, int half, int cols, int vec, const floatx16& x) {
+__device__ __forceinline__ void store_block(uint16_t* row, bool ok, int nb, int half, int cols, const floatx16& x) {
   uint32_t two[8];
 #pragma unroll
   for (int v = 0; v < 8; ++v) two[v] = pack_bf16(x[2 * v], x[2 * v + 1]);
-  if (FULL || (vec && nb + 32 <= cols)) {
+  if (FULL || nb + 32 <= cols) {
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
       const auto a = __builtin_amdgcn_permlane32_swap(two[4 * q], two[4 * q + 2], false, false);
       const auto b = __builtin_amdgcn_permlane32_swap(two[4 * q + 1], two[4 * q + 3], false, false);
-      if (ok) *reinterpret_cast<u32x4*>(row + nb + 16 * q + 8 * half) = u32x4{a[0], b[0], a[1], b[1]};
+      if (ok) *reinterpret_cast<u32x4_any*>(row + nb + 16 * q + 8 * half) = u32x4{a[0], b[0], a[1], b[1]};
     }
   } else if (ok) {
 #pragma unroll
@@ -145,13 +145,13 @@ __device__ __forceinline__ void store_block(uint16_t* row, bool ok, int nb, int 
 }
 
 // Rows `ld` elements apart, of float32 (dt 0) or bfloat16 (dt 2).
-__device__ __forceinline__ floatx16 load_rows(const void* p, int dt, int64_t ld, int m, bool ok, int nb, int half, int cols, int vec) {
-  if (dt == 0) return load_block(reinterpret_cast<const float*>(p) + m * ld, ok, nb, half, cols, vec);
-  return load_block(reinterpret_cast<const uint16_t*>(p) + m * ld, ok, nb, half, cols, vec);
+__device__ __forceinline__ floatx16 load_rows(const void* p, int dt, int64_t ld, int m, bool ok, int nb, int half, int cols) {
+  if (dt == 0) return load_block(reinterpret_cast<const float*>(p) + m * ld, ok, nb, half, cols);
+  return load_block(reinterpret_cast<const uint16_t*>(p) + m * ld, ok, nb, half, cols);
 }
-__device__ __forceinline__ void store_rows(void* p, int dt, int64_t ld, int m, bool ok, int nb, int half, int cols, int vec, const floatx16& x) {
-  if (dt == 0) store_block(reinterpret_cast<float*>(p) + m * ld, ok, nb, half, cols, vec, x);
-  else store_block(reinterpret_cast<uint16_t*>(p) + m * ld, ok, nb, half, cols, vec, x);
+__device__ __forceinline__ void store_rows(void* p, int dt, int64_t ld, int m, bool ok, int nb, int half, int cols, const floatx16& x) {
+  if (dt == 0) store_block(reinterpret_cast<float*>(p) + m * ld, ok, nb, half, cols, x);
+  else store_block(reinterpret_cast<uint16_t*>(p) + m * ld, ok, nb, half, cols, x);
 }
 
 // 2^(byte - 127), byte 0 included
@@ -195,7 +195,7 @@ __device__ __forceinline__ uint32_t keep_f8(uint8_t* q, int64_t ld, int m, bool 
 }
 __device__ __forceinline__ uint32_t keep_block(const FfnArgs& e, int which, int m, bool ok, int nb, int half, int cols, const floatx16& x) {
   if (e.keep_dt == 4) return keep_f8((uint8_t*)e.keep[which], e.ld_keep, m, ok, nb, half, cols, x);
-  store_rows(e.keep[which], e.keep_dt, e.ld_keep, m, ok, nb, half, cols, e.keep_vec, x);
+  store_rows(e.keep[which], e.keep_dt, e.ld_keep, m, ok, nb, half, cols, x);
   return 0;
 }
 
@@ -235,12 +235,12 @@ template <int COUNT> __device__ __forceinline__ uint32_t load_scales(const FfnAr
 struct Half {
   float v[8];
 };
-__device__ __forceinline__ Half load_half(const float* row, bool ok, int n0, int half, int cols, int vec) {
+__device__ __forceinline__ Half load_half(const float* row, bool ok, int n0, int half, int cols) {
   Half r;
-  if (vec && n0 + 16 <= cols) {
+  if (n0 + 16 <= cols) {
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
-      const floatx4 w = ok ? *reinterpret_cast<const floatx4*>(row + n0 + 8 * q + 4 * half) : floatx4{0.f, 0.f, 0.f, 0.f};
+      const floatx4 w = ok ? *reinterpret_cast<const floatx4_any*>(row + n0 + 8 * q + 4 * half) : floatx4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int e = 0; e < 4; ++e) r.v[4 * q + e] = w[e];
     }
@@ -253,10 +253,10 @@ __device__ __forceinline__ Half load_half(const float* row, bool ok, int n0, int
   }
   return r;
 }
-__device__ __forceinline__ Half load_half(const uint16_t* row, bool ok, int n0, int half, int cols, int vec) {
+__device__ __forceinline__ Half load_half(const uint16_t* row, bool ok, int n0, int half, int cols) {
   Half r;
-  if (vec && n0 + 16 <= cols) {
-    const u32x4 w = ok ? *reinterpret_cast<const u32x4*>(row + n0 + 8 * half) : u32x4{0, 0, 0, 0};
+  if (n0 + 16 <= cols) {
+    const u32x4 w = ok ? *reinterpret_cast<const u32x4_any*>(row + n0 + 8 * half) : u32x4{0, 0, 0, 0};
     const auto a = __builtin_amdgcn_permlane32_swap(w[0], w[2], false, false);
     const auto b = __builtin_amdgcn_permlane32_swap(w[1], w[3], false, false);
     const uint32_t two[4] = {a[0], b[0], a[1], b[1]};
@@ -317,13 +317,13 @@ struct KeptF8 {
   }
 };
 
-// Loads that a block's epilogue will need, issued a block ahead: bfloat16 rows
-// that start on 16 bytes, wholly inside.
+// Loads that a block's epilogue will need, issued a block ahead: blocks of
+// bfloat16 rows, wholly inside.
 struct Ahead {
   u32x4 w[2];
   __device__ __forceinline__ void load(const uint16_t* row, bool ok, int nb, int half) {
 #pragma unroll
-    for (int q = 0; q < 2; ++q) w[q] = ok ? *reinterpret_cast<const u32x4*>(row + nb + 16 * q + 8 * half) : u32x4{0, 0, 0, 0};
+    for (int q = 0; q < 2; ++q) w[q] = ok ? *reinterpret_cast<const u32x4_any*>(row + nb + 16 * q + 8 * half) : u32x4{0, 0, 0, 0};
   }
   __device__ __forceinline__ Half values(int q) const {
     const auto a = __builtin_amdgcn_permlane32_swap(w[q][0], w[q][2], false, false);
@@ -341,16 +341,16 @@ struct Ahead {
 
 __device__ __forceinline__ floatx16 bias_block(const FfnArgs& e, int nb, int half, int cols) {
   floatx16 b;
-  if (nb + 32 <= cols && e.bias_vec) {
+  if (nb + 32 <= cols) {
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       const int n = nb + 8 * q + 4 * half;
       if (e.bias_bf16) {
-        const u32x2 w = *reinterpret_cast<const u32x2*>(reinterpret_cast<const uint16_t*>(e.bias) + n);
+        const u32x2 w = *reinterpret_cast<const u32x2_any*>(reinterpret_cast<const uint16_t*>(e.bias) + n);
 #pragma unroll
         for (int c = 0; c < 4; ++c) b[4 * q + c] = bits_float(c & 1 ? w[c >> 1] & 0xffff0000u : w[c >> 1] << 16);
       } else {
-        const floatx4 w = *reinterpret_cast<const floatx4*>(reinterpret_cast<const float*>(e.bias) + n);
+        const floatx4 w = *reinterpret_cast<const floatx4_any*>(reinterpret_cast<const float*>(e.bias) + n);
 #pragma unroll
         for (int c = 0; c < 4; ++c) b[4 * q + c] = w[c];
       }
@@ -368,7 +368,7 @@ __device__ __forceinline__ floatx16 bias_block(const FfnArgs& e, int nb, int hal
 template <int FM, int FN>
 __device__ __forceinline__ void linear_epilogue(const ProductArgs& g, floatx16 (&acc)[FM][FN], int m0, int n0, int l32, int half) {
   const FfnArgs& e = g.ffn;
-  const bool early = e.residual && e.residual_vec && g.c_dt == 2 && n0 + 32 * FN <= g.N;
+  const bool early = e.residual && g.c_dt == 2 && n0 + 32 * FN <= g.N;
   const auto residual_row = [&](int i) __attribute__((always_inline)) {
     return reinterpret_cast<const uint16_t*>(e.residual) + (m0 + 32 * i + l32) * e.ld_residual;
   };
@@ -411,11 +411,11 @@ __device__ __forceinline__ void linear_epilogue(const ProductArgs& g, floatx16 (
           for (int v = 0; v < 8; ++v) z[8 * q + v] += r.v[v];
         }
       } else if (e.residual) {
-        const floatx16 r = load_rows(e.residual, g.c_dt, e.ld_residual, m, ok, nb, half, g.N, e.residual_vec);
+        const floatx16 r = load_rows(e.residual, g.c_dt, e.ld_residual, m, ok, nb, half, g.N);
 #pragma unroll
         for (int v = 0; v < 16; ++v) z[v] += r[v];
       }
-      store_rows(g.C, g.c_dt, g.ldc, m, ok, nb, half, g.N, g.vec, z);
+      store_rows(g.C, g.c_dt, g.ldc, m, ok, nb, half, g.N, z);
     });
   });
   if (e.keep[0] && e.keep_dt == 4) {
@@ -436,7 +436,7 @@ __device__ __forceinline__ void gated_epilogue(const ProductArgs& g, floatx16 (&
     for_each<FM * FN>([&](auto K) __attribute__((always_inline)) {
       constexpr int I = K.value / FN, J = K.value % FN;
       const int m = m0 + 32 * I + l32;
-      store_block(part + m * (int64_t)(2 * P) + J / HF * P, m < g.M, n0 + 32 * (J % HF), half, g.N, 1, acc[I][J]);
+      store_block(part + m * (int64_t)(2 * P) + J / HF * P, m < g.M, n0 + 32 * (J % HF), half, g.N, acc[I][J]);
     });
     return;
   }
@@ -462,8 +462,8 @@ __device__ __forceinline__ void gated_epilogue(const ProductArgs& g, floatx16 (&
       for (int v = 0; v < 16; ++v)
         if (nb + 8 * (v >> 2) + 4 * half + (v & 3) >= g.N) h[v] = 0.f;
     }
-    if (g.c_dt == 0) store_block<true>(reinterpret_cast<float*>(g.C) + m * g.ldc, ok, nb, half, 0, 1, h);
-    else store_block<true>(reinterpret_cast<uint16_t*>(g.C) + m * g.ldc, ok, nb, half, 0, 1, h);
+    if (g.c_dt == 0) store_block<true>(reinterpret_cast<float*>(g.C) + m * g.ldc, ok, nb, half, 0, h);
+    else store_block<true>(reinterpret_cast<uint16_t*>(g.C) + m * g.ldc, ok, nb, half, 0, h);
   });
   if (e.keep[0] && e.keep_dt == 4) {
 #pragma unroll
@@ -480,7 +480,7 @@ __device__ __forceinline__ void gated_grad_epilogue(const ProductArgs& g, floatx
   const int wide = (int)(g.ldc / 2);
   const bool f8 = e.keep_dt == 4;
   // what was kept of the next block is loaded before this one is computed
-  const bool early = ES == 2 && !f8 && e.keep_vec && n0 + 32 * FN <= g.N;
+  const bool early = ES == 2 && !f8 && n0 + 32 * FN <= g.N;
   uint32_t scales[FM][2];
   if (f8) {
 #pragma unroll
@@ -524,8 +524,8 @@ __device__ __forceinline__ void gated_grad_epilogue(const ProductArgs& g, floatx
         gate = gate16.values(q);
         up = up16.values(q);
       } else {
-        gate = load_half(reinterpret_cast<const T*>(e.keep[0]) + m * e.ld_keep, ok, n, half, g.N, e.keep_vec);
-        up = load_half(reinterpret_cast<const T*>(e.keep[1]) + m * e.ld_keep, ok, n, half, g.N, e.keep_vec);
+        gate = load_half(reinterpret_cast<const T*>(e.keep[0]) + m * e.ld_keep, ok, n, half, g.N);
+        up = load_half(reinterpret_cast<const T*>(e.keep[1]) + m * e.ld_keep, ok, n, half, g.N);
       }
       // gate becomes dg, up du
       with_activation(e.act, [&](auto act) __attribute__((always_inline)) {

@@ -182,7 +182,7 @@ static __global__ __launch_bounds__(256) void ffn_finish_kernel(FinishArgs g) {
       for (int c = 0; c < 4; ++c) z[p][c] = 0.f;
       const float* from = g.part + m * row + p * P + n;
       if (n < g.N) {
-#pragma unroll 4
+#pragma unroll 8
         for (int s = 0; s < g.splits; ++s) {
           const floatx4 v = *reinterpret_cast<const floatx4*>(from + s * g.range_stride);
 #pragma unroll

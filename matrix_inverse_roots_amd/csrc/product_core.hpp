@@ -581,7 +581,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_kernel(ProductArgs g)
               floatx4 v = floatx4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
               if (m >= g.M || n >= g.N) continue;
               if (g.vec && n + 4 <= g.N) {
-                floatx4* P = reinterpret_cast<floatx4*>(C + n);
+                floatx4_any* P = reinterpret_cast<floatx4_any*>(C + n);
                 if (g.beta != 0.f) v += g.beta * *P;
                 *P = v;
               } else {
@@ -611,14 +611,14 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_kernel(ProductArgs g)
               };
               if (g.vec && n + 8 <= g.N) {
                 if (g.beta != 0.f) {
-                  const u32x4 old = *reinterpret_cast<const u32x4*>(C);
+                  const u32x4 old = *reinterpret_cast<const u32x4_any*>(C);
 #pragma unroll
                   for (int e = 0; e < 8; ++e) x[e] += g.beta * widen((uint16_t)(old[e >> 1] >> (16 * (e & 1))));
                 }
                 u32x4 o;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) o[e] = g.c_dt == 2 ? pack_bf16(x[2 * e], x[2 * e + 1]) : pack_f16(x[2 * e], x[2 * e + 1]);
-                *reinterpret_cast<u32x4*>(C) = o;
+                *reinterpret_cast<u32x4_any*>(C) = o;
               } else {
 #pragma unroll
                 for (int e = 0; e < 8; ++e)

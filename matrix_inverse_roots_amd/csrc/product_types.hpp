@@ -15,6 +15,11 @@ typedef short shortx4_t __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef float floatx2 __attribute__((ext_vector_type(2)));
 
+// 16 and 8 bytes at an element's address: one access wherever it lies.
+typedef u32x4 u32x4_any __attribute__((aligned(2)));
+typedef u32x2 u32x2_any __attribute__((aligned(2)));
+typedef floatx4 floatx4_any __attribute__((aligned(4)));
+
 enum class Elem { BF16, F32, F8, F8W };
 // What becomes of a tile.  STORE: C = alpha acc + beta C.  STORE2: the same, B's
 // rows of k continued in a second matrix.  SOFTMAX: the projection's loss.
@@ -34,7 +39,7 @@ struct FfnArgs {
   float* part;            // GATED with ranges of k: partial results [range][M][2 P], P: N rounded up to 4
   void* du;               // GATED_GRAD: rows of ldc (C receives dg)
   void* h;                // GATED_GRAD: rows of ldc / 2
-  int bias_bf16, bias_vec, act, keep_dt, keep_vec, scale_vec, residual_vec;  // keep_dt: 0 float32, 2 bfloat16, 4 e4m3; scale_vec: rows of scales start on 4 bytes
+  int bias_bf16, act, keep_dt, scale_vec;  // keep_dt: 0 float32, 2 bfloat16, 4 e4m3; scale_vec: rows of scales start on 4 bytes
 };
 
 struct ProductArgs {
@@ -53,7 +58,7 @@ struct ProductArgs {
   int nst;                            // k-stages of 128 bytes
   int splits, split_stages;           // ranges of k; stages of each but the last (F8: a multiple of 4)
   int c_dt;                           // 0 float32, 1 half, 2 bfloat16
-  int vec;                            // rows of C allow 16-byte stores
+  int vec;                            // whole runs of C in 16-byte accesses
   float alpha, beta;                  // STORE: C = alpha acc + beta C
   const float* alpha_dev;             // times this, or null
   int64_t items;                      // batch * splits * mt * nt
