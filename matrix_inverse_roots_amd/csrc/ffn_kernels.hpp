@@ -77,9 +77,12 @@ template <typename T, bool ROUND> __device__ __forceinline__ void load8(const T*
 // of a wave's share of k in flight.  kw waves of a workgroup share a column's
 // k, 512 elements each at a time, and meet in LDS, so that short and long sums
 // both fill the chip.  Products and sums are float32.
-// One row, 4096 x 1024 bfloat16 (8.4 MB): 4.0 us; both projections (16.8 MB) 6.6 us
-// = 2.5 TB/s, 1024 x 4096 5.0 us: bound by the latency of the loads and of the
-// launch.  The 128-tiles take 16 us and more.
+// One row, 4096 x 1024 bfloat16 (8.4 MB): 3.7-4.0 us; both projections (16.8 MB)
+// 6.6 us = 2.5 TB/s, 1024 x 4096 5.0 us: bound by the latency of the loads and of
+// the launch.  Against the 128-tiles with their ranges of k: 4096 x 1024, one row
+// 3.7 and 10.2 us, four 5.1 and 10.2; 1024 x 4096, four rows 6.3 and 10.4; 8192 x
+// 8192, four rows 40 and 39: from there on the widening of more rows costs more
+// than a second launch, so four rows are the most.
 // MB: rows, at most.  TX, TW: float, or uint16_t for bfloat16.  ROUND: a
 // float32 weight enters as bfloat16.
 template <typename TX, typename TW, bool ROUND, int MB, bool GATED>
