@@ -588,8 +588,10 @@ shampoo_status shampoo_linear_xent(const shampoo_xent_args* args, hipStream_t st
  * stored.  Weights are in dt, or F32 beside BF16 (rounded to bfloat16 for the
  * products).  Between two products h, dz, dg and du are rounded to dt (h of at
  * most 4 rows stays float32).  Formulas are followed where values are not
- * finite: silu and gelu of minus infinity are NaN, and a row of x with a NaN
- * reaches the weights' gradients even where its row of dy is zero.
+ * finite: silu and gelu of minus infinity are NaN, their derivatives NaN at
+ * both infinities; relu' is 1 where z > 0 and 0 elsewhere, NaN among it; and a
+ * row of x with a NaN reaches the weights' gradients even where its row of dy
+ * is zero.
  *
  * Kept.  What a forward call keeps for the backward one, z or g and u, is
  * written by the products' epilogues and is one of
@@ -599,8 +601,8 @@ shampoo_status shampoo_linear_xent(const shampoo_xent_args* args, hipStream_t st
  *         a row, [rows, that / 32]: 2^e is the least power of two that keeps
  *         the block's largest finite magnitude within 448 (e = 0 for zeros, e >=
  *         -127), and a value is rounded once, from float32, to nearest even
- *         (NaN and infinities: NaN).  Half of bfloat16's bytes, a quarter of
- *         float32's.
+ *         (NaN and infinities: NaN, so that relu' is 0 at an infinity kept
+ *         here).  Half of bfloat16's bytes, a quarter of float32's.
  * A gradient is that of the formulas at the kept values; y is computed from
  * the unrounded ones.  x of a weight's gradient may be in 8 bits too: E4M3 as
  * shampoo_quantize_f8 gives it with block_rows 1 (x_scale), widened exactly in

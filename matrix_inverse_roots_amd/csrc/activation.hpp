@@ -12,6 +12,10 @@
 // all x >= 0: 3.2e-8 relative in exact arithmetic, 3.6e-7 at most as it is
 // evaluated here.  Small probabilities keep their digits, which 1 + erf would
 // lose, and the exponential serves the derivative too.
+//
+// Values that are not finite follow the formulas: relu's derivative is [z > 0],
+// so 0 at NaN; the others' are NaN at NaN and, as infinity times zero, at
+// both infinities.  Finite values reach the limits 0 and 1 without overflow.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -30,7 +34,7 @@ struct ActNone {
 struct ActRelu {
   __device__ __forceinline__ float value(float z) const { return z < 0.f ? 0.f : z; }  // a NaN stays one
   __device__ __forceinline__ float both(float z, float& slope) const {
-    slope = z <= 0.f ? 0.f : 1.f;
+    slope = z > 0.f ? 1.f : 0.f;  // 0 at NaN
     return value(z);
   }
 };
@@ -76,9 +80,14 @@ template <bool CUBIC> struct ActSigmoid {
   __device__ __forceinline__ float value(float z) const { return z * sigma(z); }
   __device__ __forceinline__ float both(float z, float& slope) const {
     const float s = sigma(z);
-    // behind 10^4 sigma is 0 or 1, and z p'(z) would overflow
-    const float w = fminf(fmaxf(z, -1e4f), 1e4f);
-    slope = __builtin_fmaf(s * (1.f - s), CUBIC ? w * __builtin_fmaf(3.f * C3, w * w, C1) : w, s);
+    if constexpr (CUBIC) {
+      // behind 10^4 sigma is 0 or 1, and z p'(z) would overflow; NaN at an
+      // infinity, which the bound takes away, comes back through z 0
+      const float w = fminf(fmaxf(z, -1e4f), 1e4f), one = __builtin_fmaf(z, 0.f, 1.f);
+      slope = __builtin_fmaf(s * (one - s), w * __builtin_fmaf(3.f * C3, w * w, C1), s);
+    } else {
+      slope = __builtin_fmaf(s * (1.f - s), z, s);
+    }
     return z * s;
   }
 };
