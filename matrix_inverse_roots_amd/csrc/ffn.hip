@@ -112,60 +112,6 @@ hipError_t place(const Operand& o, const void*& p, const void* scale, int64_t ro
   return hipGetLastError();
 }
 
-// Tile and ranges of k of a layer's product: the least of the tiles' costs.
-//
-// Costs in the time of one 256 x 256 tile (bfloat16) where the chip is full and
-// power holds its clock: 256 x 256 1, 256 x 128 0.54, two 128 x 128 on a unit 0.60
-// (8192 x 10240 x 4096: 533, 585 and 644 us; 4096^3: 115, 122 and 138), one alone
-// 0.33.  Where it is not, the clock rises and a tile is faster: 0.63, 0.40, 0.45,
-// so that a last round which few units take costs less than a full one (4096 x
-// 10240 x 8192, 2.5 rounds of large tiles, 5 of medium: 575 and 585 us; 8192 x
-// 1024 x 4096, half a round and one: 88 and 65).  The epilogue of a large tile
-// leaves the matrix cores waiting for longer: `epilogue` counts it in columns of
-// k (150 for bias, activation, residual or kept values, 300 for the gated block's
-// gradients; 8192 x 4096 x 1024 with gelu and kept values: 103 us large, 95
-// medium, 100 small; with k 4096 and 10240 columns 598, 665, 775).
-// float32 (matrix instructions, not loads, bound it): a 128 x 128 tile 0.26, a 64
-// x 64 one 0.073 (777 x 2731 x 1000, 154 tiles or 559: 76 and 60 us; 2048 x
-// 2048 x 1024, 256 or 1024: 72 and 79).
-Shape plan_layer(int64_t batch, int64_t M, int64_t N, int64_t K, int es, bool may_split, int epilogue, bool dual = false) {
-  if (M == 0 || K == 0) return Shape{};  // an empty batch, which launches none
-  Shape s = plan_shape(batch, M, N, K, es, may_split);
-  s.tile = s.large ? TILE_LARGE : TILE_128;
-  auto tiles = [&](int64_t m, int64_t n) { return batch * ((M + m - 1) / m) * ((N + n - 1) / n); };
-  if (es == 4) {
-    // a range of k costs some 6 us, for the launch that sums them, and its reading
-    auto ranges = [&](int64_t n, double tile, int r) {
-      return (double)((n * r + CUS - 1) / CUS) * tile / r + (r > 1 ? (30.0 + 1.2 * r) / K : 0.0);
-    };
-    double now = s.large ? (double)((tiles(256, 256) + CUS - 1) / CUS) : ranges(tiles(128, 128), 0.26, s.splits);
-    for (int r = 1; !dual && r <= (may_split ? 16 : 1) && (r == 1 || r <= s.nst / 4); ++r) {
-      const int stages = (s.nst + r - 1) / r;
-      if ((s.nst + stages - 1) / stages != r) continue;
-      const double c = ranges(tiles(64, 64), 0.073, r);
-      if (c >= now) continue;
-      now = c;
-      s.large = false;
-      s.tile = TILE_64;
-      s.splits = r;
-      s.split_stages = stages;
-    }
-    return s;
-  }
-  if (s.splits > 1) return s;
-  auto cost = [&](int64_t n, int64_t slots, double full, double alone) {
-    return std::max((double)n / slots * full, (double)((n + slots - 1) / slots) * alone);
-  };
-  const double e = 1.0 + (double)epilogue / K;
-  const int64_t small = tiles(128, 128);
-  const double large = cost(tiles(256, 256), CUS, 1.0, 0.63) * e;
-  const double medium = cost(tiles(256, 128), CUS, 0.54, 0.40);
-  const double least = small <= CUS ? 0.33 : cost(small, 2 * CUS, 0.60, 0.45);
-  s.large = large <= medium && large <= least;
-  s.tile = s.large ? TILE_LARGE : medium <= least ? TILE_MEDIUM : TILE_128;
-  return s;
-}
-
 int kept_code(int dt) { return dt == SHAMPOO_E4M3 ? 4 : out_code(dt); }
 // A call of few rows takes no matrix cores, unless it keeps blocks of 8 bits,
 // which reach over its workgroups.
@@ -255,7 +201,7 @@ shampoo_status linear_layout(const shampoo_linear_args* a, LinearLayout* L) {
   if (!L->few) {
     L->x = operand(c, a->x, a->M, a->K, a->ld_x, a->dt, a->dt);
     L->w = operand(c, a->w, a->N, a->K, a->ld_w, a->w_dt, a->dt);
-    L->shape = plan_layer(1, a->M, a->N, a->K, (int)size_of(a->dt), true, a->bias || a->residual || a->keep || a->activation ? 150 : 0);
+    L->shape = plan_linear(a->M, a->N, a->K, (int)size_of(a->dt), a->bias || a->residual || a->keep || a->activation);
     L->part = c.take(padded_bytes(L->shape, 1, a->M, a->N));
   }
   L->total = c.at;
@@ -300,8 +246,8 @@ shampoo_status linear_grad_layout(const shampoo_linear_grad_args* a, LinearGradL
   L->ld_dz = L->store ? up(a->N, 8) : a->ld_dy;
   L->x = operand(c, a->x, a->M, a->K, a->ld_x, a->x_dt, a->dt, a->dw);
   L->w = operand(c, a->w, a->N, a->K, a->ld_w, a->w_dt, a->dt, a->dx);
-  L->dx = plan_layer(1, a->M, a->K, a->N, es, true, 0);
-  L->dw = plan_layer(1, a->N, a->K, a->M, es, true, 0);
+  L->dx = plan_linear_dx(a->M, a->N, a->K, es);
+  L->dw = plan_linear_dw(a->M, a->N, a->K, es);
   L->dz = c.take(L->store ? (size_t)a->M * L->ld_dz * es : 0);
   L->sums = c.take(a->dbias ? (size_t)((a->M + GRAD_ROWS - 1) / GRAD_ROWS) * a->N * 4 : 0);
   size_t part = 0;
@@ -429,9 +375,9 @@ shampoo_status gated_layout(const shampoo_gated_ffn_args* a, GatedLayout* L) {
   L->x = operand(c, a->x, a->T, a->d, a->ld_x, a->dt, a->dt);
   gated_operands(c, L->gate, L->up_, a->w_gate, a->w_up, a->f, a->d, a->ld_gate, a->ld_up, a->w_dt, a->dt);
   L->down = operand(c, a->w_down, a->d, a->f, a->ld_down, a->w_dt, a->dt);
-  L->ldh = up(a->f, 64);
-  L->in = plan_layer(1, a->T, 2 * a->f, a->d, es, true, 0, true);
-  L->out = plan_layer(1, a->T, a->d, a->f, es, true, a->residual ? 150 : 0);
+  L->ldh = gated_width(a->f);
+  L->in = plan_gated_in(a->T, a->d, a->f, es);
+  L->out = plan_gated_out(a->T, a->d, a->f, es, a->residual);
   L->h = c.take((size_t)a->T * L->ldh * es);
   L->part = c.take(std::max(partial_bytes(L->in, 1, a->T, 2 * up(a->f, 4)), padded_bytes(L->out, 1, a->T, a->d)));
   L->total = c.at;
@@ -535,12 +481,12 @@ shampoo_status gated_grad_layout(const shampoo_gated_ffn_grad_args* a, GatedGrad
   L->x = operand(c, a->x, a->T, a->d, a->ld_x, a->x_dt, a->dt, a->dw_gate || a->dw_up);
   gated_operands(c, L->gate, L->up_, a->w_gate, a->w_up, a->f, a->d, a->ld_gate, a->ld_up, a->w_dt, a->dt, a->dx);
   L->down = operand(c, a->w_down, a->d, a->f, a->ld_down, a->w_dt, a->dt);
-  L->fp = up(a->f, 64);
+  L->fp = gated_width(a->f);
   L->pair = a->dw_gate && a->dw_up && a->ld_dw_gate == a->ld_dw_up;
-  L->dh = plan_layer(1, a->T, L->fp, a->d, es, false, 300);
-  L->dx = plan_layer(1, a->T, a->d, 2 * L->fp, es, true, 0);
-  L->dwd = plan_layer(1, a->d, a->f, a->T, es, true, 0);
-  L->dwp = plan_layer(L->pair ? 2 : 1, a->f, a->d, a->T, es, true, 0);
+  L->dh = plan_gated_dh(a->T, a->d, a->f, es);
+  L->dx = plan_gated_dx(a->T, a->d, a->f, es);
+  L->dwd = plan_gated_dw_down(a->T, a->d, a->f, es);
+  L->dwp = plan_gated_dw(a->T, a->d, a->f, es, L->pair);
   L->D = c.take((size_t)a->T * 2 * L->fp * es);
   L->h = c.take((size_t)a->T * L->fp * es);
   size_t part = 0;

@@ -11,11 +11,11 @@
 #include "host_common.hpp"
 #include "product_core.hpp"
 #include "product_passes.hpp"
+#include "product_shapes.hpp"
 #include "shampoo.h"
 
 namespace shampoo {
 
-inline int64_t up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 inline bool aligned(const void* p, size_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 inline size_t size_of(int dt) { return dt == SHAMPOO_F32 ? 4 : dt == SHAMPOO_E4M3 || dt == SHAMPOO_E5M2 ? 1 : 2; }
 
@@ -53,46 +53,6 @@ template <size_t COUNT> shampoo_status check_apart(const Span (&spans)[COUNT], s
 // ---------------------------------------------------------------------------
 // products
 // ---------------------------------------------------------------------------
-// Tile of a product and its split of k.  LARGE: 256 x 256, one workgroup of
-// 8 waves per CU; SMALL: 128 x 128, two workgroups of 4 waves.
-struct Shape {
-  bool large;
-  int splits, split_stages, nst;
-  int tile = 0;  // Tile, where plan_layer chose
-};
-
-constexpr int CUS = 256;  // planning only; the grid follows the device
-
-inline Shape plan_shape(int64_t batch, int64_t M, int64_t N, int64_t K, int es, bool may_split) {
-  Shape s;
-  s.nst = (int)((K * es + 127) / 128);
-  const int64_t tl = batch * ((M + 255) / 256) * ((N + 255) / 256);
-  const int64_t ts = batch * ((M + 127) / 128) * ((N + 127) / 128);
-  // Tiles of the busiest compute unit, in large tiles' time.  A small tile is
-  // a quarter of the work, at 84% of the rate of a large one (8-bit 4096^3,
-  // 4 small per unit against 1 large: 80 and 71 us; bfloat16 8192 x 65536 x
-  // 1024: 1190 and 980 us), or 95% in float32, whose matrix instructions
-  // outlast the loads (2048 x 16384 x 1024: 543 and 522 us).  So small tiles
-  // win where they divide among the units better (8-bit 6144^2 x 2048, 9 small
-  // against 3 large: 95 and 102 us; float32 10007 x 1024 x 999: 617 and 727 us
-  // for the loss with both gradients).
-  const double large_cost = (double)((tl + CUS - 1) / CUS);
-  const double small_cost = (double)((ts + CUS - 1) / CUS) * 0.25 / (es == 4 ? 0.95 : 0.84);
-  s.large = large_cost <= small_cost;
-  s.splits = 1;
-  s.split_stages = s.nst;
-  const int64_t items = s.large ? tl : ts, slots = CUS;
-  if (may_split && items * 2 <= slots) {
-    // at least 4 stages a range
-    const int64_t want = std::min<int64_t>(slots / items, s.nst / 4);
-    if (want >= 2) {
-      s.split_stages = (int)up((s.nst + want - 1) / want, 4);
-      s.splits = (s.nst + s.split_stages - 1) / s.split_stages;
-    }
-  }
-  return s;
-}
-
 template <Elem E, int FM, int FN, int WM, int WN, int NB, int PER_CU, bool AS, bool BS, Epi EPI, int FA, int FB>
 hipError_t launch_tiles(ProductArgs g, int64_t batch, hipStream_t st) {
   constexpr int TM = 32 * FM * WM, TN = 32 * FN * WN;
@@ -119,25 +79,30 @@ hipError_t launch_tiles(ProductArgs g, int64_t batch, hipStream_t st) {
 template <Elem E, bool AS, bool BS, Epi EPI, int FA = 0, int FB = 0>
 hipError_t launch_product(const ProductArgs& g, bool large, int64_t batch, hipStream_t st) {
   if (large) return launch_tiles<E, 2, 4, 4, 2, 2, 1, AS, BS, EPI, FA, FB>(g, batch, st);
-  const int64_t items = batch * g.splits * ((g.M + 127) / 128) * (EPI == Epi::GATED ? (g.N + 63) / 64 : (g.N + 127) / 128);
+  const int64_t items = batch * g.splits * ((g.M + 127) / 128) * ((g.N + 127) / 128);
   if (items <= CUS) return launch_tiles<E, 1, 4, 4, 1, 4, 1, AS, BS, EPI, FA, FB>(g, batch, st);
   return launch_tiles<E, 1, 4, 4, 1, 2, 2, AS, BS, EPI, FA, FB>(g, batch, st);
 }
 
-// Tiles of the feed-forward layers' products: 64 x 64 (float32 only), 128 x 128,
-// 256 x 128 (bfloat16 only; three buffers, since its stages are half as long as a large
-// tile's and loads take as long), 256 x 256.
-enum Tile { TILE_64 = 1, TILE_128, TILE_MEDIUM, TILE_LARGE };
-
+// A feed-forward layer's product on the tile that its plan chose.  Only the
+// tiles that some plan reaches are built: float32 has no 256 x 128, GATED none of
+// 64 x 64 (it needs two fragments of columns), and a forward product over ranges of
+// k (STORE without strided operands), which has few tiles, no large ones.
 template <Elem E, bool AS, bool BS, Epi EPI>
 hipError_t launch_layer(const ProductArgs& g, const Shape& s, int64_t batch, hipStream_t st) {
-  if constexpr (E == Elem::F32 && EPI != Epi::GATED) {  // GATED needs two fragments of columns
+  constexpr bool RANGES_ONLY = EPI == Epi::STORE && !AS && !BS;
+  if constexpr (E == Elem::F32 && EPI != Epi::GATED) {
     if (s.tile == TILE_64) return launch_tiles<E, 1, 1, 2, 2, 3, 3, AS, BS, EPI, 0, 0>(g, batch, st);
   }
-  if constexpr (E == Elem::BF16) {
-    if (s.tile == TILE_MEDIUM) return launch_tiles<E, 2, 2, 4, 2, 3, 1, AS, BS, EPI, 0, 0>(g, batch, st);
+  if constexpr (!RANGES_ONLY) {
+    if constexpr (E == Elem::BF16) {
+      if (s.tile == TILE_MEDIUM) return launch_tiles<E, 2, 2, 4, 2, 3, 1, AS, BS, EPI, 0, 0>(g, batch, st);
+    }
+    if (s.tile == TILE_LARGE) return launch_tiles<E, 2, 4, 4, 2, 2, 1, AS, BS, EPI, 0, 0>(g, batch, st);
+    if (s.tile == TILE_128_TWO) return launch_tiles<E, 1, 4, 4, 1, 2, 2, AS, BS, EPI, 0, 0>(g, batch, st);
   }
-  return launch_product<E, AS, BS, EPI>(g, s.tile == TILE_LARGE, batch, st);
+  if (s.tile == TILE_128) return launch_tiles<E, 1, 4, 4, 1, 4, 1, AS, BS, EPI, 0, 0>(g, batch, st);
+  return hipErrorInvalidValue;
 }
 
 inline void set_shape(ProductArgs& g, const Shape& s) {
