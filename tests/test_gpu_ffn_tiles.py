@@ -139,3 +139,50 @@ def test_block(mir, dt, size, keep):
     one = torch.empty((f, d), dtype=dt, device="cuda")   # a projection's gradient alone
     mir.shampoo_gated_ffn_grad(dy, x8, None, None, wd, kept, dw_up=one, activation="relu")
     same(one, du.t() @ x.double(), "dw_up alone")
+
+
+def test_rows_past_32_bits(mir):
+    """Rows of which the last lie more than 2^31 elements from the first: all
+    of what the calls write, sums over the rows and over the long inner size among it."""
+    import torch
+    dt, M, K, N, step = torch.bfloat16, 66001, 17, 33024, 6000
+    gen = gen_of(43)
+    x, w, wd = whole(gen, M, K, 2, dt), whole(gen, N, K, 2, dt), whole(gen, K, N, 1, dt)
+    pair = [mir.shampoo_kept_empty(M, N, "e4m3", "cuda") for _ in range(2)]
+    y = mir.shampoo_linear(x, w, activation="relu", keep=pair[0])
+    for r in range(0, M, step):
+        z = x[r:r + step].double() @ w.double().t()
+        same(y[r:r + step], z.clamp(min=0), "y")
+        same(tuple(t[r:r + step] for t in pair[0]), z, "kept")
+    out = dict(dx=torch.empty_like(x), dw=torch.empty((N, K), device="cuda"), dbias=torch.empty(N, device="cuda"))
+    mir.shampoo_linear_grad(y, x, w, kept=pair[0], activation="relu", **out)
+    dw, db = torch.zeros((N, K), dtype=torch.float64, device="cuda"), torch.zeros(N, dtype=torch.float64, device="cuda")
+    for r in range(0, M, step):
+        dz = y[r:r + step].double() * (ref.widen(tuple(t[r:r + step] for t in pair[0]), N) > 0)
+        same(out["dx"][r:r + step], exact(dz @ w.double(), dz @ w.double().abs()), "dx")
+        dw += dz.t() @ x[r:r + step].double()
+        db += dz.sum(dim=0)
+    same(out["dbias"], exact(db, db), "dbias")
+    same(out["dw"], exact(dw, 2 * db), "dw")
+    del out, y, dz, z
+
+    out = mir.shampoo_gated_ffn(x, w, w, wd, activation="relu", keep=pair)
+    dx, dwd = torch.empty_like(x), torch.empty((K, N), dtype=dt, device="cuda")
+    dy = x.clamp(-1, 1)
+    mir.shampoo_gated_ffn_grad(dy, x, w, w, wd, pair, dx, dw_down=dwd, activation="relu")
+    want, size = (torch.zeros((K, N), dtype=torch.float64, device="cuda") for _ in range(2))
+    for r in range(0, M, step):
+        z = x[r:r + step].double() @ w.double().t()
+        h = (z.clamp(min=0) * z).to(dt).double()
+        same(out[r:r + step], exact(h @ wd.double().t(), h @ wd.double().abs().t()), "gated y")
+        for t in pair:
+            same(tuple(v[r:r + step] for v in t), z, "gated kept")
+        z = ref.widen(tuple(t[r:r + step] for t in pair[0]), N)
+        d = dy[r:r + step].double()
+        dh = d @ wd.double()
+        dg, h = (dh * z.clamp(min=0)).to(dt).double(), (z.clamp(min=0) * z).to(dt).double()   # dg is du: the projections are equal
+        same(dx[r:r + step], exact(2 * dg @ w.double(), 2 * dg.abs() @ w.double().abs()), "gated dx")
+        want += d.t() @ h
+        size += d.abs().t() @ h
+    same(dwd, exact(want, size), "gated dw_down")
+    torch.cuda.empty_cache()
