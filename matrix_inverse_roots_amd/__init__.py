@@ -252,6 +252,13 @@ def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
+def _ws_bytes(ws):
+    """Bytes of a workspace tensor: those from its address on, so that it must lie in one piece."""
+    if not ws.is_contiguous():
+        raise ValueError("the workspace must be contiguous")
+    return ws.numel() * ws.element_size()
+
+
 def _stream(stream):
     torch = _torch()
     s = stream if stream is not None else torch.cuda.current_stream()
@@ -381,7 +388,7 @@ def shampoo_inverse_root(inp, out, p, opts, valid=None, scale_out=None, flags=No
         ws = torch.empty(max(nb, 1), dtype=torch.uint8, device=inp.device)
     oc = opts.c()
     _check(lib.shampoo_inverse_root(_ptr(inp), _ptr(out), _dtype_code(inp), n, B, int(p), ctypes.byref(oc),
-                                    _ptr(valid), _ptr(scale_out), _ptr(flags), _ptr(ws), ws.numel(),
+                                    _ptr(valid), _ptr(scale_out), _ptr(flags), _ptr(ws), _ws_bytes(ws),
                                     _stream(stream)))
     return out
 
@@ -411,7 +418,7 @@ def shampoo_precondition(roots, gstack, dstack, ws=None, stream=None):
         _check(lib.shampoo_precondition_workspace(nblk, B, _dtype_code(roots), ctypes.byref(b)))
         ws = torch.empty(max(b.value, 1), dtype=torch.uint8, device=gstack.device)
     _check(lib.shampoo_precondition(_ptr(roots), _dtype_code(roots), _ptr(gstack), _dtype_code(gstack), nblk, B,
-                                    _ptr(dstack), _ptr(ws), ws.numel(), _stream(stream)))
+                                    _ptr(dstack), _ptr(ws), _ws_bytes(ws), _stream(stream)))
 
 
 def shampoo_step_workspace(args):
@@ -637,7 +644,7 @@ def shampoo_matmul_f8(a, a_scale, b, b_scale, c, ws=None, stream=None):
         need = shampoo_matmul_f8_workspace(n, M, N, K)
         ws = _empty(need, torch.uint8, dev, stream) if need else None
     if ws is not None:
-        room = ws.numel() * ws.element_size()
+        room = _ws_bytes(ws)
     _launch(lib.shampoo_matmul_f8, dev, stream, a.data_ptr(), _f8_code(a), a_scale.data_ptr(), arb, b.data_ptr(),
             _f8_code(b), b_scale.data_ptr(), brb, n, M, N, K, c.data_ptr(), cdt,
             None if ws is None else ws.data_ptr(), room)
@@ -739,7 +746,7 @@ def shampoo_linear_xent(hidden, weight, targets, loss=None, lse=None, dhidden=No
         b = ctypes.c_size_t(0)
         _check(lib.shampoo_linear_xent_workspace(ctypes.byref(args), ctypes.byref(b)))
         ws = _empty(max(b.value, 1), torch.uint8, dev, stream)
-    args.ws, args.ws_bytes = ws.data_ptr(), ws.numel() * ws.element_size()
+    args.ws, args.ws_bytes = ws.data_ptr(), _ws_bytes(ws)
     _launch(lib.shampoo_linear_xent, dev, stream, ctypes.byref(args))
     return loss
 
@@ -864,7 +871,7 @@ def _with_workspace(name, args, ws, dev, stream, none=False):
         if need.value:
             ws = _empty(need.value, _torch().uint8, dev, stream)
     if ws is not None:
-        args.ws, args.ws_bytes = ws.data_ptr(), ws.numel() * ws.element_size()
+        args.ws, args.ws_bytes = ws.data_ptr(), _ws_bytes(ws)
     _launch(getattr(lib, name), dev, stream, ctypes.byref(args))
 
 
