@@ -69,17 +69,23 @@ inline Shape plan_shape(int64_t batch, int64_t M, int64_t N, int64_t K, int es, 
 // gradients; 8192 x 4096 x 1024 with gelu and kept values: 103 us large, 95
 // medium, 100 small; with k 4096 and 10240 columns 598, 665, 775).
 // float32 (matrix instructions, not loads, bound it): a 128 x 128 tile 0.26, a 64
-// x 64 one 0.073 (777 x 2731 x 1000, 154 tiles or 559: 76 and 60 us; 2048 x
-// 2048 x 1024, 256 or 1024: 72 and 79).
+// x 64 one 0.073 (777 x 2731 x 1000, 154 tiles or 559: 73 and 57 us; 1000 x 1000 x
+// 1000, 64 or 256: 69 and 26; 2048 x 2048 x 1024, 256 or 1024: 72-78 and 75-79).
 inline Shape plan_layer(int64_t batch, int64_t M, int64_t N, int64_t K, int es, bool may_split, int epilogue, bool dual = false) {
   if (M == 0 || K == 0) return Shape{};  // an empty batch, which launches none
   Shape s = plan_shape(batch, M, N, K, es, may_split);
   s.tile = s.large ? TILE_LARGE : TILE_128;
   auto tiles = [&](int64_t m, int64_t n) { return batch * ((M + m - 1) / m) * ((N + n - 1) / n); };
   if (es == 4) {
-    // a range of k costs some 6 us, for the launch that sums them, and its reading
+    // Ranges of k cost a launch that sums them, some 5 us, 0.3 us a range and 8 bytes
+    // of traffic for each of its values, at 6.5 TB/s; a large tile takes 0.245 us for
+    // each k, so in its time 20 / K, 1.2 / K and 5e-6 / K.  With all of the epilogue,
+    // whole and in 2, 3, 5 ranges: 777 x 2731 x 1000 58, 59, 60, 64 us; 2048 x 2048 x
+    // 1024 77, 93, 99, 110; 1100 x 1300 x 3000 104, 88, 99, 97; 497 x 434 x 3980 79, 45, 34,
+    // 37 and, in 9, 28.  8 x 64 x 8000 in 16 ranges of 64-tiles 15.5 us, in 62 of one
+    // 128-tile 20.
     auto ranges = [&](int64_t n, double tile, int r) {
-      return (double)((n * r + CUS - 1) / CUS) * tile / r + (r > 1 ? (30.0 + 1.2 * r) / K : 0.0);
+      return (double)((n * r + CUS - 1) / CUS) * tile / r + (r > 1 ? (20.0 + (1.2 + 5e-6 * batch * M * N) * r) / K : 0.0);
     };
     double now = s.large ? (double)((tiles(256, 256) + CUS - 1) / CUS) : ranges(tiles(128, 128), 0.26, s.splits);
     for (int r = 1; !dual && r <= (may_split ? 16 : 1) && (r == 1 || r <= s.nst / 4); ++r) {
